@@ -1,6 +1,6 @@
 /*
  * moe.h - C ABI of libmoe: the forward pass of one Mixture-of-Experts layer on
- * one AMD Instinct MI355X (gfx950).
+ * one AMD Instinct MI355X (gfx950), and the operators that train it.
  *
  * The layer, as the page "MOE推理流程解析" (ffner.com) describes it:
  *   section 三: the router scores every expert and top-k keeps the chosen
@@ -327,6 +327,120 @@ moe_status moe_ep_exchange(int G, const void *in, long long in_rank_stride, cons
  * E = E/G). */
 moe_status moe_ep_local_experts(const moe_ep_record *recv_meta, int n, int E, int G, int rank, int32_t *local_idx,
                                 hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Training the layer. The calls below are the backward side of the forward
+ * above: the router's balance loss and counts, the gradient at its logits,
+ * and the expert FFN with its backward pass, which keeps the activations it
+ * needs in 8 bits. One step:
+ *   moe_route -> moe_balance_loss -> moe_permute -> moe_ffn_train_forward ->
+ *   moe_combine -> ... dY ... -> moe_ffn_train_backward (dX, dtopk_w, dW) ->
+ *   moe_route_backward (dlogits; the gate's own products are plain GEMMs).
+ * (Page "MOE推理流程解析" §九 names load balance and dropped tokens as what
+ * training adds to routing.)
+ * ------------------------------------------------------------------------- */
+
+/* Balance loss, z loss and per-expert counts of a batch of B token sequences.
+ * With p = softmax(logits[t]), lse = log sum_e exp(logits[t, e]), n_b the
+ * tokens of sequence b, B' the sequences with n_b > 0 and N = sum_b n_b:
+ *   seq_counts[b,e] = #{(t in b, j): topk_idx[t,j] = e}        [B, E]
+ *   counts[e]       = sum_b seq_counts[b,e]                     [E]
+ *   f_b[e]          = E / (k n_b) * seq_counts[b,e]
+ *   loss[0] = alpha / B' * sum_b sum_e f_b[e] * (1/n_b) sum_{t in b} p[t,e]
+ *   loss[1] = beta / N * sum_t lse[t]^2                          loss [2]
+ * (loss[0] is alpha when every expert is picked and expected equally often.)
+ * Sequence b is tokens seq_offsets[b] .. seq_offsets[b+1] - 1 (device
+ * [B+1], ascending, in [0, T]); sequences may be empty, and tokens outside
+ * every sequence (padding) count nowhere. seq_offsets NULL: one sequence of T
+ * tokens (B must be 1). Picks outside [0, E) are counted nowhere. Logits may
+ * be -inf (an expert masked out: p = 0); a row of only -inf has p = 0 and
+ * lse = 0. A NaN or +inf logit makes the losses NaN. T == 0 writes zeros.
+ * fp32; sums in a fixed order, identical run to run.
+ * E <= 1024, k <= 64, B <= 65535. Workspace: moe_balance_loss_workspace_bytes
+ * bytes (device, any contents). */
+size_t moe_balance_loss_workspace_bytes(int T, int E, int B);
+moe_status moe_balance_loss(const float *logits, const int32_t *topk_idx, int T, int E, int k,
+                            const int32_t *seq_offsets, int B, float alpha, float beta, float *loss, int32_t *counts,
+                            int32_t *seq_counts, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* Gradient at the router's logits, dlogits [T, E] (every element written):
+ *   dlogits[t,e] = dloss[0] alpha / (B' n_b) p[t,e] (f_b[e] - sum_e' p[t,e'] f_b[e'])
+ *                + dloss[1] 2 beta / N lse[t] p[t,e]
+ *                + sum_{j: topk_idx[t,j] = e} w_j (dw_j - sum_j' w_j' dw_j')
+ * where w = topk_w[t,:] and dw = dtopk_w[t,:] (the last line is the gradient
+ * through moe_route's renormalised weights; counts have none). seq_counts as
+ * moe_balance_loss wrote them for the same tokens, offsets and picks; NULL
+ * leaves the first two terms out. dtopk_w NULL leaves the third out (topk_w
+ * and topk_idx are then not read); one of the two must be given. dloss
+ * [2] (device): the gradients of the two losses, NULL for 1 and 1. Tokens
+ * outside every sequence get the third term only. Picks outside [0, E) get
+ * no gradient. T == 0 returns MOE_OK. */
+moe_status moe_route_backward(const float *logits, const int32_t *topk_idx, const float *topk_w, const float *dtopk_w,
+                              int T, int E, int k, const int32_t *seq_offsets, int B, const int32_t *seq_counts,
+                              float alpha, float beta, const float *dloss, float *dlogits, hipStream_t stream);
+
+/* Activation checkpoints in 8 bits (MXFP8). For each row and 32 consecutive
+ * columns: e = the smallest integer in [-126, 127] with amax <= 448 * 2^e
+ * over the group's finite |x| (e = 0 when amax = 0),
+ *   S[r, c] = e + 127 (E8M0 byte),  Q[r, j] = E4M3(x[j] * 2^-e), round to
+ *   nearest, ties to even (nothing saturates; NaN and infinities give NaN).
+ * Unpacking gives decode(Q) * 2^(S - 127), exact in bf16 and fp32 (values
+ * below 2^-126 may be flushed to zero). X [R, ldx] F32 or BF16, its first C
+ * columns; C a multiple of 32; ldx >= C, ldx * element size a multiple of 16;
+ * Q [R, C], S [R, C/32]; Y [R, C]. X, Q and Y 16-byte aligned. Bit-exact. */
+moe_status moe_checkpoint_pack(const void *X, moe_dtype x_dt, long long ldx, long long R, int C, uint8_t *Q, uint8_t *S,
+                               hipStream_t stream);
+moe_status moe_checkpoint_unpack(const uint8_t *Q, const uint8_t *S, long long R, int C, moe_dtype y_dt, void *Y,
+                                 hipStream_t stream);
+
+/* What the FFN's backward pass keeps (caller's buffers, format as above): the
+ * T token rows and, for each of the M = T*k permuted rows, the gate and up
+ * projections g = x W1 and u = x W3. Codes 16-byte aligned. */
+typedef struct moe_ffn_checkpoint {
+    uint8_t *xq, *xs; /* [T, H], [T, H/32] */
+    uint8_t *gq, *gs; /* [M, F], [M, F/32] */
+    uint8_t *uq, *us; /* [M, F], [M, F/32] */
+} moe_ffn_checkpoint;
+
+/* Grouped expert FFN that writes its checkpoint: Yp as moe_grouped_ffn's, from
+ * the unquantised projections (h = silu(g) u rounded to bf16). M = T*k rows
+ * grouped by expert: row r is X[row_src[r] / k], as moe_permute gives them;
+ * row_src NULL: X [T, H] is in row order and k must be 1 (a shared expert, or
+ * one dense FFN: G = 1, offsets {0, T}). offsets [G+1]: row counts per group,
+ * offsets[G] <= M; rows from offsets[G] on are neither read nor written
+ * (Yp, gq, gs, uq, us). dt: BF16 (X, weights and Yp). H, F multiples of 32;
+ * k <= 64. Tensors 16-byte aligned. T == 0 returns MOE_OK.
+ * Workspace: moe_ffn_train_forward_workspace_bytes bytes. */
+size_t moe_ffn_train_forward_workspace_bytes(int T, int k, int G, int H, int F);
+moe_status moe_ffn_train_forward(const void *X, const int32_t *row_src, int k, int T, const int32_t *offsets, int G,
+                                 int H, int F, const void *W1, const void *W3, const void *W2, moe_dtype dt, void *Yp,
+                                 const moe_ffn_checkpoint *ckpt, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* Backward pass of moe_ffn_train_forward followed by moe_combine. For row r
+ * holding assignment a = t*k + j (a = row_src[r]), w = topk_w[a] and the
+ * checkpoint's values x, g, u (s = 1/(1 + exp(-g)), h = g s u):
+ *   p  = dY[t] W2^T                  dtopk_w[a] = sum_f p h
+ *   dg = w p u s (1 + g (1 - s))     du = w p g s
+ *   dX[t] = sum_j (dg W1^T + du W3^T)[assign_row[t*k + j]]  (+ dX_add[t])
+ *   dW1 = x^T dg, dW3 = x^T du, dW2 = (w h)^T dY per expert
+ * dg, du and w h are rounded to bf16 (matrix-core operands); every sum is
+ * fp32, in a fixed order. topk_w NULL: w = 1. row_src, assign_row: the
+ * permutation and its inverse, or both NULL (k == 1). An assign_row entry
+ * outside [0, offsets[G]) contributes nothing and gets dtopk_w = 0.
+ * Outputs may be NULL and are then not computed: dX [T, H] bf16, dtopk_w
+ * [T, k] fp32, dW1 and dW3 [G, H, F] (both or neither) and dW2 [G, F, H] in
+ * dw_dt (BF16 or F32). accumulate = 1 adds to what dW1, dW3 and dW2 hold
+ * (experts without rows are left as they were; with 0 they get zeros, also
+ * when T == 0). dX_add [T, H] bf16 or NULL: another path's gradient (the
+ * shared expert's, the residual's); may be dX itself.
+ * Workspace: moe_ffn_train_backward_workspace_bytes bytes. */
+size_t moe_ffn_train_backward_workspace_bytes(int T, int k, int G, int H, int F);
+moe_status moe_ffn_train_backward(const void *dY, const float *topk_w, const int32_t *row_src,
+                                  const int32_t *assign_row, int k, int T, const int32_t *offsets, int G, int H, int F,
+                                  const void *W1, const void *W3, const void *W2, moe_dtype dt,
+                                  const moe_ffn_checkpoint *ckpt, const void *dX_add, void *dX, float *dtopk_w,
+                                  void *dW1, void *dW3, void *dW2, moe_dtype dw_dt, int accumulate, void *ws,
+                                  size_t ws_bytes, hipStream_t stream);
 
 /* ---------------------------------------------------------------------------
  * moe_forward without a caller workspace, for callers that cannot allocate

@@ -3,29 +3,14 @@
 // here synchronises with the device or allocates device memory.
 #include <string.h>
 
+#include "abi_util.h"
 #include "common.h"
 
 using namespace moe;
 
 namespace {
 
-constexpr size_t kAlign = 256;
 constexpr int kGemvBM = 16;  // rows per tile of the row-streaming GEMM
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-// Bump allocator over a caller-provided workspace. With base == NULL it only
-// measures.
-struct Carver {
-    char *base;
-    size_t used = 0;
-    explicit Carver(void *b) : base(static_cast<char *>(b)) {}
-    void *take(size_t bytes) {
-        void *p = base ? base + used : nullptr;
-        used += align_up(bytes);
-        return p;
-    }
-};
 
 size_t dt_size(moe_dtype d) { return d == MOE_F32 ? 4 : d == MOE_BF16 ? 2 : 1; }
 
@@ -44,17 +29,7 @@ WType wtype(moe_dtype w) {
     return w == MOE_F32 ? W_F32 : w == MOE_BF16 ? W_BF16 : w == MOE_MXFP4 ? W_MXFP4 : W_FP8;
 }
 
-moe_status hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
-
-#define MOE_TRY(expr)                                  \
-    do {                                               \
-        hipError_t e_ = (expr);                        \
-        if (e_ != hipSuccess) return MOE_ERR_HIP;      \
-    } while (0)
-
 // Shape rules for expert matrices [K][N].
-constexpr int kMaxDim = 1 << 20;  // largest H or F (keeps every size product in range)
-
 moe_status check_ffn_dims(int H, int F, moe_dtype w_dt) {
     if (H < 1 || F < 1) return MOE_ERR_INVALID_ARG;
     if (H % 32 || F % 32 || H > kMaxDim || F > kMaxDim) return MOE_ERR_UNSUPPORTED;
@@ -155,8 +130,6 @@ struct ExtraGroup {
     const void *W1 = nullptr, *W3 = nullptr, *W2 = nullptr;
     const float *S1 = nullptr, *S3 = nullptr, *S2 = nullptr;
 };
-
-long long max_tiles_for(long long rows, int groups, int bm) { return (rows + bm - 1) / bm + groups; }
 
 // xrows: rows of quantised expert input (W8A8 only).
 size_t ffn_ws_carve(Carver &c, FfnWs &w, const FfnPlan &p, int rows, int groups, int H, int hw,
@@ -316,7 +289,8 @@ unsigned moe_debug_bounds(void) {
     if (hipDeviceSynchronize() != hipSuccess) return ~0u;
     return bounds_take_tiled128() | bounds_take_tiled256() | bounds_take_tiledf32() | bounds_take_a8() |
            bounds_take_stream() | bounds_take_permute() | bounds_take_combine() | bounds_take_quant() |
-           bounds_take_ep() | bounds_take_persist();
+           bounds_take_ep() | bounds_take_persist() | bounds_take_tiled_ckpt() | bounds_take_train_rows() |
+           bounds_take_train_weights() | bounds_take_train_gather();
 #else
     return 0u;
 #endif

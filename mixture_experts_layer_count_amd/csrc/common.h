@@ -57,6 +57,10 @@ unsigned bounds_take_combine();
 unsigned bounds_take_quant();
 unsigned bounds_take_ep();
 unsigned bounds_take_persist();
+unsigned bounds_take_tiled_ckpt();
+unsigned bounds_take_train_rows();
+unsigned bounds_take_train_weights();
+unsigned bounds_take_train_gather();
 
 // ---------------------------------------------------------------------------
 // Vector types for MFMA operands and wide loads
@@ -192,6 +196,9 @@ struct GemmProblem {
     // and left zero). NULL: no split.
     float *tail_part = nullptr;
     int32_t *tail_cnt = nullptr;
+    // checkpointing gate/up (launch_tiled_ckpt): codes and scale bytes of the
+    // gate and the up projection
+    uint8_t *ckpt[4] = {nullptr, nullptr, nullptr, nullptr};
     // rows of A (the bounds-checked build's checks only; 0: not known)
     long long a_rows = 0;
 };
@@ -223,6 +230,10 @@ hipError_t launch_tiled_persist(const GemmProblem &p, bool swiglu, hipStream_t s
 // and the number of counters
 size_t tiled_tail_bytes(int bm);
 constexpr int tiled_tail_counters = 256;
+
+// gate/up with bf16 weights that also writes both projections as MXFP8
+// checkpoints (p.ckpt); bm as for launch_tiled_gemm
+hipError_t launch_tiled_ckpt(const GemmProblem &p, int bm, hipStream_t s);
 
 // W8A8 variant of the LDS-tiled grouped GEMM (fp8 weights and fp8
 // activations with per-row 128-column scales, p.As transposed by GEMM row):
@@ -293,5 +304,75 @@ hipError_t launch_combine(const void *Yp, const void *S, long long split_stride,
 // Sum fp32 split partials [nsplit][M][N] into out [M][N] (f32 or bf16).
 hipError_t launch_reduce_splits(const float *part, long long split_stride, int nsplit, int M,
                                 int N, moe_dtype out_dt, void *out, hipStream_t s);
+
+// MXFP8 activation checkpoints (mx8.hip): rows of C values (a multiple of 32),
+// codes Q [R][C] and scale bytes S [R][C/32]
+hipError_t launch_mx8_pack(const void *X, moe_dtype x_dt, long long ldx, long long R, int C, uint8_t *Q, uint8_t *S,
+                           hipStream_t s);
+hipError_t launch_mx8_unpack(const uint8_t *Q, const uint8_t *S, long long R, int C, moe_dtype y_dt, void *Y,
+                             hipStream_t s);
+
+// Router losses and the gradient at its logits (balance.hip). seq: device
+// [B + 1] token offsets or NULL (then B == 1).
+size_t balance_ws_bytes(int T, int E, int B);
+hipError_t launch_balance_loss(const float *logits, const int32_t *idx, int T, int E, int k, const int32_t *seq, int B,
+                               float alpha, float beta, float *loss, int32_t *counts, int32_t *seq_counts, void *ws,
+                               hipStream_t s);
+hipError_t launch_route_backward(const float *logits, const int32_t *idx, const float *w, const float *dw, int T, int E,
+                                 int k, const int32_t *seq, int B, const int32_t *seq_counts, float alpha, float beta,
+                                 const float *dloss, float *dlogits, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// Backward pass of the grouped FFN (train_rows.hip, train_weights.hip)
+// ---------------------------------------------------------------------------
+
+// C[r][n] = sum_k A(r)[k] B_g[n][k]: both operands K-contiguous. K is one
+// matrix's K0 columns, or two matrices' one after the other (B1 != NULL: K =
+// 2 K0, A rows 2 K0 wide). Row r of A is A[row_src[r] / gk] (A[r] if NULL).
+struct RowsProblem {
+    const uint16_t *A;
+    const int32_t *row_src;
+    int gk, lda;
+    const int32_t *tiles, *n_tiles, *group_tile_start;
+    int n_groups, max_tiles;
+    int M, N, K0;
+    const uint16_t *B0, *B1;  // [G][N][K0]
+    float *C;                 // plain form: [M][N] fp32
+    // SwiGLU backward form: C is p = dY W2^T, and with the checkpointed g, u
+    // and the row's routing weight w (1 if topk_w is NULL): dGU [M][2 N] (dg
+    // then du), Hw [M][N] = w h, and dw_part[column tile][M] = sum over the
+    // tile's columns of p h
+    const uint8_t *gq, *gs, *uq, *us;
+    const float *topk_w;
+    const int32_t *w_src;     // row_src for topk_w (NULL: row r)
+    uint16_t *dGU, *Hw;
+    float *dw_part;
+    long long a_rows = 0;     // rows of A (bounds-checked build; 0: not known)
+};
+int rows_gemm_bm(long long rows, int groups);
+constexpr int rows_gemm_bn = 256;  // columns per tile
+hipError_t launch_rows_gemm(const RowsProblem &p, bool swiglu_backward, int bm, hipStream_t s);
+
+// dW_g[m][n] = sum over rows r of group g of A(r)[m] B(r)[n], for one or two
+// (B1cols: columns N .. 2 N - 1 of B's rows) output matrices.
+struct WeightsProblem {
+    const uint16_t *A, *B;
+    int lda, ldb;
+    const int32_t *a_src, *b_src;  // row r is A[a_src[r] / gk]; NULL: A[r]
+    int gk;
+    const int32_t *offsets;        // [G + 1]
+    int G, M, MD, ND;              // M rows in all; output MD x ND
+    void *C0, *C1;                 // [G][MD][ND]; C1 NULL: one output
+    moe_dtype c_dt;
+    int accumulate;                // add to what C holds
+    long long a_rows = 0, b_rows = 0;
+};
+hipError_t launch_weights_gemm(const WeightsProblem &p, hipStream_t s);
+
+// dX[t] = sum_j rows[assign_row[t k + j]] (+ add[t]) and dw[t k + j] = sum
+// over column tiles of dw_part[tile][row]; assign_row NULL: row t (k == 1).
+// Rows outside [0, min(M, *n_rows)) contribute nothing. dX or dw may be NULL.
+hipError_t launch_gather_grads(const float *rows, const float *dw_part, int n_part, const int32_t *assign_row, int T,
+                               int k, const int32_t *n_rows, int M, int H, const void *add, void *dX, float *dw, hipStream_t s);
 
 }  // namespace moe

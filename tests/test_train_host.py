@@ -1,0 +1,139 @@
+"""The training entry points on the host: arguments are answered with status
+codes before anything is launched, sizes are formed without overflow, and the
+binding refuses tensors the calls cannot take. No GPU is needed."""
+import ctypes
+
+import pytest
+import torch
+
+import mixture_experts_layer_count_amd as moe
+from mixture_experts_layer_count_amd import _lib
+
+OK, INVALID, UNSUPPORTED, WS_SMALL = 0, 1, 2, 3
+F32, BF16, FP8 = 0, 1, 2
+FAKE = ctypes.c_void_p(0x1000)  # never dereferenced: validation fails first
+ODD = ctypes.c_void_p(0x1004)   # not on a 16-byte boundary
+BIG = 1 << 50
+
+
+def _balance(**kw):
+    a = dict(logits=FAKE, idx=FAKE, T=64, E=8, k=2, seq=None, B=1, alpha=0.1, beta=0.1, loss=FAKE, counts=FAKE,
+             seq_counts=FAKE, ws=FAKE, ws_bytes=16, stream=None) | kw
+    return moe.lib().moe_balance_loss(*a.values())
+
+
+def test_balance_loss_validation():
+    ws = moe.lib().moe_balance_loss_workspace_bytes
+    assert 0 < ws(64, 8, 1) < ws(4096, 8, 1) < ws(4096, 256, 16)
+    assert ws(0, 8, 1) > 0 and ws(64, 2048, 1) == 0 and ws(64, 8, 0) == 0 and ws(-1, 8, 1) == 0 and ws(64, 8, 65536) == 0
+    assert ws(0x7fffffff, 1024, 65535) > 1 << 32
+    assert _balance() == WS_SMALL
+    assert _balance(ws=None, ws_bytes=BIG) == WS_SMALL
+    for bad in (dict(T=-1), dict(E=0), dict(k=0), dict(k=9), dict(B=0), dict(B=2), dict(logits=None), dict(idx=None),
+                dict(loss=None), dict(counts=None), dict(seq_counts=None)):
+        assert _balance(**bad) == INVALID, bad
+    for bad in (dict(E=1025), dict(E=128, k=65), dict(seq=FAKE, B=65536), dict(T=0x7fffffff), dict(T=1 << 30, E=2, k=2)):
+        assert _balance(**bad) == UNSUPPORTED, bad
+
+
+def _route_back(**kw):
+    a = dict(logits=FAKE, idx=FAKE, w=FAKE, dw=FAKE, T=64, E=8, k=2, seq=None, B=1, seq_counts=FAKE, alpha=0.1,
+             beta=0.1, dloss=None, d=FAKE, stream=None) | kw
+    return moe.lib().moe_route_backward(*a.values())
+
+
+def test_route_backward_validation():
+    assert _route_back(T=0, logits=None, idx=None, w=None, d=None) == OK
+    for bad in (dict(dw=None, seq_counts=None), dict(d=None), dict(logits=None), dict(w=None), dict(idx=None),
+                dict(B=3), dict(k=9), dict(T=-1)):
+        assert _route_back(**bad) == INVALID, bad
+    assert _route_back(E=2048) == UNSUPPORTED and _route_back(T=1 << 30, E=8) == UNSUPPORTED
+
+
+def test_checkpoint_validation():
+    pack, unpack = moe.lib().moe_checkpoint_pack, moe.lib().moe_checkpoint_unpack
+    assert pack(None, BF16, 64, 0, 64, None, None, None) == OK
+    assert pack(FAKE, BF16, 32, 4, 64, FAKE, FAKE, None) == INVALID      # ldx < C
+    assert pack(FAKE, BF16, 64, -1, 64, FAKE, FAKE, None) == INVALID
+    assert pack(FAKE, FP8, 64, 4, 64, FAKE, FAKE, None) == UNSUPPORTED
+    assert pack(FAKE, BF16, 72, 4, 72, FAKE, FAKE, None) == UNSUPPORTED  # C % 32
+    assert pack(FAKE, BF16, 68, 4, 64, FAKE, FAKE, None) == UNSUPPORTED  # rows off 16 bytes
+    assert pack(FAKE, F32, 66, 4, 64, FAKE, FAKE, None) == UNSUPPORTED
+    assert pack(FAKE, BF16, 1 << 20, 0x7fffffff, 1 << 20, FAKE, FAKE, None) == UNSUPPORTED
+    for a in ((None, FAKE, FAKE), (ODD, FAKE, FAKE), (FAKE, ODD, FAKE), (FAKE, FAKE, None)):
+        assert pack(a[0], BF16, 64, 4, 64, a[1], a[2], None) == INVALID
+        assert unpack(a[0], a[2], 4, 64, BF16, a[1], None) == INVALID
+    assert unpack(FAKE, FAKE, 4, 60, BF16, FAKE, None) == UNSUPPORTED
+    assert unpack(FAKE, FAKE, 4, 64, FP8, FAKE, None) == UNSUPPORTED
+    assert unpack(None, None, 0, 64, F32, None, None) == OK
+
+
+def _ckpt(**kw):
+    c = _lib._CheckpointPtrs(*([0x1000] * 6))
+    for n, v in kw.items():
+        setattr(c, n, v)
+    return ctypes.byref(c)
+
+
+def _forward(**kw):
+    a = dict(X=FAKE, row_src=FAKE, k=2, T=64, offsets=FAKE, G=8, H=256, F=96, W1=FAKE, W3=FAKE, W2=FAKE, dt=BF16,
+             Yp=FAKE, ckpt=_ckpt(), ws=FAKE, ws_bytes=16, stream=None) | kw
+    return moe.lib().moe_ffn_train_forward(*a.values())
+
+
+def _backward(**kw):
+    a = dict(dY=FAKE, w=FAKE, row_src=FAKE, assign_row=FAKE, k=2, T=64, offsets=FAKE, G=8, H=256, F=96, W1=FAKE,
+             W3=FAKE, W2=FAKE, dt=BF16, ckpt=_ckpt(), add=None, dX=FAKE, dw=FAKE, dW1=FAKE, dW3=FAKE, dW2=FAKE,
+             dw_dt=BF16, accumulate=0, ws=FAKE, ws_bytes=16, stream=None) | kw
+    return moe.lib().moe_ffn_train_backward(*a.values())
+
+
+SHARED_INVALID = [dict(T=-1), dict(k=0), dict(G=0), dict(H=0), dict(F=-32), dict(offsets=None), dict(W1=None),
+                  dict(W2=ODD), dict(W3=ODD), dict(ckpt=None), dict(ckpt=_ckpt(xq=None)), dict(ckpt=_ckpt(uq=0x1008)),
+                  dict(ckpt=_ckpt(gs=None)), dict(row_src=None)]
+SHARED_UNSUPPORTED = [dict(dt=F32), dict(dt=FP8), dict(H=250), dict(F=100), dict(H=1 << 21), dict(k=65),
+                      dict(T=1 << 30), dict(G=65536)]
+
+
+def test_ffn_train_forward_validation():
+    ws = moe.lib().moe_ffn_train_forward_workspace_bytes
+    assert 0 < ws(64, 2, 8, 256, 96) < ws(4096, 2, 8, 256, 96)
+    assert ws(64, 2, 8, 250, 96) == 0 and ws(64, 0, 8, 256, 96) == 0
+    assert ws(1 << 25, 63, 65535, 1 << 20, 1 << 20) > 1 << 50
+    assert _forward() == WS_SMALL and _forward(ws=None, ws_bytes=BIG) == WS_SMALL
+    assert _forward(T=0, X=None, Yp=None, ckpt=None, ws=None) == OK
+    for bad in SHARED_INVALID + [dict(X=None), dict(X=ODD), dict(Yp=None), dict(row_src=None, k=2)]:
+        assert _forward(**bad) == INVALID, bad
+    for bad in SHARED_UNSUPPORTED:
+        assert _forward(**bad) == UNSUPPORTED, bad
+    assert _forward(row_src=None, k=1) == WS_SMALL
+
+
+def test_ffn_train_backward_validation():
+    ws = moe.lib().moe_ffn_train_backward_workspace_bytes
+    assert 0 < ws(64, 2, 8, 256, 96) < ws(4096, 2, 8, 256, 96)
+    assert ws(1 << 25, 63, 65535, 1 << 20, 1 << 20) > 1 << 51
+    assert _backward() == WS_SMALL and _backward(ws=None, ws_bytes=BIG) == WS_SMALL
+    assert _backward(ws=ODD, ws_bytes=BIG) == WS_SMALL
+    for bad in SHARED_INVALID + [dict(dY=None), dict(dY=ODD), dict(assign_row=None), dict(dW1=None), dict(dW3=None),
+                                 dict(dW2=ODD), dict(dX=ODD), dict(add=FAKE, dX=None), dict(accumulate=2)]:
+        assert _backward(**bad) == INVALID, bad
+    for bad in SHARED_UNSUPPORTED + [dict(dw_dt=FP8)]:
+        assert _backward(**bad) == UNSUPPORTED, bad
+    assert _backward(row_src=None, assign_row=None, k=1, w=None, dX=None, dw=None, dW2=None) == WS_SMALL
+
+
+def test_binding_refuses():
+    """The binding names the operand it refuses (host tensors never reach the library)."""
+    z, idx = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="logits"):
+        moe.balance_loss(z, idx, 0.1)
+    with pytest.raises(TypeError, match="logits"):
+        moe.balance_loss(z.double(), idx, 0.1)
+    with pytest.raises(TypeError, match="W1"):
+        w = torch.zeros(2, 64, 32)
+        moe.ffn_train_forward(torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32), w, w, w)
+    with pytest.raises(ValueError, match="Q"):
+        moe.checkpoint_unpack(torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 2, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="X"):
+        moe.checkpoint_pack(torch.zeros(4, 64))
