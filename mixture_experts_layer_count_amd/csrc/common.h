@@ -347,10 +347,20 @@ struct RowsProblem {
     const int32_t *w_src;     // row_src for topk_w (NULL: row r)
     uint16_t *dGU, *Hw;
     float *dw_part;
-    long long a_rows = 0;     // rows of A (bounds-checked build; 0: not known)
+    int a_rows = 0;           // rows of A, when gathered (in at most gather_max_bytes)
+    // split of the last, partial round: room for xcd_parts parts' sums per XCD
+    // (rows_gemm_part_bytes) and rows_gemm_counters counters, zero at launch
+    // and used by one launch. NULL: no split
+    float *part = nullptr;
+    int32_t *part_cnt = nullptr;
+    int xcd_parts = 0;
 };
 int rows_gemm_bm(long long rows, int groups);
 constexpr int rows_gemm_bn = 256;  // columns per tile
+constexpr int rows_gemm_counters = 256;
+int rows_gemm_xcd_parts(long long max_tiles, int N);
+size_t rows_gemm_part_bytes(int bm, int xcd_parts);
+constexpr uint32_t gather_max_bytes = 0xfffff000u;  // of a gathered matrix: 32-bit offsets
 hipError_t launch_rows_gemm(const RowsProblem &p, bool swiglu_backward, int bm, hipStream_t s);
 
 // dW_g[m][n] = sum over rows r of group g of A(r)[m] B(r)[n], for one or two
@@ -358,14 +368,13 @@ hipError_t launch_rows_gemm(const RowsProblem &p, bool swiglu_backward, int bm, 
 struct WeightsProblem {
     const uint16_t *A, *B;
     int lda, ldb;
-    const int32_t *a_src, *b_src;  // row r is A[a_src[r] / gk]; NULL: A[r]
-    int gk;
+    const int32_t *a_src, *b_src;  // row r is A[a_src[r] / gk]; NULL: A[r] (at most one given)
+    int gk, src_rows;              // rows of the gathered operand (in at most gather_max_bytes)
     const int32_t *offsets;        // [G + 1]
     int G, M, MD, ND;              // M rows in all; output MD x ND
     void *C0, *C1;                 // [G][MD][ND]; C1 NULL: one output
     moe_dtype c_dt;
     int accumulate;                // add to what C holds
-    long long a_rows = 0, b_rows = 0;
 };
 hipError_t launch_weights_gemm(const WeightsProblem &p, hipStream_t s);
 

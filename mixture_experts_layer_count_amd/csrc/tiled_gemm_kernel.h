@@ -178,6 +178,14 @@ __device__ __forceinline__ void copy16(const void *g, uint8_t *l) {
 __device__ __forceinline__ void copy4(const void *g, uint8_t *l) {
     __builtin_amdgcn_global_load_lds((AS1 void *)g, (AS3 void *)l, 4, 0, 0);
 }
+// a buffer descriptor's last word: raw 32-bit elements, no swizzle
+constexpr int kBufferWord3 = 0x00020000;
+// copy16 from byte offset off of [base, base + bytes): zeros where the 16 bytes
+// pass the end (the hardware's range check)
+__device__ __forceinline__ void copy16_buffer(const void *base, uint32_t bytes, uint32_t off, uint8_t *l) {
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, bytes, kBufferWord3);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (AS3 void *)l, 16, off, 0, 0, 0);
+}
 __device__ __forceinline__ uint32_t lds_addr(const uint8_t *p) {
     return (uint32_t)(uintptr_t)(const AS3 uint8_t *)p;
 }
@@ -201,6 +209,13 @@ __device__ __forceinline__ u32x2 ds_tr8_at(uint32_t addr) {
     static_assert(OFF >= 0 && OFF < 65536, "ds offset field");
     u32x2 r;
     asm volatile("ds_read_b64_tr_b8 %0, %1 offset:%2" : "=v"(r) : "v"(addr), "i"(OFF));
+    return r;
+}
+template <int OFF>
+__device__ __forceinline__ u32x2 ds_tr16_at(uint32_t addr) {
+    static_assert(OFF >= 0 && OFF < 65536, "ds offset field");
+    u32x2 r;
+    asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%2" : "=v"(r) : "v"(addr), "i"(OFF));
     return r;
 }
 __device__ __forceinline__ void fence(u32x2 &v) { asm volatile("" : "+v"(v)); }

@@ -24,8 +24,8 @@ moe_status check_router(int T, int E, int k, int B, const int32_t *seq_offsets) 
 // gathered: row_src is given (without tokens it may be null)
 moe_status check_train_ffn(bool gathered, int k, int T, int G, int H, int F, moe_dtype dt) {
     if (T < 0 || k < 1 || G < 1 || H < 1 || F < 1 || (!gathered && k != 1)) return MOE_ERR_INVALID_ARG;
-    if (dt != MOE_BF16 || H % 32 || F % 32 || H > kMaxDim || F > kMaxDim || G > 65535 || k > 64) return MOE_ERR_UNSUPPORTED;
-    if ((long long)T * k > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
+    if (dt != MOE_BF16 || H % 32 || F % 32 || H > kMaxDim || F > kMaxDim || G > 1024 || k > 64) return MOE_ERR_UNSUPPORTED;
+    if ((long long)T * k > 0x7fffffffLL || 2LL * T * H > gather_max_bytes) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 
@@ -66,6 +66,9 @@ struct BackwardWs {
     uint16_t *hw;   // [M][F]
     float *rows;    // [M][H] row gradients at the token rows
     float *dw_part; // [column tiles of F][M]
+    float *part;    // sums of split items, and their counters (one set per launch)
+    int32_t *part_cnt;
+    int parts_f, parts_h;
     size_t carve(void *ws, long long T, long long M, int G, int H, int F) {
         Carver c(ws);
         t.carve(c, M, G, rows_gemm_bm(M, G));
@@ -74,6 +77,10 @@ struct BackwardWs {
         hw = static_cast<uint16_t *>(c.take(2 * (size_t)M * F));
         rows = static_cast<float *>(c.take(4 * (size_t)M * H));
         dw_part = static_cast<float *>(c.take(4 * (size_t)M * ((F + rows_gemm_bn - 1) / rows_gemm_bn)));
+        parts_f = rows_gemm_xcd_parts(t.max_tiles, F);
+        parts_h = rows_gemm_xcd_parts(t.max_tiles, H);
+        part = static_cast<float *>(c.take(rows_gemm_part_bytes(t.bm, parts_f > parts_h ? parts_f : parts_h)));
+        part_cnt = static_cast<int32_t *>(c.take(sizeof(int32_t) * 2 * rows_gemm_counters));
         return c.used;
     }
 };
@@ -226,7 +233,7 @@ moe_status moe_ffn_train_backward(const void *dY, const float *topk_w, const int
     if (bad16(ws) || ws_bytes < w.carve(ws, T, M, G, H, F)) return MOE_ERR_WORKSPACE_TOO_SMALL;
 
     if (T > 0) {
-        MOE_TRY(w.t.build(offsets, G, stream));
+        MOE_TRY(w.t.build(offsets, G, stream, w.part_cnt, 2 * rows_gemm_counters));
         RowsProblem p{};
         p.gk = k;
         p.tiles = w.t.tiles;
@@ -235,6 +242,7 @@ moe_status moe_ffn_train_backward(const void *dY, const float *topk_w, const int
         p.n_groups = G;
         p.max_tiles = w.t.max_tiles;
         p.M = M;
+        p.part = w.part;
         // p = dY W2^T, then dg, du, w h and the routing weights' partial sums
         RowsProblem b = p;
         b.A = static_cast<const uint16_t *>(dY);
@@ -252,6 +260,8 @@ moe_status moe_ffn_train_backward(const void *dY, const float *topk_w, const int
         b.w_src = row_src;
         b.dGU = w.dgu;
         b.Hw = w.hw;
+        b.part_cnt = w.part_cnt;
+        b.xcd_parts = w.parts_f;
         b.dw_part = dtopk_w ? w.dw_part : nullptr;
         MOE_TRY(launch_rows_gemm(b, true, w.t.bm, stream));
         if (dX) {
@@ -264,6 +274,8 @@ moe_status moe_ffn_train_backward(const void *dY, const float *topk_w, const int
             d.B0 = static_cast<const uint16_t *>(W1);
             d.B1 = static_cast<const uint16_t *>(W3);
             d.C = w.rows;
+            d.part_cnt = w.part_cnt + rows_gemm_counters;
+            d.xcd_parts = w.parts_h;
             MOE_TRY(launch_rows_gemm(d, false, w.t.bm, stream));
         }
         MOE_TRY(launch_gather_grads(w.rows, w.dw_part, (F + rows_gemm_bn - 1) / rows_gemm_bn, assign_row, T, k,
@@ -273,6 +285,7 @@ moe_status moe_ffn_train_backward(const void *dY, const float *topk_w, const int
     // with T == 0 every expert is empty: zeros (or, accumulating, nothing)
     WeightsProblem q{};
     q.gk = k;
+    q.src_rows = T;
     q.offsets = offsets;
     q.G = G;
     q.M = M;
@@ -281,11 +294,9 @@ moe_status moe_ffn_train_backward(const void *dY, const float *topk_w, const int
     if (dW1) {
         q.A = w.x;
         q.a_src = row_src;
-        q.a_rows = T;
         q.lda = H;
         q.MD = H;
         q.B = w.dgu;
-        q.b_rows = M;
         q.ldb = 2 * F;
         q.ND = F;
         q.C0 = dW1;
@@ -295,12 +306,10 @@ moe_status moe_ffn_train_backward(const void *dY, const float *topk_w, const int
     if (dW2) {
         q.A = w.hw;
         q.a_src = nullptr;
-        q.a_rows = M;
         q.lda = F;
         q.MD = F;
         q.B = T > 0 ? static_cast<const uint16_t *>(dY) : w.hw;
         q.b_src = row_src;
-        q.b_rows = T;
         q.ldb = H;
         q.ND = H;
         q.C0 = dW2;

@@ -13,10 +13,23 @@
 //    out (they are summed over a token's k rows before the one rounding).
 // dg, du and w h are rounded to bf16: the operands of the bf16 matrix cores.
 //
-// Tile BM (128 or 256) rows x 256 columns, 32 deep a step, 8 wavefronts in
-// 2 x 4, each BM/2 rows x 64 columns; copy ring, swizzle, waits and barriers
-// as in tiled_gemm_kernel.h, whose A-operand layout (64-byte rows, 16-byte
-// reads) serves both operands here: no transposing reads.
+// Tile BM (128 or 256) rows x 256 columns, 64 deep a step, 8 wavefronts in
+// 2 x 4, each BM/2 rows x 64 columns. Both operands are copied as whole
+// 128-byte lines of a row (32 deep, the 64-byte halves were separate requests
+// to L2) by buffer loads: a lane's offset stays the same over k, the step only
+// moves the scalar descriptor. LDS rows are 128 bytes, 16-byte chunk c of row
+// r at c ^ ((r >> 1) & 7): a ds_read_b128 serves lanes 0-3, 12-15 and 20-27
+// (then the others) together, whose eight even and eight odd rows then hit all
+// 64 banks once.
+// A step's two 32-deep halves alternate in two register sets: the second
+// half's fragments are read while the first is multiplied and the next step's
+// first while the second is, so one barrier a step (after the next step's
+// copies have landed) both publishes the next stage and frees this one.
+//
+// Tail: the last, partial round of an XCD's items is split over k into up to
+// kRowsParts parts where that shortens it and an item is long (see
+// pick_rows); a part leaves its fp32 sums and the last one to finish adds them
+// in part order, so results do not depend on which that is.
 // build-flags: -mllvm -amdgpu-mfma-vgpr-form
 #include "tiled_gemm_kernel.h"
 
@@ -29,13 +42,18 @@ namespace {
 
 constexpr int kRowsBN = rows_gemm_bn;
 
+constexpr int kRowsBK = 64;
+constexpr int kRowsParts = 4;        // parts of a split item at most
+constexpr int kRowsPartSteps = 32;   // and steps a part has at least (a part's sums cost about 10 steps)
+constexpr int kRowsXcdParts = 64;    // parts (and their fp32 sums) per XCD at most
+
 template <int BM>
 struct RowsRing {
-    static constexpr int a_bytes = BM * 64;
-    static constexpr int stage = a_bytes + kRowsBN * 64;
-    static constexpr int S = kRingBudget / stage < 6 ? kRingBudget / stage : 6;
-    static constexpr int nA = BM / 128;  // 1 KB copies (16 rows) per wavefront and step
-    static constexpr int nB = 2;
+    static constexpr int a_bytes = BM * 128;
+    static constexpr int stage = a_bytes + kRowsBN * 128;
+    static constexpr int S = kRingBudget / stage < 3 ? kRingBudget / stage : 3;
+    static constexpr int nA = BM / 64;  // 1 KB copies (8 rows) per wavefront and step
+    static constexpr int nB = kRowsBN / 64;
     static constexpr int per_tile = nA + nB;
     static constexpr int MI = BM / 32;   // 16-row blocks per wavefront
     // epilogue staging per wavefront: a 16 x 64 block of each output (bf16,
@@ -44,8 +62,48 @@ struct RowsRing {
     static constexpr int stg = 3 * 16 * old * 2 + 2 * 16 * cld;
     static constexpr int dw = 8 * stg;   // [4][BM] floats behind it
     static constexpr int lds = S * stage > dw + 16 * BM ? S * stage : dw + 16 * BM;
-    static_assert(lds <= 160 * 1024, "LDS");
+    static_assert(S >= 2 && lds <= 160 * 1024, "LDS");
 };
+
+// This workgroup's item, or part of one. Items are in tile_of's order, a
+// contiguous run of them per XCD; the run's last `tail` items (one partial
+// round of the XCD's CUs) are split into the number of parts that ends the
+// round soonest: ceil(tail parts / CUs) / parts rounds.
+__device__ __forceinline__ bool pick_rows(const RowsProblem &p, int nN, int nk, Unit &u) {
+    GemmProblem order{};
+    order.tiles = p.tiles;
+    order.n_tiles = p.n_tiles;
+    order.group_tile_start = p.group_tile_start;
+    const int n_tiles = *p.n_tiles, n_work = n_tiles * nN;
+    const int per = (n_work + kXcds - 1) / kXcds;
+    const int xcd = blockIdx.x % kXcds, slot = blockIdx.x / kXcds;
+    const int first = xcd * per, n = min(per, n_work - first);
+    if (n <= 0) return false;
+    const int tail = n % kBlocksPerXcd, full = n - tail;
+    int parts = 1;
+    if (p.part && tail > 0) {
+        int rounds = 1;  // of 1 / parts
+        for (int q = 2; q <= kRowsParts; ++q) {
+            const int r = (tail * q + kBlocksPerXcd - 1) / kBlocksPerXcd;
+            if (tail * q <= p.xcd_parts && q * kRowsPartSteps <= nk && r * parts < rounds * q) {
+                parts = q;
+                rounds = r;
+            }
+        }
+    }
+    int item = slot;
+    if (slot >= full) {
+        const int v = slot - full;
+        if (v >= tail * parts) return false;
+        item = full + v / parts;
+        u.part = v % parts;
+        u.parts = parts;
+        u.tail_slot = xcd * kBlocksPerXcd + v / parts;
+        u.part_slot = xcd * p.xcd_parts + v;
+    }
+    tile_of(order, nN, n_tiles, first + item, u.mt, u.nt);
+    return true;
+}
 
 template <int BM, bool BACK>
 __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN) {
@@ -53,13 +111,13 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
     constexpr int S = R::S, MI = R::MI, NB = 4, NC = R::per_tile, NR = NB + MI;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[R::lds];
 
-    GemmProblem order{};
-    order.tiles = p.tiles;
-    order.n_tiles = p.n_tiles;
-    order.group_tile_start = p.group_tile_start;
-    order.M = p.M;
-    int mt, nt;
-    if (!pick_tile(order, nN, BM, mt, nt)) return;
+    // steps of one B matrix (the last may be half) and of all
+    const int nk0 = (p.K0 + kRowsBK - 1) / kRowsBK, nk_all = p.B1 ? 2 * nk0 : nk0;
+    Unit u;
+    if (!pick_rows(p, nN, nk_all, u)) return;
+    const int mt = u.mt, nt = u.nt;
+    const int k_first = nk_all * u.part / u.parts;
+    const int nk = nk_all * (u.part + 1) / u.parts - k_first;
     if (MOE_BOUNDS_FAIL(mt < p.max_tiles, BOUNDS_TILE)) return;
     const int g = p.tiles[4 * mt], row0 = p.tiles[4 * mt + 1], row_end = p.tiles[4 * mt + 2];
     if (MOE_BOUNDS_FAIL(g >= 0 && g < p.n_groups && row0 >= 0 && row0 < row_end && row_end <= p.M, BOUNDS_TILE))
@@ -70,48 +128,62 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
     const int i16 = lane & 15, gq = lane >> 4;
     const int nblk = min(max((row_end - row0 - wr * (BM / 2) + 15) >> 4, 0), MI);
 
-    // ---- copy sources: lane -> row lane / 4 of a 16-row copy, chunk lane % 4 ----
-    const uint16_t *a_src[R::nA], *b_src[R::nB];
+    // ---- copy sources: lane -> row lane / 8 of an 8-row copy, physical chunk
+    // lane % 8; byte offsets from the descriptor's start, which is the tile's
+    // first row (gathered A: row 0) at the step's first column ----
+    uint32_t a_off[R::nA], b_off[R::nB];
 #pragma unroll
     for (int q = 0; q < R::nA; ++q) {
-        int r = row0 + 16 * (w * R::nA + q) + (lane >> 2);
+        const int tr = 8 * (w * R::nA + q) + (lane >> 3);
+        int r = row0 + tr;
         if (r >= row_end) r = row0;  // rows past the tile's end copy a valid row (never stored)
-        long long src = p.row_src ? (long long)(p.row_src[r] / p.gk) : (long long)r;
-        if (MOE_BOUNDS_FAIL(src >= 0 && (p.a_rows <= 0 || src < p.a_rows), BOUNDS_A_ROW)) src = 0;
-        a_src[q] = p.A + src * p.lda + 8 * aswz_chunk(lane);
+        int src = p.row_src ? p.row_src[r] / p.gk : r - row0;
+        if (p.row_src && MOE_BOUNDS_FAIL(src >= 0 && src < p.a_rows, BOUNDS_A_ROW)) src = 0;
+        a_off[q] = 2u * ((uint32_t)src * p.lda + 8 * ((lane & 7) ^ ((tr >> 1) & 7)));
     }
-    const long long b_stride = (long long)p.N * p.K0;
 #pragma unroll
     for (int q = 0; q < R::nB; ++q) {
-        const int n = min(n0 + 16 * (w * R::nB + q) + (lane >> 2), p.N - 1);
-        b_src[q] = p.B0 + g * b_stride + (long long)n * p.K0 + 8 * aswz_chunk(lane);
+        const int tr = 8 * (w * R::nB + q) + (lane >> 3);
+        b_off[q] = 2u * ((uint32_t)min(tr, p.N - 1 - n0) * p.K0 + 8 * ((lane & 7) ^ ((tr >> 1) & 7)));
     }
-    const int nk0 = p.K0 / kBK, nk = p.B1 ? 2 * nk0 : nk0;
-    // the second matrix continues k: its elements lie this far behind the
-    // first's (two allocations: integer arithmetic on their addresses)
-    const long long b_next = p.B1 ? (long long)((uintptr_t)p.B1 - (uintptr_t)p.B0) - 2LL * p.K0 : 0;
+    const char *a0 = reinterpret_cast<const char *>(p.A + (p.row_src ? 0LL : (long long)row0 * p.lda));
+    const long long b_first = ((long long)g * p.N + n0) * p.K0;
+    const char *b0 = reinterpret_cast<const char *>(p.B0 + b_first);
+    const char *b1 = p.B1 ? reinterpret_cast<const char *>(p.B1 + b_first) : b0;
+    // bytes from the descriptor's start to the last row's end
+    const uint32_t a_len = 2u * p.lda * (uint32_t)(p.row_src ? p.a_rows : row_end - row0);
+    const uint32_t b_len = 2u * p.K0 * (uint32_t)min(kRowsBN, p.N - n0);
+    // where K0 ends in the middle of a step, the lanes of the step's second 64
+    // bytes get offsets past any range and so read zeros
+    // (a copy's rows are 8 q' .. + 7, q' even or odd with q: its chunk swizzle
+    // is (4 q' + lane / 16) % 8)
+    static_assert(R::nA % 2 == 0 && R::nB % 2 == 0, "parity of a copy's rows");
+    uint32_t second[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) second[q] = ((lane & 7) ^ (4 * q + (lane >> 4))) >= 4 ? gather_max_bytes : 0;
     auto copy = [&](int q, int kt, int stage) {
         uint8_t *st = lds + stage * R::stage;
+        const int seg = kt >= nk0 ? 1 : 0, k = kRowsBK * (kt - seg * nk0);  // first column of the step in its matrix
+        const uint32_t cut = k + kRowsBK > p.K0 ? ~0u : 0u;
         if (q < R::nA) {
-            copy16(a_src[q] + kt * kBK, st + (w * R::nA + q) * 1024);
+            const int ka = 2 * (k + seg * p.K0);
+            copy16_buffer(a0 + ka, a_len - ka, a_off[q] | (second[q & 1] & cut), st + (w * R::nA + q) * 1024);
         } else {
-            const char *b = reinterpret_cast<const char *>(b_src[q - R::nA]) + 2LL * kt * kBK;
-            if (kt >= nk0) b += b_next;
-            copy16(b, st + R::a_bytes + (w * R::nB + q - R::nA) * 1024);
+            copy16_buffer((seg ? b1 : b0) + 2 * k, b_len - 2 * k, b_off[q - R::nA] | (second[(q - R::nA) & 1] & cut),
+                          st + R::a_bytes + (w * R::nB + q - R::nA) * 1024);
         }
     };
 
-    // ---- fragment reads: 16-byte pieces of 64-byte rows, both operands ----
+    // ---- fragment reads of half h: B blocks, then A row blocks ----
     struct Frag {
         bf16x8 a[MI], b[NB];
     };
-    const int chunk = 16 * (gq ^ ((lane >> 2) & 3));
-    const int a_off = (wr * (BM / 2) + i16) * 64 + chunk;
-    const int b_off = R::a_bytes + (64 * wc + i16) * 64 + chunk;
-    auto read = [&](Frag &f, int r, int stage) {
-        const uint8_t *st = lds + stage * R::stage;
-        if (r < NB) f.b[r] = *reinterpret_cast<const bf16x8 *>(st + b_off + r * 1024);
-        else f.a[r - NB] = *reinterpret_cast<const bf16x8 *>(st + a_off + (r - NB) * 1024);
+    const int swz = (i16 >> 1) & 7;  // of row i16 of any 16-row block
+    const int a_row = (wr * (BM / 2) + i16) * 128, b_row = R::a_bytes + (64 * wc + i16) * 128;
+    auto read = [&](Frag &f, int r, int stage, int h) {
+        const uint8_t *st = lds + stage * R::stage + 16 * ((4 * h + gq) ^ swz);
+        if (r < NB) f.b[r] = *reinterpret_cast<const bf16x8 *>(st + b_row + r * 2048);
+        else f.a[r - NB] = *reinterpret_cast<const bf16x8 *>(st + a_row + (r - NB) * 2048);
     };
 
     f32x4 acc[MI][NB];
@@ -130,25 +202,38 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
         __builtin_amdgcn_sched_barrier(0);
     };
 
+    const int k_last = k_first + nk - 1;
     Frag fa, fb;
 #pragma unroll
     for (int t = 0; t < S; ++t)
 #pragma unroll
-        for (int q = 0; q < NC; ++q) copy(q, min(t, nk - 1), t);
+        for (int q = 0; q < NC; ++q) copy(q, min(k_first + t, k_last), t);
     wait_vm<(S - 1) * NC>();
     __builtin_amdgcn_s_barrier();
 #pragma unroll
-    for (int r = 0; r < NR; ++r) read(fa, r, 0);
+    for (int r = 0; r < NR; ++r) read(fa, r, 0, 0);
     wait_lds();
     auto kloop = [&](auto act) {
         constexpr int ACT = decltype(act)::value;
+        auto wanted = [](int r) { return ACT > 0 && (r < NB || r - NB < ACT); };
         int stage = 0;
-        auto step = [&](Frag &cur, Frag &nxt, int kt) {
+        for (int kt = k_first; kt <= k_last; ++kt) {
             const int nstage = stage + 1 == S ? 0 : stage + 1;
-            const int src = min(kt + S, nk - 1);
+            const int src = min(kt + S, k_last);
+            // first half; the second's fragments are read
+            constexpr int SA = MI - 1;
+#pragma unroll
+            for (int c = 0; c < MI; ++c) {
+#pragma unroll
+                for (int r = c * NR / SA; r < (c + 1) * NR / SA && r < NR; ++r)
+                    if (wanted(r)) read(fb, r, stage, 1);
+                mma_rows(fa, c, act);
+            }
+            wait_lds();
+            // second half; the next step's first fragments are read
             constexpr int PRE = MI >= 8 ? 2 : 1, SLOTS = MI - PRE;
 #pragma unroll
-            for (int m = 0; m < PRE; ++m) mma_rows(cur, m, act);
+            for (int m = 0; m < PRE; ++m) mma_rows(fb, m, act);
             wait_vm<(S - 2) * NC>();
             __builtin_amdgcn_s_barrier();
 #pragma unroll
@@ -157,24 +242,46 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
                 for (int q = c * NC / SLOTS; q < (c + 1) * NC / SLOTS; ++q) copy(q, src, stage);
 #pragma unroll
                 for (int r = c * NR / SLOTS; r < (c + 1) * NR / SLOTS; ++r)
-                    if (ACT > 0 && (r < NB || r - NB < ACT)) read(nxt, r, nstage);
-                mma_rows(cur, c + PRE, act);
+                    if (wanted(r)) read(fa, r, nstage, 0);
+                mma_rows(fb, c + PRE, act);
             }
             wait_lds();  // every read of the stage is done before anyone refills it
             stage = nstage;
-        };
-        int kt = 0;
-        for (; kt + 1 < nk; kt += 2) {
-            step(fa, fb, kt);
-            step(fb, fa, kt + 1);
         }
-        if (kt < nk) step(fa, fb, kt);
     };
     if (nblk == 0) kloop(std::integral_constant<int, 0>{});
     else if (MI >= 8 && nblk <= MI / 2) kloop(std::integral_constant<int, MI / 2>{});
     else kloop(std::integral_constant<int, MI>{});
 
     wait_vm<0>();  // the repeated copies of the last steps land before the LDS is used again
+    if (u.parts > 1) {
+        // leave this part's sums ([accumulator][thread] vectors); the last part
+        // to count itself adds all of them in part order
+        if (MOE_BOUNDS_FAIL(u.part_slot < kXcds * p.xcd_parts && u.part_slot >= u.part, BOUNDS_TAIL_SLOT)) return;
+        f32x4 *mine = reinterpret_cast<f32x4 *>(p.part) + (long long)u.part_slot * (MI * NB * 512);
+#pragma unroll
+        for (int i = 0; i < MI * NB; ++i) mine[i * 512 + tid] = acc[i / NB][i % NB];
+        wait_vm<0>();
+        __syncthreads();
+        int *last = reinterpret_cast<int *>(lds);
+        if (tid == 0) {
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+            *last = __hip_atomic_fetch_add(p.part_cnt + u.tail_slot, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                    u.parts - 1;
+            if (*last) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+        }
+        __syncthreads();
+        if (!*last) return;
+        const f32x4 *part0 = mine - (long long)u.part * (MI * NB * 512);
+#pragma unroll
+        for (int i = 0; i < MI * NB; ++i) acc[i / NB][i % NB] = part0[i * 512 + tid];
+        for (int q = 1; q < u.parts; ++q) {
+            part0 += MI * NB * 512;
+#pragma unroll
+            for (int i = 0; i < MI * NB; ++i) acc[i / NB][i % NB] += part0[i * 512 + tid];
+        }
+        __syncthreads();  // the flag has been read: the LDS is free
+    }
     if constexpr (!BACK) {
 #pragma unroll
         for (int m = 0; m < MI; ++m) {
@@ -294,7 +401,9 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
 template <int BM>
 hipError_t launch_rows(const RowsProblem &p, bool back, hipStream_t s) {
     const int nN = (p.N + kRowsBN - 1) / kRowsBN;
-    const long long per = ((long long)p.max_tiles * nN + kXcds - 1) / kXcds, blocks = per * kXcds;
+    // items per XCD, and the parts that the last of them may be split into
+    const long long per = ((long long)p.max_tiles * nN + kXcds - 1) / kXcds + (p.part ? p.xcd_parts : 0);
+    const long long blocks = per * kXcds;
     if (blocks <= 0) return hipSuccess;
     if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
     if (back)
@@ -310,9 +419,18 @@ hipError_t launch_rows(const RowsProblem &p, bool back, hipStream_t s) {
 // 256-row tiles once experts average 192 rows (as the forward's tiles), else 128
 int rows_gemm_bm(long long rows, int groups) { return groups > 0 && rows >= 192LL * groups ? 256 : 128; }
 
+int rows_gemm_xcd_parts(long long max_tiles, int N) {
+    const long long per = (max_tiles * ((N + rows_gemm_bn - 1) / rows_gemm_bn) + tiled::kXcds - 1) / tiled::kXcds;
+    return (int)(per * tiled::kRowsParts < tiled::kRowsXcdParts ? per * tiled::kRowsParts : tiled::kRowsXcdParts);
+}
+size_t rows_gemm_part_bytes(int bm, int xcd_parts) {
+    return sizeof(float) * (size_t)tiled::kXcds * xcd_parts * bm * rows_gemm_bn;
+}
+
 hipError_t launch_rows_gemm(const RowsProblem &p, bool back, int bm, hipStream_t s) {
     if (!p.A || !p.B0 || !p.tiles || !p.n_tiles || !p.group_tile_start || p.N < 32 || p.N % 32 || p.K0 < 32 ||
-        p.K0 % 32 || p.gk < 1 || p.lda < (p.B1 ? 2 * p.K0 : p.K0))
+        p.K0 % 32 || p.gk < 1 || p.lda < (p.B1 ? 2 * p.K0 : p.K0) ||
+        (p.row_src && (p.a_rows < 1 || 2LL * p.a_rows * p.lda > gather_max_bytes)) || (p.part && (!p.part_cnt || p.xcd_parts < 1)))
         return hipErrorInvalidValue;
     if (back ? (!p.gq || !p.gs || !p.uq || !p.us || !p.dGU || !p.Hw || p.B1) : !p.C) return hipErrorInvalidValue;
     if (bm == 256) return tiled::launch_rows<256>(p, back, s);

@@ -8,14 +8,25 @@
 //
 // A work item is one 256 x 256 tile of one expert's output; its K loop is that
 // expert's rows, 32 a step (rows past the end read zeros, so NaN or infinite
-// rows of another expert never enter). An expert without rows writes zeros.
-// 8 wavefronts in 2 x 4 (128 x 64 each), a ring of 4 stages as in
-// tiled_gemm_kernel.h. The gathered rows' token numbers are kept in LDS,
-// kWindow rows at a time, so that the ring's vector-memory count holds
-// only copies.
-// Items are handed to the XCDs in runs of 32 (one per CU) of consecutive
-// tiles of an expert, in turn: an XCD's L2 serves a run's panels, and an
-// expert with many rows is spread over the XCDs.
+// rows of another expert never enter; an expert without rows is one step of
+// zeros). 8 wavefronts in 2 x 4 (128 x 64 each), a ring of S = 4 stages.
+//
+// Persistent: one workgroup per CU walks its items with one copy ring that
+// never drains. Three positions move along the same sequence of (item, step):
+// the multiplied step; the copied one, S steps ahead, already in the next
+// item while the last steps of this one are multiplied; and, for the gathered
+// operand, a window of 16 steps whose row numbers are copied to LDS (each
+// wavefront its own rows) one window ahead of the copies. Finished tiles are
+// stored through a small staging area per wavefront while the next item's
+// copies are in flight. One workgroup per item took 7.3 us of each 23 us
+// (16-step) item for finding its rows, filling the ring and storing.
+//
+// Work order: experts by falling row count, an expert's tiles in bands of
+// kBand tile rows, column by column; consecutive runs of 32 tiles (one per CU)
+// go to the XCDs in turn, forth and back. So a run reads about 4 panels of A
+// and 8 of B through its XCD's L2 (tile rows one by one read 33: 5 % slower),
+// and workgroups differ by at most about one item's work whatever the
+// experts' row counts.
 // build-flags: -mllvm -amdgpu-mfma-vgpr-form
 #include "tiled_gemm_kernel.h"
 
@@ -26,8 +37,9 @@ MOE_BOUNDS_FILE(train_weights)
 namespace tiled {
 namespace {
 
-// what rows past an expert's end are read from
-__device__ __attribute__((aligned(16))) const uint32_t kZeroPiece[4] = {0, 0, 0, 0};
+constexpr int kBand = 4;         // tile rows per band of the work order
+constexpr int kMaxGroups = 1024;
+constexpr uint32_t kNoRow = gather_max_bytes;  // a column's offset added, it stays below 2^32
 
 struct WRing {
     static constexpr int tile = 32 * 512;  // one operand: 32 rows of 256 bf16
@@ -35,72 +47,235 @@ struct WRing {
     static constexpr int S = 4;
     static constexpr int nC = 4;           // copies per wavefront and step (2 of each operand)
     static constexpr int MI = 8, NB = 4;
-    static constexpr int kWindow = 4096;   // rows per K loop
-    static constexpr int idx = S * stage;
-    static constexpr int lds = idx + kWindow * 4;
     static constexpr int old = 64 + 8;     // epilogue staging (bf16), 16 rows a wavefront
-    static_assert(lds <= 160 * 1024 && 8 * 16 * old * 2 <= S * stage, "LDS");
+    static constexpr int stg = S * stage, stg_bytes = 16 * old * 2;
+    static constexpr int window = 16;      // steps per window of row numbers (4 rows a wavefront and step)
+    static constexpr int rows = stg + 8 * stg_bytes, rows_bytes = 4 * 4 * window;
+    // experts by falling row count: index (uint16), first row and end (int)
+    static constexpr int order = rows + 8 * 2 * rows_bytes;
+    static constexpr int range = order + 2 * kMaxGroups;
+    static constexpr int lds = range + 8 * kMaxGroups;
+    static_assert(lds <= 160 * 1024 && rows_bytes == 256 && 4 * kMaxGroups <= S * stage, "LDS");
 };
 
-template <bool F32>
-__global__ __launch_bounds__(512, 1) void weights_gemm_kernel(WeightsProblem p, int nM, int nN) {
+// n / d for 0 <= n < 2^31 as (n mul) >> shift, exact: with shift = 31 +
+// ceil(log2 d) and mul = ceil(2^shift / d), n (mul d - 2^shift) < 2^shift
+struct Divisor {
+    uint32_t mul;
+    int shift;
+    Divisor(int d) : shift(31) {
+        while ((1LL << (shift - 31)) < d) ++shift;
+        mul = (uint32_t)(((1ULL << shift) + d - 1) / d);
+    }
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (uint32_t)(((uint64_t)n * mul) >> shift); }
+};
+
+// which operand's rows are gathered
+enum Gather { GATHER_NONE, GATHER_A, GATHER_B };
+
+// one work item (all uniform)
+struct WItem {
+    int lo, hi;       // its expert's rows
+    int m0, n0;       // first row and column of the tile
+    int half, g;      // output matrix, expert
+    __device__ __forceinline__ int steps() const { return hi > lo ? (hi - lo + 31) >> 5 : 1; }
+};
+
+template <bool F32, bool ACC, Gather GATHER>
+__global__ __launch_bounds__(512, 1) void weights_gemm_kernel(WeightsProblem p, int nM, int nN, Divisor gk,
+                                                              Divisor group_tiles, Divisor band_tiles) {
     typedef WRing R;
     constexpr int S = R::S, MI = R::MI, NB = R::NB, NC = R::nC, NR = 2 * (MI + NB);
     __shared__ __attribute__((aligned(1024))) uint8_t lds[R::lds];
-    int *idx = reinterpret_cast<int *>(lds + R::idx);
-
-    // ---- this workgroup's item ----
-    const int mats = p.C1 ? 2 : 1;
-    const long long per_group = (long long)nM * nN * mats;
-    const int xcd = blockIdx.x % kXcds, slot = blockIdx.x / kXcds;
-    const long long id = ((long long)(slot / kBlocksPerXcd) * kXcds + xcd) * kBlocksPerXcd + slot % kBlocksPerXcd;
-    const int g = (int)(id / per_group);
-    if (g >= p.G) return;
-    const int t = (int)(id % per_group);
-    const int m0 = 256 * (t / (nN * mats)), nt = t % (nN * mats);
-    const int half = nt >= nN ? 1 : 0, n0 = 256 * (nt - half * nN);
-    const int lo = min(max(p.offsets[g], 0), p.M), hi = min(max(p.offsets[g + 1], lo), p.M);
-    if (lo == hi && p.accumulate) return;
+    uint16_t *order = reinterpret_cast<uint16_t *>(lds + R::order);
+    int *range = reinterpret_cast<int *>(lds + R::range);
 
     const int tid = threadIdx.x;
     const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wr = w / 4, wc = w % 4;
     const int i16 = lane & 15, gq = lane >> 4;
 
-    // ---- copies: q < 2 operand A, else B; copy q of wavefront w fills rows
-    // 2 (2 w + q % 2) + lane / 32 of the step, the lane's 16-byte chunk being
-    // the one the swizzle puts there ----
-    const uint16_t *base[NC];
-    int krow[2];
+    // ---- experts by falling row count (equal counts by index) ----
+    {
+        int *count = reinterpret_cast<int *>(lds);
+        int lo[kMaxGroups / 512], hi[kMaxGroups / 512];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int k = 2 * (2 * w + q) + (lane >> 5);
-        const int c = 8 * ((lane & 31) ^ bswz16(k));
-        krow[q] = k;
-        base[q] = p.A + min(m0 + c, p.MD - 8);
-        base[2 + q] = p.B + (long long)half * p.ND + min(n0 + c, p.ND - 8);
+        for (int i = 0; i < kMaxGroups / 512; ++i) {
+            const int g = tid + 512 * i;
+            if (g < p.G) {
+                lo[i] = min(max(p.offsets[g], 0), p.M);
+                hi[i] = min(max(p.offsets[g + 1], lo[i]), p.M);
+                count[g] = hi[i] - lo[i];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kMaxGroups / 512; ++i) {
+            const int g = tid + 512 * i;
+            if (g < p.G) {
+                const int mine = hi[i] - lo[i];
+                int rank = 0;
+                for (int o = 0; o < p.G; ++o) {
+                    const int c = count[o];
+                    rank += (c > mine) | ((c == mine) & (o < g));
+                }
+                order[rank] = (uint16_t)g;
+                range[2 * rank] = lo[i];
+                range[2 * rank + 1] = hi[i];
+            }
+        }
+        __syncthreads();
     }
-    const int32_t *src = p.a_src ? p.a_src : p.b_src;
-    int w0 = lo;  // first row of the window
-    auto copy = [&](int q, int kt, int stage) {
-        const int k = kt * 32 + krow[q & 1];
-        const bool gathered = q < 2 ? p.a_src != nullptr : p.b_src != nullptr;
-        const int r = gathered ? idx[k] : (w0 + k < hi ? w0 + k : -1);
-        const void *s = r < 0 ? (const void *)kZeroPiece
-                              : (const void *)(base[q] + (long long)r * (q < 2 ? p.lda : p.ldb));
-        copy16(s, lds + stage * R::stage + (q < 2 ? 0 : R::tile) + (2 * w + (q & 1)) * 1024);
+
+    // ---- this workgroup's items: number `slot` of every run that its XCD takes ----
+    const int mats = p.C1 ? 2 : 1, nT = nN * mats, per_group = nM * nT;
+    const int items = p.G * per_group;  // the launcher keeps it below 2^31
+    const int xcd = blockIdx.x % kXcds, slot = blockIdx.x / kXcds;
+    auto item_id = [&](int j) {
+        const int run = j * kXcds + ((j & 1) ? kXcds - 1 - xcd : xcd);
+        return (long long)run * kBlocksPerXcd + slot;
+    };
+    // item j; past the last one an item without rows (copied, never multiplied)
+    auto item_at = [&](int j) {
+        WItem it{0, 0, 0, 0, 0, 0};
+        const long long id = item_id(j);
+        if (id < items) {
+            const int e = (int)group_tiles((uint32_t)id), t = (int)id - e * per_group;
+            it.g = __builtin_amdgcn_readfirstlane((int)order[e]);
+            const int band = (int)band_tiles(t), in = t - band * kBand * nT, deep = min(kBand, nM - kBand * band);
+            static_assert(kBand == 4, "in / deep");
+            const int n = deep == 4 ? in >> 2 : deep == 3 ? (int)(((uint64_t)in * 0xaaaaaaabu) >> 33) : in >> (deep - 1);
+            it.m0 = 256 * (kBand * band + in - n * deep);
+            it.half = n >= nN ? 1 : 0;
+            it.n0 = 256 * (n - it.half * nN);
+            it.lo = __builtin_amdgcn_readfirstlane(range[2 * e]);
+            it.hi = __builtin_amdgcn_readfirstlane(range[2 * e + 1]);
+        }
+        return it;
+    };
+    if (item_id(0) >= items) return;
+
+    // ---- the copied position: copy q of an operand and wavefront w fills rows
+    // 4 w + 2 q + lane / 32 of the step, the lane's 16-byte chunk being the one
+    // the swizzle puts there. Buffer loads, whose range check gives zeros for
+    // rows past the expert's end: an operand in row order has a descriptor that
+    // starts at the step's first row and ends with the expert's last, so its
+    // copies need no address arithmetic but the scalar descriptor's; the
+    // gathered one has a descriptor of the whole matrix, and rows past the end
+    // get the offset kNoRow, past any range ----
+    WItem ci = item_at(0), cn = item_at(1);  // the item being copied, and the one after it
+    int cj = 0, ck = 0, cnk = ci.steps();
+    const uint32_t lda2 = 2u * p.lda, ldb2 = 2u * p.ldb;
+    uint32_t a_off[2], b_off[2];  // the lane's byte offset within the step (gathered: within its row)
+    const char *a_ptr, *b_ptr;    // the step's first row at the tile's first column (gathered: row 0)
+    uint32_t a_bytes, b_bytes;    // from there to the end of the step's rows (gathered: of the matrix)
+    // the scalar unit's descriptors: the rows left in the step, as a scalar
+    auto set_bytes = [&]() {
+        const uint32_t n = __builtin_amdgcn_readfirstlane(min(max(ci.hi - ci.lo - 32 * ck, 0), 32));
+        if (GATHER != GATHER_A) a_bytes = n * lda2;
+        if (GATHER != GATHER_B) b_bytes = n * ldb2;
+    };
+    auto set_item = [&]() {
+        // the lane, re-read so that this rare path's offsets do not stay live
+        int ln = lane;
+        asm volatile("" : "+v"(ln));
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int k = 4 * w + 2 * q + (ln >> 5), c = 8 * ((ln & 31) ^ bswz16(k));
+            // columns past the matrix read its last ones (never stored)
+            a_off[q] = 2 * min(c, p.MD - 8 - ci.m0) + (GATHER == GATHER_A ? 0 : k * lda2);
+            b_off[q] = 2 * min(c, p.ND - 8 - ci.n0) + (GATHER == GATHER_B ? 0 : k * ldb2);
+        }
+        a_ptr = reinterpret_cast<const char *>(p.A + ci.m0) + (GATHER == GATHER_A ? 0LL : (long long)ci.lo * lda2);
+        b_ptr = reinterpret_cast<const char *>(p.B + (long long)ci.half * p.ND + ci.n0) +
+                (GATHER == GATHER_B ? 0LL : (long long)ci.lo * ldb2);
+        if (GATHER == GATHER_A) a_bytes = (uint32_t)p.src_rows * lda2 - 2u * ci.m0;
+        if (GATHER == GATHER_B) b_bytes = (uint32_t)p.src_rows * ldb2 - 2u * ci.n0;
+    };
+    // the gathered operand's rows: byte offsets of the current window's rows
+    // (16 steps x the wavefront's 4) lie in LDS; the next window's row numbers
+    // are on their way there. wk: steps copied since they were sent for
+    const int32_t *src = GATHER == GATHER_A ? p.a_src : p.b_src;
+    int buf = 0, wk = 0;
+    uint8_t *my_rows = lds + R::rows + w * 2 * R::rows_bytes;
+    auto fetch_rows = [&](const WItem &it, int k, int b) {
+        if (GATHER == GATHER_NONE || it.hi == it.lo) return;
+        const int r = it.lo + 32 * (k + (lane >> 2)) + 4 * w + (lane & 3);
+        copy4(src + min(r, it.hi - 1), my_rows + b * R::rows_bytes);
+    };
+    auto take_rows = [&]() {
+        if (GATHER == GATHER_NONE) return;
+        uint32_t *row = reinterpret_cast<uint32_t *>(my_rows + buf * R::rows_bytes) + lane;
+        uint32_t got = gk(*row);
+        const int r = ci.lo + 32 * ((ck & -R::window) + (lane >> 2)) + 4 * w + (lane & 3);
+        if (r < ci.hi && MOE_BOUNDS_FAIL(got < (uint32_t)p.src_rows, BOUNDS_A_ROW)) got = 0;
+        *row = r < ci.hi ? got * (GATHER == GATHER_A ? lda2 : ldb2) : kNoRow;
+    };
+    uint32_t row_off[2] = {0, 0};  // of the gathered operand's two copies of the step
+    auto step_rows = [&]() {
+        if (GATHER == GATHER_NONE) return;
+        const uint32_t *row = reinterpret_cast<const uint32_t *>(my_rows + buf * R::rows_bytes) +
+                              4 * (ck & (R::window - 1)) + (lane >> 5);
+        row_off[0] = row[0];
+        row_off[1] = row[2];
+    };
+    // to the next step: at a window's end the next window becomes current and
+    // the one after it is sent for
+    auto advance = [&]() {
+        ++ck;
+        ++wk;
+        a_ptr += GATHER == GATHER_A ? 0 : 32 * lda2;
+        b_ptr += GATHER == GATHER_B ? 0 : 32 * ldb2;
+        const bool next_item = ck == cnk;
+        if (next_item || (ck & (R::window - 1)) == 0) {
+            if (GATHER != GATHER_NONE) {
+                // at least NC wk copies are newer than the window's: it has
+                // landed when no more than that are outstanding
+                if (wk >= 3) wait_vm<3 * NC>();
+                else wait_vm<0>();
+            }
+            wk = 0;
+            buf ^= 1;
+            if (next_item) {
+                ci = cn;
+                ++cj;
+                ck = 0;
+                cnk = ci.steps();
+                cn = item_at(cj + 1);
+                set_item();
+            }
+            take_rows();
+            if (ck + R::window < cnk) fetch_rows(ci, ck + R::window, buf ^ 1);
+            else fetch_rows(cn, 0, buf ^ 1);
+        }
+        set_bytes();
+        step_rows();
+    };
+    auto copy = [&](int q, int stage) {
+        const bool is_a = q < 2;
+        uint32_t off = (is_a ? a_off : b_off)[q & 1];
+        if (GATHER == (is_a ? GATHER_A : GATHER_B)) off += row_off[q & 1];
+        copy16_buffer(is_a ? a_ptr : b_ptr, is_a ? a_bytes : b_bytes, off,
+                      lds + stage * R::stage + (is_a ? 0 : R::tile) + (2 * w + (q & 1)) * 1024);
     };
 
-    // ---- fragment reads: r = 2 block + half; blocks 0..MI-1 of A, then B ----
+    // ---- fragment reads: r = 2 block + half; blocks 0..MI-1 of A, then B.
+    // The lane's K rows are 8 gq + 4 half + i16 / 4, whose chunk swizzle does
+    // not depend on the half; column block b moves the chunk index by 2 b in
+    // bits that the other terms leave to the swizzle's XOR, so its address is
+    // the lane's first address XOR 32 b ----
     struct Frag {
         bf16x8 a[MI], b[NB];
         u32x2 raw[MI + NB][2];
     };
+    const int k0 = 8 * gq + (i16 >> 2), b0 = (i16 & 3) >> 1;
+    const uint32_t a_base = k0 * 512 + 16 * ((16 * wr + b0) ^ bswz16(k0)) + 8 * (i16 & 1);
+    const uint32_t b_base = R::tile + k0 * 512 + 16 * ((8 * wc + b0) ^ bswz16(k0)) + 8 * (i16 & 1);
     auto read = [&](Frag &f, int r, int stage) {
-        const int blk = r >> 1, kh = r & 1;
-        const int k = 8 * gq + 4 * kh + (i16 >> 2);
-        const int n = (blk < MI ? 128 * wr + 16 * blk : 64 * wc + 16 * (blk - MI)) + 4 * (i16 & 3);
-        f.raw[blk][kh] = ds_tr16(lds_addr(lds + stage * R::stage + (blk < MI ? 0 : R::tile)) + k * 512 +
-                                 16 * ((n >> 3) ^ bswz16(k)) + 2 * (n & 7));
+        const int blk = r >> 1;
+        const uint32_t st = lds_addr(lds + stage * R::stage);
+        const uint32_t addr = (st + (blk < MI ? a_base : b_base)) ^ (32 * (blk < MI ? blk : blk - MI));
+        if (r & 1) f.raw[blk][1] = ds_tr16_at<2048>(addr);
+        else f.raw[blk][0] = ds_tr16_at<0>(addr);
     };
     auto land = [&](Frag &f) {
         wait_lds();
@@ -127,121 +302,169 @@ __global__ __launch_bounds__(512, 1) void weights_gemm_kernel(WeightsProblem p, 
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    for (; w0 < hi; w0 += R::kWindow) {
-        const int rows = min(hi - w0, R::kWindow), nk = (rows + 31) / 32;
-        if (src) {
-            const long long lim = p.a_src ? p.a_rows : p.b_rows;
-            for (int i = tid; i < 32 * nk; i += 512) {
-                int v = i < rows ? src[w0 + i] / p.gk : -1;
-                if (MOE_BOUNDS_FAIL(v >= -1 && (lim <= 0 || v < lim), BOUNDS_A_ROW)) v = -1;
-                idx[i] = v;
-            }
-            __syncthreads();
-        }
-        Frag fa, fb;
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-            for (int q = 0; q < NC; ++q) copy(q, min(s, nk - 1), s);
-        wait_vm<(S - 1) * NC>();
-        __builtin_amdgcn_s_barrier();
-#pragma unroll
-        for (int r = 0; r < NR; ++r) read(fa, r, 0);
-        land(fa);
-        int stage = 0;
-        auto step = [&](Frag &cur, Frag &nxt, int kt) {
-            const int nstage = stage + 1 == S ? 0 : stage + 1;
-            const int from = min(kt + S, nk - 1);
-            mma_rows(cur, 0);
-            mma_rows(cur, 1);
-            wait_vm<(S - 2) * NC>();
-            __builtin_amdgcn_s_barrier();
-            constexpr int SLOTS = MI - 2;
-#pragma unroll
-            for (int c = 0; c < SLOTS; ++c) {
-#pragma unroll
-                for (int q = c * NC / SLOTS; q < (c + 1) * NC / SLOTS; ++q) copy(q, from, stage);
-#pragma unroll
-                for (int r = c * NR / SLOTS; r < (c + 1) * NR / SLOTS; ++r) read(nxt, r, nstage);
-                mma_rows(cur, c + 2);
-            }
-            land(nxt);
-            stage = nstage;
-        };
-        int kt = 0;
-        for (; kt + 1 < nk; kt += 2) {
-            step(fa, fb, kt);
-            step(fb, fa, kt + 1);
-        }
-        if (kt < nk) step(fa, fb, kt);
-        wait_vm<0>();     // the repeated copies of the last steps have landed,
-        __syncthreads();  // and every wavefront is done with the ring and the rows' numbers
-    }
-
-    // ---- store ----
-    void *C = half ? p.C1 : p.C0;
-    const long long out0 = (long long)g * p.MD * p.ND;
-    const int c0 = n0 + 64 * wc;
-    if constexpr (F32) {
-        float *Cf = reinterpret_cast<float *>(C) + out0;
+    // ---- a finished tile: row block by row block through the wavefront's
+    // staging area, or (fp32) straight from the accumulators, which are
+    // cleared. Buffer stores: those outside the matrix get an offset past the
+    // buffer's range and are dropped by the hardware, so every wavefront
+    // issues exactly kStores of them whatever the tile ----
+    constexpr int kStores = F32 ? MI * NB : 2 * MI;
+    constexpr int kOut = 0x7fffffff;
+    auto tile_out = [&](const WItem &it) {
+        constexpr int size = F32 ? 4 : 2;
+        const long long first = (((long long)it.g * p.MD + it.m0 + 128 * wr) * p.ND + it.n0 + 64 * wc) * size;
+        char *C = reinterpret_cast<char *>(it.half ? p.C1 : p.C0) + first;
+        const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(C, 0, kOut, kBufferWord3);
+        // re-read here, so that the offsets are not kept through the K loop
+        int nd = p.ND, ln = lane;
+        asm volatile("" : "+v"(nd), "+v"(ln));
+        const int l16 = ln & 15, lq = ln >> 4;
+        const int rows = p.MD - it.m0 - 128 * wr, cols = p.ND - it.n0 - 64 * wc;
+        uint16_t *stg = reinterpret_cast<uint16_t *>(lds + R::stg + w * R::stg_bytes);
 #pragma unroll
         for (int m = 0; m < MI; ++m) {
-            const int row = m0 + 128 * wr + 16 * m + i16;
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
-                const int col = c0 + 16 * j + 4 * gq;
-                if (row >= p.MD || col >= p.ND) continue;
-                f32x4 *o = reinterpret_cast<f32x4 *>(Cf + (long long)row * p.ND + col);
+                const int row = 16 * m + l16, col = 16 * j + 4 * lq;
+                int off = (row * nd + col) * size;
+                asm volatile("" : "+v"(off));  // formed first: the choice is then no branch
+                off = (row < rows) & (col < cols) ? off : kOut;
                 f32x4 v = acc[m][j];
-                if (p.accumulate) v += *o;
-                *o = v;
-            }
-        }
-    } else {
-        uint16_t *Cb = reinterpret_cast<uint16_t *>(C) + out0;
-        uint16_t *stg = reinterpret_cast<uint16_t *>(lds) + w * 16 * R::old;
-#pragma unroll
-        for (int m = 0; m < MI; ++m) {
-#pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                const int row = m0 + 128 * wr + 16 * m + i16, col = c0 + 16 * j + 4 * gq;
-                f32x4 v = acc[m][j];
-                if (p.accumulate && row < p.MD && col < p.ND) {
-                    const u32x2 old = *reinterpret_cast<const u32x2 *>(Cb + (long long)row * p.ND + col);
-                    v += f32x4{bf16_lo(old[0]), bf16_hi(old[0]), bf16_lo(old[1]), bf16_hi(old[1])};
+                if constexpr (F32) {
+                    if (ACC && off != kOut) v += *reinterpret_cast<const f32x4 *>(C + off);
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rsrc, off, 0, 0);
+                } else {
+                    if (ACC && off != kOut) {
+                        const u32x2 old = *reinterpret_cast<const u32x2 *>(C + off);
+                        v += f32x4{bf16_lo(old[0]), bf16_hi(old[0]), bf16_lo(old[1]), bf16_hi(old[1])};
+                    }
+                    *reinterpret_cast<u32x2 *>(stg + l16 * R::old + col) =
+                        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
                 }
-                *reinterpret_cast<u32x2 *>(stg + i16 * R::old + 16 * j + 4 * gq) =
-                    u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+            }
+            if constexpr (!F32) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int piece = ln + 64 * c, r = piece >> 3, col = 8 * (piece & 7), row = 16 * m + r;
+                    const u32x4 v = *reinterpret_cast<const u32x4 *>(stg + r * R::old + col);
+                    int off = (row * nd + col) * size;
+                    asm volatile("" : "+v"(off));
+                    off = (row < rows) & (col < cols) ? off : kOut;
+                    __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, off, 0, 0);
+                }
             }
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int piece = lane + 64 * c, r = piece >> 3, col = 8 * (piece & 7);
-                const int row = m0 + 128 * wr + 16 * m + r;
-                if (row < p.MD && c0 + col < p.ND)
-                    *reinterpret_cast<u32x4 *>(Cb + (long long)row * p.ND + c0 + col) =
-                        *reinterpret_cast<const u32x4 *>(stg + r * R::old + col);
-            }
+            for (int j = 0; j < NB; ++j) acc[m][j] = f32x4{};
         }
+    };
+
+    // ---- fill the ring ----
+    Frag fa, fb;
+    set_item();
+    fetch_rows(ci, 0, 0);
+    if (R::window < cnk) fetch_rows(ci, R::window, 1);
+    else fetch_rows(cn, 0, 1);
+    if (GATHER != GATHER_NONE) wait_vm<0>();
+    take_rows();
+    set_bytes();
+    step_rows();
+#pragma unroll 1
+    for (int s = 0; s < S; ++s) {
+#pragma unroll
+        for (int q = 0; q < NC; ++q) copy(q, s);
+        advance();
     }
+    wait_vm<(S - 1) * NC>();
+    __builtin_amdgcn_s_barrier();
+#pragma unroll
+    for (int r = 0; r < NR; ++r) read(fa, r, 0);
+    land(fa);
+
+    // ---- the multiplied position ----
+    WItem mi = item_at(0), mn = item_at(1);
+    int mj = 0, left = mi.steps(), stage = 0;
+    int relax = 0;  // steps whose awaited copies are older than a finished tile's stores
+    auto step = [&](Frag &cur, Frag &nxt) {
+        const int nstage = stage + 1 == S ? 0 : stage + 1;
+        mma_rows(cur, 0);
+        mma_rows(cur, 1);
+        // the next step's copies have landed when no more than the S - 2 newer
+        // steps' (and, for S - 1 steps after a tile, its stores) are outstanding
+        if (relax > 0) {
+            --relax;
+            wait_vm<(S - 2) * NC + kStores>();
+        } else {
+            wait_vm<(S - 2) * NC>();
+        }
+        __builtin_amdgcn_s_barrier();
+        // copies and reads spread between the MFMA groups; the next copies'
+        // descriptors and row offsets formed before the last group
+        constexpr int SLOTS = MI - 2;
+#pragma unroll
+        for (int c = 0; c < SLOTS; ++c) {
+#pragma unroll
+            for (int q = c * (NC + 1) / SLOTS; q < (c + 1) * (NC + 1) / SLOTS && q < NC; ++q) copy(q, stage);
+#pragma unroll
+            for (int r = c * NR / SLOTS; r < (c + 1) * NR / SLOTS; ++r) read(nxt, r, nstage);
+            if (c == SLOTS - 1) advance();
+            mma_rows(cur, c + 2);
+        }
+        land(nxt);
+        stage = nstage;
+    };
+    for (;;) {
+        int k = left;
+        for (; k > 1; k -= 2) {
+            step(fa, fb);
+            step(fb, fa);
+        }
+        if (k > 0) {
+            step(fa, fb);
+            // once per item: the fragment sets change roles by a copy
+#pragma unroll
+            for (int m = 0; m < MI; ++m) fa.a[m] = fb.a[m];
+#pragma unroll
+            for (int j = 0; j < NB; ++j) fa.b[j] = fb.b[j];
+        }
+        if (!ACC || mi.lo < mi.hi) {
+            tile_out(mi);
+            relax = ACC ? 0 : S - 1;
+        }
+        ++mj;
+        if (item_id(mj) >= items) break;
+        mi = mn;
+        left = mi.steps();
+        mn = item_at(mj + 1);
+    }
+    wait_vm<0>();  // the copies past the last item land before the workgroup ends
 }
 
 }  // namespace
 }  // namespace tiled
 
 hipError_t launch_weights_gemm(const WeightsProblem &p, hipStream_t s) {
-    if (!p.A || !p.B || !p.offsets || !p.C0 || p.G < 1 || p.M < 0 || p.MD < 32 || p.MD % 32 || p.ND < 32 ||
-        p.ND % 32 || p.gk < 1 || (p.a_src && p.b_src) || p.lda < p.MD || p.ldb < (p.C1 ? 2 : 1) * p.ND ||
-        (p.c_dt != MOE_F32 && p.c_dt != MOE_BF16))
+    using namespace tiled;
+    if (!p.A || !p.B || !p.offsets || !p.C0 || p.G < 1 || p.G > kMaxGroups || p.M < 0 || p.MD < 32 || p.MD % 32 ||
+        p.ND < 32 || p.ND % 32 || p.gk < 1 || p.gk > 64 || (p.a_src && p.b_src) || p.lda < p.MD ||
+        p.ldb < (p.C1 ? 2 : 1) * p.ND ||
+        ((p.a_src || p.b_src) && (p.src_rows < 1 || 2LL * p.src_rows * (p.a_src ? p.lda : p.ldb) > gather_max_bytes)) || (p.c_dt != MOE_F32 && p.c_dt != MOE_BF16))
         return hipErrorInvalidValue;
     const int nM = (p.MD + 255) / 256, nN = (p.ND + 255) / 256;
     const long long items = (long long)p.G * nM * nN * (p.C1 ? 2 : 1);
-    constexpr long long run = tiled::kXcds * tiled::kBlocksPerXcd;
-    const long long blocks = (items + run - 1) / run * run;
-    if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-    if (p.c_dt == MOE_F32)
-        hipLaunchKernelGGL(tiled::weights_gemm_kernel<true>, dim3((unsigned)blocks), dim3(512), 0, s, p, nM, nN);
-    else
-        hipLaunchKernelGGL(tiled::weights_gemm_kernel<false>, dim3((unsigned)blocks), dim3(512), 0, s, p, nM, nN);
+    if (items > 0x7fffffffLL) return hipErrorInvalidValue;
+    const int nT = nN * (p.C1 ? 2 : 1);
+    auto launch = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(kXcds * kBlocksPerXcd), dim3(512), 0, s, p, nM, nN, Divisor(p.gk),
+                           Divisor(nM * nT), Divisor(kBand * nT));
+    };
+    const bool f32 = p.c_dt == MOE_F32;
+#define MOE_WEIGHTS(G)                                                                                           \
+    (f32 ? (p.accumulate ? launch(weights_gemm_kernel<true, true, G>) : launch(weights_gemm_kernel<true, false, G>)) \
+         : (p.accumulate ? launch(weights_gemm_kernel<false, true, G>) : launch(weights_gemm_kernel<false, false, G>)))
+    if (p.a_src) MOE_WEIGHTS(GATHER_A);
+    else if (p.b_src) MOE_WEIGHTS(GATHER_B);
+    else MOE_WEIGHTS(GATHER_NONE);
+#undef MOE_WEIGHTS
     return hipGetLastError();
 }
 
