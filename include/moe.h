@@ -409,7 +409,8 @@ typedef struct moe_ffn_checkpoint {
  * one dense FFN: G = 1, offsets {0, T}). offsets [G+1]: row counts per group,
  * offsets[G] <= M; rows from offsets[G] on are neither read nor written
  * (Yp, gq, gs, uq, us). dt: BF16 (X, weights and Yp). H, F multiples of 32;
- * k <= 64. Tensors 16-byte aligned. T == 0 returns MOE_OK.
+ * G <= 1024; k <= 64; the token matrix (T*H values) below 4 GiB. Tensors
+ * 16-byte aligned. T == 0 returns MOE_OK.
  * Workspace: moe_ffn_train_forward_workspace_bytes bytes. */
 size_t moe_ffn_train_forward_workspace_bytes(int T, int k, int G, int H, int F);
 moe_status moe_ffn_train_forward(const void *X, const int32_t *row_src, int k, int T, const int32_t *offsets, int G,

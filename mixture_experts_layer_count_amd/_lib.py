@@ -7,6 +7,7 @@ built (python -m mixture_experts_layer_count_amd.build); there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -567,35 +568,54 @@ class _CheckpointPtrs(ctypes.Structure):
     _fields_ = [(n, _P) for n in FFNCheckpoint._fields]
 
 
-def _want(t, name, shape, dtype, like=None):
-    """One operand: a dense device tensor of that shape and dtype (on like's device)."""
+def _want(t, name, shape, dtype, device=None) -> int:
+    """The address of one operand: a dense device tensor of that shape and dtype
+    (on `device`)."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous device tensor")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, the call runs on {like.device}")
-    return t
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
+    return t.data_ptr()
 
 
 def _call(fn: str, device, *args) -> None:
-    """A libmoe call on the current stream of `device`."""
-    if device.index == torch.cuda.current_device():
-        _check(fn, getattr(lib(), fn)(*args, _stream()))
+    """A libmoe call on the current stream of `device`. (The stream's handle and
+    the current device straight from torch's C module: the wrapped forms took
+    6 us of a 16 us call.)"""
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
+    if device.index == torch._C._cuda_getDevice():
+        status = getattr(lib(), fn)(*args, stream)
     else:
         with torch.cuda.device(device):
-            _check(fn, getattr(lib(), fn)(*args, _stream()))
+            status = getattr(lib(), fn)(*args, stream)
+    if status != MOE_OK:
+        raise MoEError(fn, status)
 
 
-def _seqs(seq_offsets, like) -> int:
+@functools.lru_cache(maxsize=256)
+def _ws_bytes(fn: str, *sizes: int) -> int:
+    """The workspace of a call (a function of its sizes alone)."""
+    return getattr(lib(), fn + "_workspace_bytes")(*sizes)
+
+
+def _new(shape, dtype, device):
+    """An output or workspace and its address."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    return t, t.data_ptr()
+
+
+def _seqs(seq_offsets, device):
+    """(B, address) of optional sequence offsets."""
     if seq_offsets is None:
-        return 1
+        return 1, None
     if seq_offsets.dim() != 1 or seq_offsets.numel() < 2:
         raise ValueError("seq_offsets must be [B + 1] with B >= 1")
-    _want(seq_offsets, "seq_offsets", seq_offsets.shape, torch.int32, like)
-    return seq_offsets.numel() - 1
+    n = seq_offsets.numel()
+    return n - 1, _want(seq_offsets, "seq_offsets", (n,), torch.int32, device)
 
 
 def balance_loss(logits, topk_idx, alpha: float, beta: float = 0.0, seq_offsets=None):
@@ -604,17 +624,16 @@ def balance_loss(logits, topk_idx, alpha: float, beta: float = 0.0, seq_offsets=
     tokens into sequences (None: one). See moe_balance_loss."""
     T, E = logits.shape
     k = topk_idx.shape[1]
-    _want(logits, "logits", (T, E), torch.float32)
-    _want(topk_idx, "topk_idx", (T, k), torch.int32, logits)
-    B = _seqs(seq_offsets, logits)
     dev = logits.device
-    loss = torch.empty(2, dtype=torch.float32, device=dev)
-    counts = torch.empty(E, dtype=torch.int32, device=dev)
-    seq_counts = torch.empty((B, E), dtype=torch.int32, device=dev)
-    nbytes = lib().moe_balance_loss_workspace_bytes(T, E, B)
-    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-    _call("moe_balance_loss", dev, _ptr(logits), _ptr(topk_idx), T, E, k, _ptr(seq_offsets), B, alpha, beta,
-          _ptr(loss), _ptr(counts), _ptr(seq_counts), _ptr(ws), nbytes)
+    zp = _want(logits, "logits", (T, E), torch.float32)
+    ip = _want(topk_idx, "topk_idx", (T, k), torch.int32, dev)
+    B, sp = _seqs(seq_offsets, dev)
+    loss, lp = _new(2, torch.float32, dev)
+    counts, cp = _new(E, torch.int32, dev)
+    seq_counts, qp = _new((B, E), torch.int32, dev)
+    nbytes = _ws_bytes("moe_balance_loss", T, E, B)
+    ws, wp = _new(nbytes, torch.uint8, dev)
+    _call("moe_balance_loss", dev, zp, ip, T, E, k, sp, B, alpha, beta, lp, cp, qp, wp, nbytes)
     return loss, counts, seq_counts
 
 
@@ -626,21 +645,22 @@ def route_backward(logits, topk_idx, topk_w=None, dtopk_w=None, seq_counts=None,
     moe_route_backward."""
     T, E = logits.shape
     k = topk_idx.shape[1]
-    _want(logits, "logits", (T, E), torch.float32)
-    _want(topk_idx, "topk_idx", (T, k), torch.int32, logits)
-    B = _seqs(seq_offsets, logits)
+    dev = logits.device
+    zp = _want(logits, "logits", (T, E), torch.float32)
+    ip = _want(topk_idx, "topk_idx", (T, k), torch.int32, dev)
+    B, sp = _seqs(seq_offsets, dev)
+    tp = gp = qp = up = None
     if dtopk_w is not None:
         if topk_w is None:
             raise ValueError("dtopk_w needs topk_w")
-        _want(topk_w, "topk_w", (T, k), torch.float32, logits)
-        _want(dtopk_w, "dtopk_w", (T, k), torch.float32, logits)
+        tp = _want(topk_w, "topk_w", (T, k), torch.float32, dev)
+        gp = _want(dtopk_w, "dtopk_w", (T, k), torch.float32, dev)
     if seq_counts is not None:
-        _want(seq_counts, "seq_counts", (B, E), torch.int32, logits)
+        qp = _want(seq_counts, "seq_counts", (B, E), torch.int32, dev)
     if dloss is not None:
-        _want(dloss, "dloss", (2,), torch.float32, logits)
-    d = torch.empty_like(logits)
-    _call("moe_route_backward", logits.device, _ptr(logits), _ptr(topk_idx), _ptr(topk_w), _ptr(dtopk_w), T, E, k,
-          _ptr(seq_offsets), B, _ptr(seq_counts), alpha, beta, _ptr(dloss), _ptr(d))
+        up = _want(dloss, "dloss", (2,), torch.float32, dev)
+    d, dp = _new((T, E), torch.float32, dev)
+    _call("moe_route_backward", dev, zp, ip, tp, gp, T, E, k, sp, B, qp, alpha, beta, up, dp)
     return d
 
 
@@ -648,16 +668,19 @@ def checkpoint_pack(X, Q=None, S=None):
     """E4M3 codes Q [R,C] and E8M0 scale bytes S [R,C/32] (uint8) of the bf16 or
     f32 rows X [R,C] (rows may be strided). See moe_checkpoint_pack."""
     R, C = X.shape
+    dev = X.device
     if not X.is_cuda or (C > 1 and X.stride(1) != 1):
         raise ValueError("X must be a device tensor with contiguous rows")
     ldx = X.stride(0) if R > 1 else C
     if Q is None:
-        Q = torch.empty((R, C), dtype=torch.uint8, device=X.device)
+        Q, qp = _new((R, C), torch.uint8, dev)
+    else:
+        qp = _want(Q, "Q", (R, C), torch.uint8, dev)
     if S is None:
-        S = torch.empty((R, C // 32), dtype=torch.uint8, device=X.device)
-    _want(Q, "Q", (R, C), torch.uint8, X)
-    _want(S, "S", (R, C // 32), torch.uint8, X)
-    _call("moe_checkpoint_pack", X.device, _ptr(X), act_dtype(X), ldx, R, C, _ptr(Q), _ptr(S))
+        S, sp = _new((R, C // 32), torch.uint8, dev)
+    else:
+        sp = _want(S, "S", (R, C // 32), torch.uint8, dev)
+    _call("moe_checkpoint_pack", dev, X.data_ptr(), act_dtype(X), ldx, R, C, qp, sp)
     return Q, S
 
 
@@ -665,24 +688,30 @@ def checkpoint_unpack(Q, S, dtype=torch.bfloat16):
     """The values [R,C] that checkpoint_pack's codes and scales stand for, in
     bfloat16 or float32 (exact in both)."""
     R, C = Q.shape
-    _want(Q, "Q", (R, C), torch.uint8)
-    _want(S, "S", (R, C // 32), torch.uint8, Q)
-    Y = torch.empty((R, C), dtype=dtype, device=Q.device)
-    _call("moe_checkpoint_unpack", Q.device, _ptr(Q), _ptr(S), R, C, act_dtype(Y), _ptr(Y))
+    dev = Q.device
+    qp = _want(Q, "Q", (R, C), torch.uint8)
+    sp = _want(S, "S", (R, C // 32), torch.uint8, dev)
+    Y, yp = _new((R, C), dtype, dev)
+    _call("moe_checkpoint_unpack", dev, qp, sp, R, C, act_dtype(Y), yp)
     return Y
 
 
-def _train_dims(T, offsets, W1, W3, W2, row_src, k, like):
+def _train_args(T, offsets, W1, W3, W2, row_src, k, dev):
+    """Dimensions and addresses that the FFN's two passes share."""
     G, H, F = W1.shape
-    for t, n, s in ((W1, "W1", (G, H, F)), (W3, "W3", (G, H, F)), (W2, "W2", (G, F, H))):
-        _want(t, n, s, torch.bfloat16, like)
-    _want(offsets, "offsets", (G + 1,), torch.int32, like)
-    if row_src is None:
-        if k != 1:
-            raise ValueError("k > 1 needs row_src")
-    else:
-        _want(row_src, "row_src", (T * k,), torch.int32, like)
-    return G, H, F
+    w = [_want(t, n, s, torch.bfloat16, dev)
+         for t, n, s in ((W1, "W1", (G, H, F)), (W3, "W3", (G, H, F)), (W2, "W2", (G, F, H)))]
+    op = _want(offsets, "offsets", (G + 1,), torch.int32, dev)
+    rp = None
+    if row_src is not None:
+        rp = _want(row_src, "row_src", (T * k,), torch.int32, dev)
+    elif k != 1:
+        raise ValueError("k > 1 needs row_src")
+    return G, H, F, w, op, rp
+
+
+def _ckpt_shapes(T, M, H, F):
+    return (T, H), (T, H // 32), (M, F), (M, F // 32), (M, F), (M, F // 32)
 
 
 def ffn_train_forward(X, offsets, W1, W3, W2, row_src=None, k: int = 1):
@@ -691,27 +720,28 @@ def ffn_train_forward(X, offsets, W1, W3, W2, row_src=None, k: int = 1):
     what ffn_train_backward needs of it. See moe_ffn_train_forward."""
     T = X.shape[0]
     dev = X.device
-    G, H, F = _train_dims(T, offsets, W1, W3, W2, row_src, k, X)
-    _want(X, "X", (T, H), torch.bfloat16)
+    G, H, F, w, op, rp = _train_args(T, offsets, W1, W3, W2, row_src, k, dev)
+    xp = _want(X, "X", (T, H), torch.bfloat16)
     M = T * k
-    Yp = torch.empty((M, H), dtype=X.dtype, device=dev)
-    c = FFNCheckpoint(*(torch.empty(s, dtype=torch.uint8, device=dev) for s in (
-        (T, H), (T, H // 32), (M, F), (M, F // 32), (M, F), (M, F // 32))))
+    Yp, yp = _new((M, H), torch.bfloat16, dev)
+    c = FFNCheckpoint(*(torch.empty(s, dtype=torch.uint8, device=dev) for s in _ckpt_shapes(T, M, H, F)))
     ptrs = _CheckpointPtrs(*(t.data_ptr() for t in c))
-    nbytes = lib().moe_ffn_train_forward_workspace_bytes(T, k, G, H, F)
-    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-    _call("moe_ffn_train_forward", dev, _ptr(X), _ptr(row_src), k, T, _ptr(offsets), G, H, F, _ptr(W1), _ptr(W3),
-          _ptr(W2), MOE_BF16, _ptr(Yp), ctypes.byref(ptrs), _ptr(ws), nbytes)
+    nbytes = _ws_bytes("moe_ffn_train_forward", T, k, G, H, F)
+    ws, wp = _new(nbytes, torch.uint8, dev)
+    _call("moe_ffn_train_forward", dev, xp, rp, k, T, op, G, H, F, *w, MOE_BF16, yp, ctypes.byref(ptrs), wp, nbytes)
     return Yp, c
+
+
+_DW_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 
 def ffn_train_backward(dY, ckpt, offsets, W1, W3, W2, topk_w=None, row_src=None, assign_row=None, dX_add=None,
                        need=("dX", "dtopk_w", "dW"), dW=None, dw_dtype=torch.bfloat16):
     """-> (dX [T,H] bf16, dtopk_w [T,k] f32, dW1, dW3 [G,H,F], dW2 [G,F,H]) of
     ffn_train_forward followed by combine, from the gradient dY [T,H] at
-    combine's output. k is topk_w's (1 without it). `need` names what to
-    compute (the others are None). `dW`: (dW1, dW3, dW2) buffers, bf16 or f32,
-    that the weight gradients are added to; without it new ones in dw_dtype.
+    combine's output (topk_w None: weights of 1). `need` names what to compute
+    (the others are None). `dW`: (dW1, dW3, dW2) buffers, bf16 or f32, that the
+    weight gradients are added to; without it new ones in dw_dtype.
     See moe_ffn_train_backward."""
     T = dY.shape[0]
     dev = dY.device
@@ -723,46 +753,46 @@ def ffn_train_backward(dY, ckpt, offsets, W1, W3, W2, topk_w=None, row_src=None,
             raise ValueError("row_src must hold T*k rows")
         else:
             k = row_src.numel() // T
-    G, H, F = _train_dims(T, offsets, W1, W3, W2, row_src, k, dY)
+    G, H, F, w, op, rp = _train_args(T, offsets, W1, W3, W2, row_src, k, dev)
     M = T * k
-    _want(dY, "dY", (T, H), torch.bfloat16)
-    for t, n, s in zip(ckpt, FFNCheckpoint._fields,
-                       ((T, H), (T, H // 32), (M, F), (M, F // 32), (M, F), (M, F // 32))):
-        _want(t, n, s, torch.uint8, dY)
+    gp = _want(dY, "dY", (T, H), torch.bfloat16)
+    ptrs = _CheckpointPtrs(*(_want(t, n, s, torch.uint8, dev)
+                             for t, n, s in zip(ckpt, FFNCheckpoint._fields, _ckpt_shapes(T, M, H, F))))
+    ap = tp = ep = xp = up = None
     if (assign_row is None) != (row_src is None):
         raise ValueError("row_src and assign_row come together")
     if assign_row is not None:
-        _want(assign_row, "assign_row", (M,), torch.int32, dY)
+        ap = _want(assign_row, "assign_row", (M,), torch.int32, dev)
     if topk_w is not None:
-        _want(topk_w, "topk_w", (T, k), torch.float32, dY)
+        tp = _want(topk_w, "topk_w", (T, k), torch.float32, dev)
     if set(need) - {"dX", "dtopk_w", "dW"}:
         raise ValueError("need names dX, dtopk_w and dW")
-    dX = torch.empty_like(dY) if "dX" in need else None
+    dX = dtopk_w = None
+    if "dX" in need:
+        dX, xp = _new((T, H), torch.bfloat16, dev)
     if dX_add is not None:
         if dX is None:
             raise ValueError("dX_add needs dX")
-        _want(dX_add, "dX_add", (T, H), torch.bfloat16, dY)
-    dtopk_w = torch.empty((T, k), dtype=torch.float32, device=dev) if "dtopk_w" in need else None
-    dW1 = dW3 = dW2 = None
+        ep = _want(dX_add, "dX_add", (T, H), torch.bfloat16, dev)
+    if "dtopk_w" in need:
+        dtopk_w, up = _new((T, k), torch.float32, dev)
+    grads, wg = (None, None, None), (None, None, None)
     if dW is not None:
         if "dW" not in need:
             raise ValueError("dW buffers need dW")
-        dW1, dW3, dW2 = dW
-        dw_dtype = dW1.dtype
-        for t, n, s in ((dW1, "dW1", W1.shape), (dW3, "dW3", W3.shape), (dW2, "dW2", W2.shape)):
-            _want(t, n, s, dw_dtype, dY)
-    elif "dW" in need:
-        dW1, dW3, dW2 = (torch.empty(w.shape, dtype=dw_dtype, device=dev) for w in (W1, W3, W2))
-    wdt = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}.get(dw_dtype)
-    if wdt is None:
+        grads = tuple(dW)
+        dw_dtype = grads[0].dtype
+    if dw_dtype not in _DW_DTYPES:
         raise TypeError(f"weight gradients must be float32 or bfloat16, got {dw_dtype}")
-    ptrs = _CheckpointPtrs(*(t.data_ptr() for t in ckpt))
-    nbytes = lib().moe_ffn_train_backward_workspace_bytes(T, k, G, H, F)
-    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-    _call("moe_ffn_train_backward", dev, _ptr(dY), _ptr(topk_w), _ptr(row_src), _ptr(assign_row), k, T, _ptr(offsets),
-          G, H, F, _ptr(W1), _ptr(W3), _ptr(W2), MOE_BF16, ctypes.byref(ptrs), _ptr(dX_add), _ptr(dX), _ptr(dtopk_w),
-          _ptr(dW1), _ptr(dW3), _ptr(dW2), wdt, int(dW is not None), _ptr(ws), nbytes)
-    return dX, dtopk_w, dW1, dW3, dW2
+    if dW is not None:
+        wg = [_want(t, n, s.shape, dw_dtype, dev) for t, n, s in zip(grads, ("dW1", "dW3", "dW2"), (W1, W3, W2))]
+    elif "dW" in need:
+        grads, wg = zip(*(_new(s.shape, dw_dtype, dev) for s in (W1, W3, W2)))
+    nbytes = _ws_bytes("moe_ffn_train_backward", T, k, G, H, F)
+    ws, wp = _new(nbytes, torch.uint8, dev)
+    _call("moe_ffn_train_backward", dev, gp, tp, rp, ap, k, T, op, G, H, F, *w, MOE_BF16, ctypes.byref(ptrs), ep, xp,
+          up, *wg, _DW_DTYPES[dw_dtype], int(dW is not None), wp, nbytes)
+    return dX, dtopk_w, *grads
 
 
 # ---------------------------------------------------------------------------

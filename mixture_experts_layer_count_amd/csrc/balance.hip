@@ -35,6 +35,39 @@
 namespace moe {
 namespace {
 
+// x combined over the LPT lanes of a token (a power of two), in every lane of
+// them: DPP permutations within 16 lanes, then row and half swaps. All VALU:
+// with cross-lane LDS permutations these reductions were most of the kernels'
+// time.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, false));
+}
+template <int LPT, class Op>
+__device__ __forceinline__ float combine_lanes(float x, Op op) {
+    if constexpr (LPT >= 2) x = op(x, dpp<0xB1>(x));    // quad_perm [1,0,3,2]
+    if constexpr (LPT >= 4) x = op(x, dpp<0x4E>(x));    // quad_perm [2,3,0,1]
+    if constexpr (LPT >= 8) x = op(x, dpp<0x141>(x));   // row_half_mirror
+    if constexpr (LPT >= 16) x = op(x, dpp<0x140>(x));  // row_mirror
+    if constexpr (LPT >= 32) {
+        const auto v = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = op(__uint_as_float(v[0]), __uint_as_float(v[1]));
+    }
+    if constexpr (LPT >= 64) {
+        const auto v = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = op(__uint_as_float(v[0]), __uint_as_float(v[1]));
+    }
+    return x;
+}
+template <int LPT>
+__device__ __forceinline__ float sum_lanes(float x) {
+    return combine_lanes<LPT>(x, [](float p, float q) { return p + q; });
+}
+template <int LPT>
+__device__ __forceinline__ float max_lanes(float x) {
+    return combine_lanes<LPT>(x, [](float p, float q) { return fmaxf(p, q); });
+}
+
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 
@@ -91,8 +124,7 @@ struct Row {
         for (int i = 0; i < NI; ++i)
 #pragma unroll
             for (int c = 0; c < V; ++c) top = fmaxf(top, x[i][c]);
-#pragma unroll
-        for (int d = LPT / 2; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+        top = max_lanes<LPT>(top);
         // a NaN logit is ignored by fmaxf and makes the sum, and so the row, NaN
         const float base = top == -INFINITY ? 0.0f : top;
         float sum = 0.0f;
@@ -100,11 +132,12 @@ struct Row {
         for (int i = 0; i < NI; ++i)
 #pragma unroll
             for (int c = 0; c < V; ++c) {
-                x[i][c] = expf(x[i][c] - base);
+                // the hardware's exp2: p's relative error is about 2^-24 times
+                // 2 + the logit's distance from the largest
+                x[i][c] = __builtin_amdgcn_exp2f(1.4426950408889634f * (x[i][c] - base));
                 sum += x[i][c];
             }
-#pragma unroll
-        for (int d = LPT / 2; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
+        sum = sum_lanes<LPT>(sum);
         const bool empty = sum == 0.0f;
         const float inv = empty ? 0.0f : 1.0f / sum;
 #pragma unroll
@@ -117,14 +150,17 @@ struct Row {
 
 template <int V, int NI, int LPT>
 __global__ __launch_bounds__(kThreads) void balance_sums_kernel(BalanceArgs a, float *partP, int32_t *partC,
-                                                                float *partZ, int32_t *done) {
+                                                                float *partZ, int32_t *done, int32_t *counts) {
     typedef Row<V, NI, LPT> R;
     __shared__ float sP[kWaves][1024];
     __shared__ int32_t sC[1024];
     __shared__ float sZ[kWaves];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int li = lane % LPT, sub = lane / LPT;
-    if (blockIdx.x == 0 && tid == 0) *done = 0;
+    if (blockIdx.x == 0) {  // for the second kernel
+        if (tid == 0) *done = 0;
+        for (int e = tid; e < a.E; e += kThreads) counts[e] = 0;
+    }
     const int t0 = blockIdx.x * a.chunk, t1 = min(t0 + a.chunk, a.T);
     for (int b = first_seq(a, t0); b < a.B; ++b) {
         int lo, hi;
@@ -210,9 +246,25 @@ __global__ __launch_bounds__(kFinalThreads) void balance_final_kernel(BalanceArg
     float p = 0.0f;
     int c = 0;
     if (e < a.E)
-        for (int x = x0 + w; x <= x1; x += NW) {
-            p += partP[((long long)x + b) * a.E + e];
-            c += partC[((long long)x + b) * a.E + e];
+        for (int x = x0 + w; x <= x1; x += 4 * NW) {
+            float pv[4];
+            int cv[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const bool in = x + q * NW <= x1;
+                const long long at = ((long long)(in ? x + q * NW : x) + b) * a.E + e;
+                pv[q] = partP[at];
+                cv[q] = partC[at];
+                if (!in) {
+                    pv[q] = 0.0f;
+                    cv[q] = 0;
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                p += pv[q];
+                c += cv[q];
+            }
         }
     sP[w][lane] = p;
     sC[w][lane] = c;
@@ -223,40 +275,35 @@ __global__ __launch_bounds__(kFinalThreads) void balance_final_kernel(BalanceArg
             p += sP[q][lane];
             c += sC[q][lane];
         }
-        if (e < a.E) seq_counts[(long long)b * a.E + e] = c;
+        if (e < a.E) {
+            seq_counts[(long long)b * a.E + e] = c;
+            if (c) atomicAdd(counts + e, c);
+        }
         const float n = (float)(hi - lo);
         // f_b[e] P_b[e], the E experts of this slice
         float v = (e < a.E && hi > lo) ? ((float)c * (float)a.E / ((float)a.k * n)) * (p / n) : 0.0f;
-#pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+        v = sum_lanes<64>(v);
         // the z sums of the sequence's chunks (slice 0)
         float z = 0.0f;
         if (blockIdx.x == 0) {
             for (int x = x0 + lane; x <= x1; x += 64) z += partZ[(long long)x + b];
-#pragma unroll
-            for (int d = 32; d >= 1; d >>= 1) z += __shfl_xor(z, d);
+            z = sum_lanes<64>(z);
         }
+        // the partial losses and the count of finished blocks go past the L2 of
+        // this XCD (device-scope accesses), the former complete before the
+        // latter: no cache needs to be written back or dropped
         if (lane == 0) {
-            part_loss[2 * ((long long)b * nsl + blockIdx.x)] = v;
-            part_loss[2 * ((long long)b * nsl + blockIdx.x) + 1] = z;
+            float *mine = part_loss + 2 * ((long long)b * nsl + blockIdx.x);
+            __hip_atomic_store(mine, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_store(mine + 1, z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            last = __hip_atomic_fetch_add(done, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                   (int)(gridDim.x * gridDim.y) - 1;
         }
-    }
-    // this block's counts and partial losses become visible beyond its L2
-    // before it is counted
-    __syncthreads();
-    if (tid == 0) {
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-        last = __hip_atomic_fetch_add(done, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-               (int)(gridDim.x * gridDim.y) - 1;
-        if (last) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
     }
     __syncthreads();
     if (!last) return;
-    for (int x = tid; x < a.E; x += kFinalThreads) {
-        int s = 0;
-        for (int q = 0; q < a.B; ++q) s += seq_counts[(long long)q * a.E + x];
-        counts[x] = s;
-    }
     if (w == 0) {
         // over sequences in 64 bits: they may be many
         double v = 0.0, z = 0.0;
@@ -269,8 +316,8 @@ __global__ __launch_bounds__(kFinalThreads) void balance_final_kernel(BalanceArg
             live += qh > ql;
         }
         for (long long q = lane; q < (long long)a.B * nsl; q += 64) {
-            v += part_loss[2 * q];
-            z += part_loss[2 * q + 1];
+            v += __hip_atomic_load(part_loss + 2 * q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            z += __hip_atomic_load(part_loss + 2 * q + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
 #pragma unroll
         for (int d = 32; d >= 1; d >>= 1) {
@@ -298,6 +345,7 @@ template <int V, int NI, int LPT>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(BalanceArgs a, RouteBackArgs g) {
     typedef Row<V, NI, LPT> R;
     constexpr int KQ = V * NI < 4 ? V * NI : 4;  // picks per lane: k <= min(E, 64) <= KQ LPT
+    __shared__ __attribute__((aligned(16))) float rows[kWaves][64 * NI * V];
     __shared__ int s_live, s_n;
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int li = lane % LPT, sub = lane / LPT;
@@ -359,16 +407,29 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(BalanceArgs a,
             const bool ok = t < end;
             const long long row = ok ? t : pos;
             R r;
+            int pick[KQ];
+            float wv[KQ], dv[KQ];
+            if (in_seq) r.load(a.logits + row * a.E, a.E, li, ok);
+            if (g.dw) {
+                // lane li holds picks li, li + LPT, ..
+#pragma unroll
+                for (int q = 0; q < KQ; ++q) {
+                    const int j = li + q * LPT;
+                    const bool in = ok && j < a.k;
+                    const long long at = row * a.k + (in ? j : 0);
+                    pick[q] = in ? a.idx[at] : -1;
+                    wv[q] = in ? g.w[at] : 0.0f;
+                    dv[q] = in ? g.dw[at] : 0.0f;
+                }
+            }
             if (in_seq) {
-                r.load(a.logits + row * a.E, a.E, li, ok);
                 const float lse = r.softmax();
                 float dot = 0.0f;
 #pragma unroll
                 for (int i = 0; i < NI; ++i)
 #pragma unroll
                     for (int c = 0; c < V; ++c) dot = fmaf(r.x[i][c], f[i][c], dot);
-#pragma unroll
-                for (int d = LPT / 2; d >= 1; d >>= 1) dot += __shfl_xor(dot, d);
+                dot = sum_lanes<LPT>(dot);
                 const float base = zc * lse - dot;
 #pragma unroll
                 for (int i = 0; i < NI; ++i)
@@ -381,38 +442,29 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(BalanceArgs a,
                     for (int c = 0; c < V; ++c) r.x[i][c] = 0.0f;
             }
             if (g.dw) {
-                // lane li holds picks li, li + LPT, ..
-                int pick[KQ];
-                float delta[KQ], wv[KQ], dot = 0.0f;
+                // w_j (dw_j - sum w dw) is added at its expert in an LDS copy of
+                // the row (comparing every pick with every lane's experts in
+                // registers took 8 us more of 54, 256 experts). Picks of one
+                // expert are added in the order of their lanes
+                float dot = 0.0f;
 #pragma unroll
-                for (int q = 0; q < KQ; ++q) {
-                    const int j = li + q * LPT;
-                    pick[q] = -1;
-                    wv[q] = delta[q] = 0.0f;
-                    if (j < a.k) {
-                        pick[q] = a.idx[row * a.k + j];
-                        wv[q] = g.w[row * a.k + j];
-                        delta[q] = g.dw[row * a.k + j];
-                        dot = fmaf(wv[q], delta[q], dot);
-                    }
-                }
+                for (int q = 0; q < KQ; ++q) dot = fmaf(wv[q], dv[q], dot);
+                dot = sum_lanes<LPT>(dot);
+                float *mine = rows[w] + sub * (LPT * NI * V);
 #pragma unroll
-                for (int d = LPT / 2; d >= 1; d >>= 1) dot += __shfl_xor(dot, d);
+                for (int i = 0; i < NI; ++i)
 #pragma unroll
-                for (int q = 0; q < KQ; ++q) delta[q] = wv[q] * (delta[q] - dot);
+                    for (int c = 0; c < V; ++c) mine[R::expert(i, li) + c] = r.x[i][c];
+                wave_lds_sync();
 #pragma unroll
-                for (int q = 0; q < KQ; ++q) {
-                    const int m = min(LPT, a.k - q * LPT);
-                    for (int j = 0; j < m; ++j) {
-                        const int e = __shfl(pick[q], j, LPT);
-                        const float v = __shfl(delta[q], j, LPT);
+                for (int q = 0; q < KQ; ++q)
+                    if (pick[q] >= 0 && pick[q] < a.E) atomicAdd(mine + pick[q], wv[q] * (dv[q] - dot));
+                wave_lds_sync();
 #pragma unroll
-                        for (int i = 0; i < NI; ++i)
+                for (int i = 0; i < NI; ++i)
 #pragma unroll
-                            for (int c = 0; c < V; ++c)
-                                if (e == R::expert(i, li) + c) r.x[i][c] += v;
-                    }
-                }
+                    for (int c = 0; c < V; ++c) r.x[i][c] = mine[R::expert(i, li) + c];
+                wave_lds_sync();
             }
             if (!ok) continue;
 #pragma unroll
@@ -504,7 +556,7 @@ hipError_t launch_balance_loss(const float *logits, const int32_t *idx, int T, i
     const dim3 grid((unsigned)(T > 0 ? (T + a.chunk - 1) / a.chunk : 1));
     with_layout(E, E % 4 == 0 && aligned16(logits), [&](auto v, auto ni, auto lpt) {
         hipLaunchKernelGGL((balance_sums_kernel<decltype(v)::value, decltype(ni)::value, decltype(lpt)::value>), grid,
-                           dim3(kThreads), 0, s, a, w.partP, w.partC, w.partZ, w.done);
+                           dim3(kThreads), 0, s, a, w.partP, w.partC, w.partZ, w.done, counts);
     });
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -104,6 +104,14 @@ __device__ __forceinline__ float silu_f32(float z) {
     return z * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
+// Between LDS writes and reads by other lanes of the same wavefront, whose LDS
+// operations complete in order: no instruction, but without it the compiler
+// may hand a lane back the value it wrote itself.
+__device__ __forceinline__ void wave_lds_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // ---------------------------------------------------------------------------
 // Block-wide exclusive scan of one int per thread (blockDim.x <= 1024,
 // multiple of 64). `lds` must hold 16 ints. Returns the exclusive prefix;

@@ -1,8 +1,8 @@
+// build-flags: -mllvm -amdgpu-mfma-vgpr-form
 // The LDS-tiled gate/up GEMM that also keeps both projections as MXFP8
 // checkpoints for the backward pass (tiled_gemm_kernel.h with CKPT): the
 // projections never leave the chip in 16 bits, only as codes (1 + 1/32 B a
 // value each). Same tile shapes as the inference gate/up.
-// build-flags: -mllvm -amdgpu-mfma-vgpr-form
 #include "tiled_gemm_kernel.h"
 
 namespace moe {

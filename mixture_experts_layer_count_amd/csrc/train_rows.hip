@@ -1,3 +1,4 @@
+// build-flags: -mllvm -amdgpu-mfma-vgpr-form
 // Row gradients of the grouped FFN: C[r][n] = sum_k A(r)[k] B_g[n][k] over
 // every expert's rows in one launch, with both operands contiguous in k (the
 // forward's weight matrices [K][N], read for the product with their
@@ -30,7 +31,6 @@
 // kRowsParts parts where that shortens it and an item is long (see
 // pick_rows); a part leaves its fp32 sums and the last one to finish adds them
 // in part order, so results do not depend on which that is.
-// build-flags: -mllvm -amdgpu-mfma-vgpr-form
 #include "tiled_gemm_kernel.h"
 
 namespace moe {
@@ -347,6 +347,7 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
             if (m + 1 < MI) load(nxt, m + 1);
             *reinterpret_cast<u32x4 *>(sc + lr * R::cld + lc) = cur.g;
             *reinterpret_cast<u32x4 *>(sc + 16 * R::cld + lr * R::cld + lc) = cur.u;
+            wave_lds_sync();
             float dw = 0.0f;
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
@@ -374,6 +375,7 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
             dw += __shfl_xor(dw, 32);
             if (gq == 0) sdw[wc * BM + wr * (BM / 2) + 16 * m + i16] = c0 < p.N ? dw : 0.0f;
             // 16-byte pieces of the staged rows: 8 a row, 2 a lane and output
+            wave_lds_sync();
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const int piece = lane + 64 * c, r = piece >> 3, col = 8 * (piece & 7);
@@ -387,6 +389,7 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
                         *reinterpret_cast<const u32x4 *>(o + 32 * R::old);
                 }
             }
+            wave_lds_sync();
             cur = nxt;
         }
         if (!p.dw_part) return;

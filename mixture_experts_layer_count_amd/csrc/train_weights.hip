@@ -1,3 +1,4 @@
+// build-flags: -mllvm -amdgpu-mfma-vgpr-form
 // Weight gradients of the grouped FFN: for every expert g,
 //   dW_g[m][n] = sum over its rows r of A(r)[m] B(r)[n]
 // in one launch: dW1 and dW3 (A = the token rows read back from their
@@ -27,7 +28,6 @@
 // and 8 of B through its XCD's L2 (tile rows one by one read 33: 5 % slower),
 // and workgroups differ by at most about one item's work whatever the
 // experts' row counts.
-// build-flags: -mllvm -amdgpu-mfma-vgpr-form
 #include "tiled_gemm_kernel.h"
 
 namespace moe {
@@ -209,6 +209,7 @@ __global__ __launch_bounds__(512, 1) void weights_gemm_kernel(WeightsProblem p, 
         const int r = ci.lo + 32 * ((ck & -R::window) + (lane >> 2)) + 4 * w + (lane & 3);
         if (r < ci.hi && MOE_BOUNDS_FAIL(got < (uint32_t)p.src_rows, BOUNDS_A_ROW)) got = 0;
         *row = r < ci.hi ? got * (GATHER == GATHER_A ? lda2 : ldb2) : kNoRow;
+        wave_lds_sync();
     };
     uint32_t row_off[2] = {0, 0};  // of the gathered operand's two copies of the step
     auto step_rows = [&]() {
@@ -343,6 +344,7 @@ __global__ __launch_bounds__(512, 1) void weights_gemm_kernel(WeightsProblem p, 
                 }
             }
             if constexpr (!F32) {
+                wave_lds_sync();
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int piece = ln + 64 * c, r = piece >> 3, col = 8 * (piece & 7), row = 16 * m + r;
@@ -352,6 +354,7 @@ __global__ __launch_bounds__(512, 1) void weights_gemm_kernel(WeightsProblem p, 
                     off = (row < rows) & (col < cols) ? off : kOut;
                     __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, off, 0, 0);
                 }
+                wave_lds_sync();
             }
 #pragma unroll
             for (int j = 0; j < NB; ++j) acc[m][j] = f32x4{};

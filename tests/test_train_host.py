@@ -92,14 +92,16 @@ SHARED_INVALID = [dict(T=-1), dict(k=0), dict(G=0), dict(H=0), dict(F=-32), dict
                   dict(W2=ODD), dict(W3=ODD), dict(ckpt=None), dict(ckpt=_ckpt(xq=None)), dict(ckpt=_ckpt(uq=0x1008)),
                   dict(ckpt=_ckpt(gs=None)), dict(row_src=None)]
 SHARED_UNSUPPORTED = [dict(dt=F32), dict(dt=FP8), dict(H=250), dict(F=100), dict(H=1 << 21), dict(k=65),
-                      dict(T=1 << 30), dict(G=65536)]
+                      dict(T=1 << 30), dict(G=1025), dict(T=1 << 23, k=1)]
 
 
 def test_ffn_train_forward_validation():
     ws = moe.lib().moe_ffn_train_forward_workspace_bytes
     assert 0 < ws(64, 2, 8, 256, 96) < ws(4096, 2, 8, 256, 96)
     assert ws(64, 2, 8, 250, 96) == 0 and ws(64, 0, 8, 256, 96) == 0
-    assert ws(1 << 25, 63, 65535, 1 << 20, 1 << 20) > 1 << 50
+    # the largest sizes: the token matrix below 4 GiB (32-bit row offsets), the rows' beyond
+    assert ws(2047, 64, 1024, 1 << 20, 1 << 20) > 1 << 37
+    assert ws(2048, 1, 8, 1 << 20, 32) == 0 and ws(1 << 25, 63, 1024, 64, 32) == 0
     assert _forward() == WS_SMALL and _forward(ws=None, ws_bytes=BIG) == WS_SMALL
     assert _forward(T=0, X=None, Yp=None, ckpt=None, ws=None) == OK
     for bad in SHARED_INVALID + [dict(X=None), dict(X=ODD), dict(Yp=None), dict(row_src=None, k=2)]:
@@ -112,7 +114,7 @@ def test_ffn_train_forward_validation():
 def test_ffn_train_backward_validation():
     ws = moe.lib().moe_ffn_train_backward_workspace_bytes
     assert 0 < ws(64, 2, 8, 256, 96) < ws(4096, 2, 8, 256, 96)
-    assert ws(1 << 25, 63, 65535, 1 << 20, 1 << 20) > 1 << 51
+    assert ws(2047, 64, 1024, 1 << 20, 1 << 20) > 1 << 39 and ws(2048, 1, 8, 1 << 20, 32) == 0
     assert _backward() == WS_SMALL and _backward(ws=None, ws_bytes=BIG) == WS_SMALL
     assert _backward(ws=ODD, ws_bytes=BIG) == WS_SMALL
     for bad in SHARED_INVALID + [dict(dY=None), dict(dY=ODD), dict(assign_row=None), dict(dW1=None), dict(dW3=None),
