@@ -57,7 +57,6 @@ unsigned bounds_take_combine();
 unsigned bounds_take_quant();
 unsigned bounds_take_ep();
 unsigned bounds_take_persist();
-unsigned bounds_take_tiled_ckpt();
 unsigned bounds_take_train_rows();
 unsigned bounds_take_train_weights();
 unsigned bounds_take_train_gather();
@@ -204,9 +203,6 @@ struct GemmProblem {
     // and left zero). NULL: no split.
     float *tail_part = nullptr;
     int32_t *tail_cnt = nullptr;
-    // checkpointing gate/up (launch_tiled_ckpt): codes and scale bytes of the
-    // gate and the up projection
-    uint8_t *ckpt[4] = {nullptr, nullptr, nullptr, nullptr};
     // rows of A (the bounds-checked build's checks only; 0: not known)
     long long a_rows = 0;
 };
@@ -238,10 +234,6 @@ hipError_t launch_tiled_persist(const GemmProblem &p, bool swiglu, hipStream_t s
 // and the number of counters
 size_t tiled_tail_bytes(int bm);
 constexpr int tiled_tail_counters = 256;
-
-// gate/up with bf16 weights that also writes both projections as MXFP8
-// checkpoints (p.ckpt); bm as for launch_tiled_gemm
-hipError_t launch_tiled_ckpt(const GemmProblem &p, int bm, hipStream_t s);
 
 // W8A8 variant of the LDS-tiled grouped GEMM (fp8 weights and fp8
 // activations with per-row 128-column scales, p.As transposed by GEMM row):
@@ -331,31 +323,36 @@ hipError_t launch_route_backward(const float *logits, const int32_t *idx, const 
                                  const float *dloss, float *dlogits, hipStream_t s);
 
 // ---------------------------------------------------------------------------
-// Backward pass of the grouped FFN (train_rows.hip, train_weights.hip)
+// The grouped FFN in training (train_rows.hip, train_weights.hip)
 // ---------------------------------------------------------------------------
 
-// C[r][n] = sum_k A(r)[k] B_g[n][k]: both operands K-contiguous. K is one
-// matrix's K0 columns, or two matrices' one after the other (B1 != NULL: K =
-// 2 K0, A rows 2 K0 wide). Row r of A is A[row_src[r] / gk] (A[r] if NULL).
+// C[r] = A(r) B_g, A(r) = A[row_src[r] / gk] (A[r] if NULL), K0 deep:
+//  GATE_UP  B0, B1 = W1, W3 [G][K0][N]: C = silu(A B0) (A B1) bf16 [M][N], and
+//           both products as MXFP8 checkpoints
+//  DOWN     B0 = W2 [G][K0][N]: C bf16 [M][N]
+//  BACK     B0 = W2 [G][N][K0]: p = A B0^T, and with the checkpointed g, u and
+//           the row's routing weight w (1 if topk_w is NULL): dGU [M][2 N] (dg
+//           then du), Hw [M][N] = w h, and dw_part[column tile][M] = sum over
+//           the tile's columns of p h
+//  DX       B0, B1 = W1, W3 [G][N][K0]: C = A[:, :K0] B0^T + A[:, K0:] B1^T,
+//           fp32 [M][N]
+enum RowsUse { ROWS_GATE_UP, ROWS_DOWN, ROWS_BACK, ROWS_DX };
 struct RowsProblem {
     const uint16_t *A;
     const int32_t *row_src;
     int gk, lda;
+    int a_rows;               // rows of A, when gathered (in at most gather_max_bytes)
     const int32_t *tiles, *n_tiles, *group_tile_start;
     int n_groups, max_tiles;
     int M, N, K0;
-    const uint16_t *B0, *B1;  // [G][N][K0]
-    float *C;                 // plain form: [M][N] fp32
-    // SwiGLU backward form: C is p = dY W2^T, and with the checkpointed g, u
-    // and the row's routing weight w (1 if topk_w is NULL): dGU [M][2 N] (dg
-    // then du), Hw [M][N] = w h, and dw_part[column tile][M] = sum over the
-    // tile's columns of p h
+    const uint16_t *B0, *B1;
+    void *C;
+    uint8_t *gq_out, *gs_out, *uq_out, *us_out;
     const uint8_t *gq, *gs, *uq, *us;
     const float *topk_w;
     const int32_t *w_src;     // row_src for topk_w (NULL: row r)
     uint16_t *dGU, *Hw;
     float *dw_part;
-    int a_rows = 0;           // rows of A, when gathered (in at most gather_max_bytes)
     // split of the last, partial round: room for xcd_parts parts' sums per XCD
     // (rows_gemm_part_bytes) and rows_gemm_counters counters, zero at launch
     // and used by one launch. NULL: no split
@@ -363,13 +360,14 @@ struct RowsProblem {
     int32_t *part_cnt = nullptr;
     int xcd_parts = 0;
 };
-int rows_gemm_bm(long long rows, int groups);
-constexpr int rows_gemm_bn = 256;  // columns per tile
+int rows_gemm_bm(long long rows, int groups, int columns);  // rows per tile; columns: column tiles
+constexpr int rows_gemm_bn = 256;  // B columns per tile
 constexpr int rows_gemm_counters = 256;
-int rows_gemm_xcd_parts(long long max_tiles, int N);
+int rows_gemm_columns(int N, RowsUse use);  // column tiles
+int rows_gemm_xcd_parts(long long max_tiles, int N, RowsUse use);
 size_t rows_gemm_part_bytes(int bm, int xcd_parts);
 constexpr uint32_t gather_max_bytes = 0xfffff000u;  // of a gathered matrix: 32-bit offsets
-hipError_t launch_rows_gemm(const RowsProblem &p, bool swiglu_backward, int bm, hipStream_t s);
+hipError_t launch_rows_gemm(const RowsProblem &p, RowsUse use, int bm, hipStream_t s);
 
 // dW_g[m][n] = sum over rows r of group g of A(r)[m] B(r)[n], for one or two
 // (B1cols: columns N .. 2 N - 1 of B's rows) output matrices.

@@ -68,7 +68,6 @@
 #include <type_traits>
 
 #include "common.h"
-#include "mx8.h"
 
 namespace moe {
 namespace tiled {
@@ -120,13 +119,10 @@ struct Out {
     static constexpr int ld = width + 8;              // LDS staging row stride (elements)
 };
 
-// checkpoint epilogue (CKPT): per tile row, 128 codes of each projection (with
-// a 16-byte pad) behind the staged h, then 4 scale bytes of each
-constexpr int kCkptLd = 256 + 16;
-template <int WT, bool SWIGLU, int BM, int WR, int WC, bool CKPT = false>
+template <int WT, bool SWIGLU, int BM, int WR, int WC>
 constexpr int lds_bytes() {
-    constexpr int out = BM * Out<SWIGLU>::ld * 2 + (CKPT ? BM * (kCkptLd + 8) : 0);
-    return Ring<WT, BM, WR, WC>::ring > out ? Ring<WT, BM, WR, WC>::ring : out;
+    return Ring<WT, BM, WR, WC>::ring > BM * Out<SWIGLU>::ld * 2 ? Ring<WT, BM, WR, WC>::ring
+                                                                  : BM * Out<SWIGLU>::ld * 2;
 }
 
 // A tile: 64-byte rows, 16-byte chunk c of row r stored at c ^ ((r >> 2) & 3),
@@ -321,10 +317,7 @@ struct Frags {
 // F32OUT (plain GEMM only): fp32 output straight from the accumulators, and
 // split-K: blockIdx.y = split s multiplies K range [s kchunk, (s+1) kchunk)
 // into C + s c_split_stride (every split must be non-empty).
-// CKPT (gate/up with bf16 weights): both projections are also written as
-// MXFP8 checkpoints (mx8.h): codes p.ckpt[0], p.ckpt[2] [M][N], scale bytes
-// p.ckpt[1], p.ckpt[3] [M][N/32].
-template <int WT, bool SWIGLU, int BM, int WR, bool F32OUT = false, int WC = 2, bool CKPT = false>
+template <int WT, bool SWIGLU, int BM, int WR, bool F32OUT = false, int WC = 2>
 __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_gemm_kernel(GemmProblem p, int nN) {
     static_assert(!(F32OUT && SWIGLU), "fp32 output is for the plain GEMM");
     typedef Ring<WT, BM, WR, WC> R;
@@ -335,8 +328,7 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_gemm_kernel(GemmProblem
     static_assert(!(F32OUT && MX), "fp32 output takes bf16 weights");
     constexpr int RW = (FP8 || MX) ? 1 : 2;
     constexpr int S = R::S;
-    static_assert(!CKPT || (SWIGLU && WT == W_BF16), "checkpoints are of bf16 gate/up projections");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[lds_bytes<WT, SWIGLU, BM, WR, WC, CKPT>()];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[lds_bytes<WT, SWIGLU, BM, WR, WC>()];
 
     // K steps of the problem (F32OUT: of this split)
     const int split = F32OUT ? (int)blockIdx.y : 0;
@@ -802,32 +794,6 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_gemm_kernel(GemmProblem
                 *reinterpret_cast<u32x2 *>(Cs + r * LD + (128 / WC) * wc + 16 * j + 4 * gq) =
                     u32x2{pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3])};
             }
-            if constexpr (CKPT) {
-                // a 32-column scale group is two adjacent column blocks: 8
-                // values in each of the four lanes that share lane % 16
-                uint8_t *cq = lds + BM * LD * 2 + r * kCkptLd;
-                uint8_t *cs = lds + BM * (LD * 2 + kCkptLd) + r * 8;
-#pragma unroll
-                for (int j = 0; j < NB; j += 2) {
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) top = max(top, mx8::amax_bits(acc[m][j + i / 4][i % 4]));
-                    top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-                    top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-                    const int e = mx8::scale_exp(top);
-                    const float inv = mx8::pow2(-e);
-                    // projection (0 gate, 1 up) and column of the group in the tile
-                    const int half = j / (NB / 2), col = (128 / WC) * wc + 16 * (j % (NB / 2));
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const f32x4 &v = acc[m][j + q];
-                        *reinterpret_cast<uint32_t *>(cq + 128 * half + col + 16 * q + 4 * gq) =
-                            mx8::codes4(mx8::scaled(v[0], inv), mx8::scaled(v[1], inv), mx8::scaled(v[2], inv),
-                                        mx8::scaled(v[3], inv));
-                    }
-                    if (gq == 0) cs[4 * half + col / 32] = (uint8_t)(e + 127);
-                }
-            }
         } else {
 #pragma unroll
             for (int j = 0; j < NB; ++j)
@@ -846,27 +812,9 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_gemm_kernel(GemmProblem
             *reinterpret_cast<u32x4 *>(Cg + (long long)row * p.ldc + col) =
                 *reinterpret_cast<const u32x4 *>(Cs + r * LD + 8 * cc);
     }
-    if constexpr (CKPT) {
-        // 16 pieces of 16 codes a row (8 of each projection; N % 32 == 0), and
-        // a row's 8 scale bytes
-        for (int idx = tid; idx < BM * 16; idx += kT) {
-            const int r = idx >> 4, half = (idx >> 3) & 1, cc = idx & 7;
-            const int row = row0 + r, col = n0 + 16 * cc;
-            if (row < row_end && col < p.N)
-                *reinterpret_cast<u32x4 *>(p.ckpt[2 * half] + (long long)row * p.N + col) =
-                    *reinterpret_cast<const u32x4 *>(lds + BM * LD * 2 + r * kCkptLd + 128 * half + 16 * cc);
-        }
-        for (int idx = tid; idx < BM * 8; idx += kT) {
-            const int r = idx >> 3, half = (idx >> 2) & 1, q = idx & 3;
-            const int row = row0 + r, col = n0 + 32 * q;
-            if (row < row_end && col < p.N)
-                p.ckpt[2 * half + 1][(long long)row * (p.N >> 5) + (col >> 5)] =
-                    lds[BM * (LD * 2 + kCkptLd) + r * 8 + 4 * half + q];
-        }
-    }
 }
 
-template <int WT, bool SWIGLU, int BM, int WR = 2, bool F32OUT = false, int WC = 2, bool CKPT = false>
+template <int WT, bool SWIGLU, int BM, int WR = 2, bool F32OUT = false, int WC = 2>
 inline hipError_t launch_t(const GemmProblem &p, hipStream_t s) {
     const int W = Out<SWIGLU>::width;
     const int nN = (p.N + W - 1) / W;
@@ -880,7 +828,7 @@ inline hipError_t launch_t(const GemmProblem &p, hipStream_t s) {
     }
     const long long blocks = per * kXcds;
     if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((tiled_gemm_kernel<WT, SWIGLU, BM, WR, F32OUT, WC, CKPT>),
+    hipLaunchKernelGGL((tiled_gemm_kernel<WT, SWIGLU, BM, WR, F32OUT, WC>),
                        dim3((unsigned)blocks, F32OUT ? (unsigned)p.ksplit : 1u), dim3(64 * WR * WC), 0, s, p, nN);
     return hipGetLastError();
 }

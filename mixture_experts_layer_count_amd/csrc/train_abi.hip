@@ -44,43 +44,97 @@ struct Tiles {
     }
 };
 
+// room for split items of two row products: sums (shared: one runs after the
+// other) and a set of counters each
+struct Parts {
+    int n[2];
+    float *sums;
+    int32_t *count;
+    void carve(Carver &c, const Tiles &t, int N0, RowsUse use0, int N1, RowsUse use1) {
+        n[0] = rows_gemm_xcd_parts(t.max_tiles, N0, use0);
+        n[1] = rows_gemm_xcd_parts(t.max_tiles, N1, use1);
+        sums = static_cast<float *>(c.take(rows_gemm_part_bytes(t.bm, n[0] > n[1] ? n[0] : n[1])));
+        count = static_cast<int32_t *>(c.take(sizeof(int32_t) * 2 * rows_gemm_counters));
+    }
+};
+
+RowsProblem rows_problem(const Tiles &t, const Parts &parts, int which, int G, int M, int k) {
+    RowsProblem p{};
+    p.gk = k;
+    p.tiles = t.tiles;
+    p.n_tiles = t.n_tiles;
+    p.group_tile_start = t.start;
+    p.n_groups = G;
+    p.max_tiles = t.max_tiles;
+    p.M = M;
+    p.part = parts.sums;
+    p.part_cnt = parts.count + which * rows_gemm_counters;
+    p.xcd_parts = parts.n[which];
+    return p;
+}
+
+// the fewer of two row products' column tiles
+int columns(int N0, RowsUse use0, int N1, RowsUse use1) {
+    const int a = rows_gemm_columns(N0, use0), b = rows_gemm_columns(N1, use1);
+    return a < b ? a : b;
+}
+
+// Yp = h W2 on the inference path's persistent kernel
+GemmProblem down_problem(const Tiles &t, int M, int G, int H, int F) {
+    GemmProblem g{};
+    g.tiles = t.tiles;
+    g.n_tiles = t.n_tiles;
+    g.group_tile_start = t.start;
+    g.n_groups = G;
+    g.max_tiles = t.max_tiles;
+    g.M = M;
+    g.gk = 1;
+    g.ksplit = 1;
+    g.lda = F;
+    g.a_rows = M;
+    g.N = g.ldc = H;
+    g.K = g.kchunk = F;
+    g.b_stride = (long long)F * H;
+    return g;
+}
+
+// down projections of at most this depth take the persistent kernel where it
+// fits: its items overlap, which counts while they are short (F 768: 257 to
+// 287 us against 286 to 326 on 65536 rows, H 2048)
+constexpr int kPersistDepth = 1024;
+
 struct ForwardWs {
     Tiles t;
+    bool persist;  // the down projection's kernel
+    Parts parts;
     uint16_t *h;  // [M][F]
-    float *tail_part;
-    int32_t *tail_cnt;
-    size_t carve(void *ws, long long M, int G, int F) {
+    size_t carve(void *ws, long long M, int G, int H, int F) {
         Carver c(ws);
-        t.carve(c, M, G, tiled_gemm_bm(W_BF16, M, G));
+        t.carve(c, M, G, rows_gemm_bm(M, G, columns(F, ROWS_GATE_UP, H, ROWS_DOWN)));
+        parts.carve(c, t, F, ROWS_GATE_UP, H, ROWS_DOWN);
+        persist = F <= kPersistDepth && tiled_persist_fits(down_problem(t, (int)M, G, H, F), W_BF16, false, t.bm);
         h = static_cast<uint16_t *>(c.take(2 * (size_t)M * F));
-        tail_part = static_cast<float *>(c.take(tiled_tail_bytes(t.bm)));
-        tail_cnt = static_cast<int32_t *>(c.take(sizeof(int32_t) * tiled_tail_counters));
         return c.used;
     }
 };
 
 struct BackwardWs {
     Tiles t;
+    Parts parts;
     uint16_t *x;    // [T][H] the token rows, read back from their checkpoint
     uint16_t *dgu;  // [M][2F]
     uint16_t *hw;   // [M][F]
     float *rows;    // [M][H] row gradients at the token rows
     float *dw_part; // [column tiles of F][M]
-    float *part;    // sums of split items, and their counters (one set per launch)
-    int32_t *part_cnt;
-    int parts_f, parts_h;
     size_t carve(void *ws, long long T, long long M, int G, int H, int F) {
         Carver c(ws);
-        t.carve(c, M, G, rows_gemm_bm(M, G));
+        t.carve(c, M, G, rows_gemm_bm(M, G, columns(F, ROWS_BACK, H, ROWS_DX)));
+        parts.carve(c, t, F, ROWS_BACK, H, ROWS_DX);
         x = static_cast<uint16_t *>(c.take(2 * (size_t)T * H));
         dgu = static_cast<uint16_t *>(c.take(4 * (size_t)M * F));
         hw = static_cast<uint16_t *>(c.take(2 * (size_t)M * F));
         rows = static_cast<float *>(c.take(4 * (size_t)M * H));
-        dw_part = static_cast<float *>(c.take(4 * (size_t)M * ((F + rows_gemm_bn - 1) / rows_gemm_bn)));
-        parts_f = rows_gemm_xcd_parts(t.max_tiles, F);
-        parts_h = rows_gemm_xcd_parts(t.max_tiles, H);
-        part = static_cast<float *>(c.take(rows_gemm_part_bytes(t.bm, parts_f > parts_h ? parts_f : parts_h)));
-        part_cnt = static_cast<int32_t *>(c.take(sizeof(int32_t) * 2 * rows_gemm_counters));
+        dw_part = static_cast<float *>(c.take(4 * (size_t)M * rows_gemm_columns(F, ROWS_BACK)));
         return c.used;
     }
 };
@@ -149,7 +203,7 @@ moe_status moe_checkpoint_unpack(const uint8_t *Q, const uint8_t *S, long long R
 size_t moe_ffn_train_forward_workspace_bytes(int T, int k, int G, int H, int F) {
     if (check_train_ffn(true, k, T, G, H, F, MOE_BF16) != MOE_OK) return 0;
     ForwardWs w;
-    return w.carve(nullptr, (long long)T * k, G, F);
+    return w.carve(nullptr, (long long)T * k, G, H, F);
 }
 
 moe_status moe_ffn_train_forward(const void *X, const int32_t *row_src, int k, int T, const int32_t *offsets, int G,
@@ -162,49 +216,40 @@ moe_status moe_ffn_train_forward(const void *X, const int32_t *row_src, int k, i
         return MOE_ERR_INVALID_ARG;
     const int M = T * k;
     ForwardWs w;
-    if (bad16(ws) || ws_bytes < w.carve(ws, M, G, F)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (bad16(ws) || ws_bytes < w.carve(ws, M, G, H, F)) return MOE_ERR_WORKSPACE_TOO_SMALL;
 
     MOE_TRY(launch_mx8_pack(X, MOE_BF16, H, T, H, ckpt->xq, ckpt->xs, stream));
-    MOE_TRY(w.t.build(offsets, G, stream, w.tail_cnt, tiled_tail_counters));
-    GemmProblem g{};
-    g.tiles = w.t.tiles;
-    g.n_tiles = w.t.n_tiles;
-    g.group_tile_start = w.t.start;
-    g.n_groups = G;
-    g.max_tiles = w.t.max_tiles;
-    g.M = M;
-    g.gk = k;
-    g.ksplit = 1;
-    GemmProblem up = g;
-    up.A = X;
+    MOE_TRY(w.t.build(offsets, G, stream, w.parts.count, 2 * rows_gemm_counters));
+    RowsProblem up = rows_problem(w.t, w.parts, 0, G, M, k);
+    up.A = static_cast<const uint16_t *>(X);
     up.row_src = row_src;
     up.lda = H;
     up.a_rows = T;
     up.N = F;
-    up.K = up.kchunk = H;
-    up.B0 = W1;
-    up.B1 = W3;
-    up.b_stride = (long long)H * F;
+    up.K0 = H;
+    up.B0 = static_cast<const uint16_t *>(W1);
+    up.B1 = static_cast<const uint16_t *>(W3);
     up.C = w.h;
-    up.ldc = F;
-    up.ckpt[0] = ckpt->gq;
-    up.ckpt[1] = ckpt->gs;
-    up.ckpt[2] = ckpt->uq;
-    up.ckpt[3] = ckpt->us;
-    MOE_TRY(launch_tiled_ckpt(up, w.t.bm, stream));
-    GemmProblem down = g;
+    up.gq_out = ckpt->gq;
+    up.gs_out = ckpt->gs;
+    up.uq_out = ckpt->uq;
+    up.us_out = ckpt->us;
+    MOE_TRY(launch_rows_gemm(up, ROWS_GATE_UP, w.t.bm, stream));
+    if (w.persist) {
+        GemmProblem d = down_problem(w.t, M, G, H, F);
+        d.A = w.h;
+        d.B0 = W2;
+        d.C = Yp;
+        return hip_status(launch_tiled_persist(d, false, stream));
+    }
+    RowsProblem down = rows_problem(w.t, w.parts, 1, G, M, k);
     down.A = w.h;
     down.lda = F;
-    down.a_rows = M;
     down.N = H;
-    down.K = down.kchunk = F;
-    down.B0 = W2;
-    down.b_stride = (long long)F * H;
+    down.K0 = F;
+    down.B0 = static_cast<const uint16_t *>(W2);
     down.C = Yp;
-    down.ldc = H;
-    down.tail_part = w.tail_part;
-    down.tail_cnt = w.tail_cnt;
-    return hip_status(launch_tiled_gemm(down, W_BF16, false, true, w.t.bm, stream));
+    return hip_status(launch_rows_gemm(down, ROWS_DOWN, w.t.bm, stream));
 }
 
 // ---------------------------------------------------------------------------
@@ -233,18 +278,9 @@ moe_status moe_ffn_train_backward(const void *dY, const float *topk_w, const int
     if (bad16(ws) || ws_bytes < w.carve(ws, T, M, G, H, F)) return MOE_ERR_WORKSPACE_TOO_SMALL;
 
     if (T > 0) {
-        MOE_TRY(w.t.build(offsets, G, stream, w.part_cnt, 2 * rows_gemm_counters));
-        RowsProblem p{};
-        p.gk = k;
-        p.tiles = w.t.tiles;
-        p.n_tiles = w.t.n_tiles;
-        p.group_tile_start = w.t.start;
-        p.n_groups = G;
-        p.max_tiles = w.t.max_tiles;
-        p.M = M;
-        p.part = w.part;
+        MOE_TRY(w.t.build(offsets, G, stream, w.parts.count, 2 * rows_gemm_counters));
         // p = dY W2^T, then dg, du, w h and the routing weights' partial sums
-        RowsProblem b = p;
+        RowsProblem b = rows_problem(w.t, w.parts, 0, G, M, k);
         b.A = static_cast<const uint16_t *>(dY);
         b.row_src = row_src;
         b.lda = H;
@@ -260,25 +296,20 @@ moe_status moe_ffn_train_backward(const void *dY, const float *topk_w, const int
         b.w_src = row_src;
         b.dGU = w.dgu;
         b.Hw = w.hw;
-        b.part_cnt = w.part_cnt;
-        b.xcd_parts = w.parts_f;
         b.dw_part = dtopk_w ? w.dw_part : nullptr;
-        MOE_TRY(launch_rows_gemm(b, true, w.t.bm, stream));
+        MOE_TRY(launch_rows_gemm(b, ROWS_BACK, w.t.bm, stream));
         if (dX) {
-            RowsProblem d = p;
+            RowsProblem d = rows_problem(w.t, w.parts, 1, G, M, k);
             d.A = w.dgu;
             d.lda = 2 * F;
-            d.a_rows = M;
             d.N = H;
             d.K0 = F;
             d.B0 = static_cast<const uint16_t *>(W1);
             d.B1 = static_cast<const uint16_t *>(W3);
             d.C = w.rows;
-            d.part_cnt = w.part_cnt + rows_gemm_counters;
-            d.xcd_parts = w.parts_h;
-            MOE_TRY(launch_rows_gemm(d, false, w.t.bm, stream));
+            MOE_TRY(launch_rows_gemm(d, ROWS_DX, w.t.bm, stream));
         }
-        MOE_TRY(launch_gather_grads(w.rows, w.dw_part, (F + rows_gemm_bn - 1) / rows_gemm_bn, assign_row, T, k,
+        MOE_TRY(launch_gather_grads(w.rows, w.dw_part, rows_gemm_columns(F, ROWS_BACK), assign_row, T, k,
                                     offsets + G, M, H, dX_add, dX, dtopk_w, stream));
         if (dW1) MOE_TRY(launch_mx8_unpack(ckpt->xq, ckpt->xs, T, H, MOE_BF16, w.x, stream));
     }

@@ -1,27 +1,33 @@
 // build-flags: -mllvm -amdgpu-mfma-vgpr-form
-// Row gradients of the grouped FFN: C[r][n] = sum_k A(r)[k] B_g[n][k] over
-// every expert's rows in one launch, with both operands contiguous in k (the
-// forward's weight matrices [K][N], read for the product with their
-// transpose). Two uses:
-//  * SwiGLU backward (BACK): A(r) = dY[token of r], B = W2 [F][H], so the
+// The expert FFN's row products in training: C[r] = A(r) B_g over every
+// expert's rows in one launch, A(r) contiguous in k. Four uses:
+//  * GATE_UP: A(r) = X[token of r], B = W1 and W3 [H][F]. The epilogue forms
+//    h = silu(g) u (bf16) and writes g and u as MXFP8 checkpoints (mx8.h):
+//    they never leave the chip in 16 bits.
+//  * DOWN: A = h, B = W2 [F][H], bf16 rows out.
+//  * BACK, the SwiGLU backward: A(r) = dY[token of r], B = W2^T, so the
 //    accumulator is p = dY W2^T, before the routing weight. The epilogue reads
-//    the checkpointed g and u (MXFP8) and forms, with s = 1 / (1 + e^-g):
+//    the checkpointed g and u and forms, with s = 1 / (1 + e^-g):
 //      h = g s u            dw[r] = sum_f p h        (gradient of the weight)
 //      dg = w p u s (1 + g (1 - s))    du = w p g s    w h for dW2
 //    dY is gathered by the copies and never multiplied by w in memory: the
 //    combine's backward pass costs no pass of its own.
-//  * plain: A = [dg | du] [M][2F], B = W1 then W3 [H][F] along k; fp32 rows
-//    out (they are summed over a token's k rows before the one rounding).
-// dg, du and w h are rounded to bf16: the operands of the bf16 matrix cores.
+//  * DX: A = [dg | du] [M][2F], B = W1^T then W3^T along k; fp32 rows out (they
+//    are summed over a token's k rows before the one rounding).
+// h, dg, du and w h are rounded to bf16: the operands of the bf16 matrix cores.
 //
 // Tile BM (128 or 256) rows x 256 columns, 64 deep a step, 8 wavefronts in
-// 2 x 4, each BM/2 rows x 64 columns. Both operands are copied as whole
-// 128-byte lines of a row (32 deep, the 64-byte halves were separate requests
-// to L2) by buffer loads: a lane's offset stays the same over k, the step only
-// moves the scalar descriptor. LDS rows are 128 bytes, 16-byte chunk c of row
+// 2 x 4, each BM/2 rows x 64 columns (GATE_UP: 128 columns of W1 and of W3).
+// Operands contiguous in k (A; B of the two backward uses, whose weight rows
+// are k) are copied as whole 128-byte lines of a row (32 deep, the 64-byte
+// halves were separate requests to L2) by buffer loads: a lane's offset stays
+// the same over k, the step only moves the scalar descriptor. LDS rows are 128
+// bytes, 16-byte chunk c of row
 // r at c ^ ((r >> 1) & 7): a ds_read_b128 serves lanes 0-3, 12-15 and 20-27
 // (then the others) together, whose eight even and eight odd rows then hit all
-// 64 banks once.
+// 64 banks once. The forward's B keeps the weights' [K][N] layout, two 64 x 128
+// panels with 256-byte rows, and is read with ds_read_b64_tr_b16 (chunks
+// swizzled by bswz16 of the row).
 // A step's two 32-deep halves alternate in two register sets: the second
 // half's fragments are read while the first is multiplied and the next step's
 // first while the second is, so one barrier a step (after the next step's
@@ -31,6 +37,7 @@
 // kRowsParts parts where that shortens it and an item is long (see
 // pick_rows); a part leaves its fp32 sums and the last one to finish adds them
 // in part order, so results do not depend on which that is.
+#include "mx8.h"
 #include "tiled_gemm_kernel.h"
 
 namespace moe {
@@ -41,7 +48,6 @@ namespace tiled {
 namespace {
 
 constexpr int kRowsBN = rows_gemm_bn;
-
 constexpr int kRowsBK = 64;
 constexpr int kRowsParts = 4;        // parts of a split item at most
 constexpr int kRowsPartSteps = 32;   // and steps a part has at least (a part's sums cost about 10 steps)
@@ -50,7 +56,8 @@ constexpr int kRowsXcdParts = 64;    // parts (and their fp32 sums) per XCD at m
 template <int BM>
 struct RowsRing {
     static constexpr int a_bytes = BM * 128;
-    static constexpr int stage = a_bytes + kRowsBN * 128;
+    static constexpr int b_bytes = kRowsBN * 128;
+    static constexpr int stage = a_bytes + b_bytes;
     static constexpr int S = kRingBudget / stage < 3 ? kRingBudget / stage : 3;
     static constexpr int nA = BM / 64;  // 1 KB copies (8 rows) per wavefront and step
     static constexpr int nB = kRowsBN / 64;
@@ -61,7 +68,12 @@ struct RowsRing {
     static constexpr int old = 64 + 8, cld = 64 + 16;
     static constexpr int stg = 3 * 16 * old * 2 + 2 * 16 * cld;
     static constexpr int dw = 8 * stg;   // [4][BM] floats behind it
-    static constexpr int lds = S * stage > dw + 16 * BM ? S * stage : dw + 16 * BM;
+    // GATE_UP's: rows of 128 bf16 h, then of both projections' 128 codes
+    // (padded), then of 4 scale bytes each
+    static constexpr int hld = 128 + 8, qld = 256 + 16;
+    static constexpr int codes = BM * hld * 2, scales = codes + BM * qld;
+    static constexpr int epi = scales + 8 * BM > dw + 16 * BM ? scales + 8 * BM : dw + 16 * BM;
+    static constexpr int lds = S * stage > epi ? S * stage : epi;
     static_assert(S >= 2 && lds <= 160 * 1024, "LDS");
 };
 
@@ -105,14 +117,17 @@ __device__ __forceinline__ bool pick_rows(const RowsProblem &p, int nN, int nk, 
     return true;
 }
 
-template <int BM, bool BACK>
+template <int BM, RowsUse USE>
 __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN) {
     typedef RowsRing<BM> R;
-    constexpr int S = R::S, MI = R::MI, NB = 4, NC = R::per_tile, NR = NB + MI;
+    constexpr bool KN = USE == ROWS_GATE_UP || USE == ROWS_DOWN;  // B is [K][N]
+    constexpr int BR = KN ? 2 : 1;                                // reads of a B block
+    constexpr int S = R::S, MI = R::MI, NB = 4, NC = R::per_tile, NR = BR * NB + MI;
+    constexpr int W = USE == ROWS_GATE_UP ? kRowsBN / 2 : kRowsBN;  // output columns per tile
     __shared__ __attribute__((aligned(1024))) uint8_t lds[R::lds];
 
     // steps of one B matrix (the last may be half) and of all
-    const int nk0 = (p.K0 + kRowsBK - 1) / kRowsBK, nk_all = p.B1 ? 2 * nk0 : nk0;
+    const int nk0 = (p.K0 + kRowsBK - 1) / kRowsBK, nk_all = USE == ROWS_DX ? 2 * nk0 : nk0;
     Unit u;
     if (!pick_rows(p, nN, nk_all, u)) return;
     const int mt = u.mt, nt = u.nt;
@@ -122,7 +137,7 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
     const int g = p.tiles[4 * mt], row0 = p.tiles[4 * mt + 1], row_end = p.tiles[4 * mt + 2];
     if (MOE_BOUNDS_FAIL(g >= 0 && g < p.n_groups && row0 >= 0 && row0 < row_end && row_end <= p.M, BOUNDS_TILE))
         return;
-    const int n0 = nt * kRowsBN;
+    const int n0 = nt * W;
     const int tid = threadIdx.x;
     const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wr = w / 4, wc = w % 4;
     const int i16 = lane & 15, gq = lane >> 4;
@@ -141,15 +156,32 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
         if (p.row_src && MOE_BOUNDS_FAIL(src >= 0 && src < p.a_rows, BOUNDS_A_ROW)) src = 0;
         a_off[q] = 2u * ((uint32_t)src * p.lda + 8 * ((lane & 7) ^ ((tr >> 1) & 7)));
     }
+    const char *a0 = reinterpret_cast<const char *>(p.A + (p.row_src ? 0LL : (long long)row0 * p.lda));
+    // B [N][K0]: rows as A's. B [K0][N]: panel q / 2 of 128 columns, copy q % 2
+    // of it fills rows 4 (2 w + q % 2) + lane / 16 of the step; columns past N
+    // read the last ones, a DOWN panel past N the first panel (never stored)
+    const char *b0, *b1;
+    static_assert(!KN || R::nB == 4, "two copies a panel");
+    const int panel1 = USE == ROWS_DOWN && p.N - n0 > 128 ? 128 : 0;
 #pragma unroll
     for (int q = 0; q < R::nB; ++q) {
-        const int tr = 8 * (w * R::nB + q) + (lane >> 3);
-        b_off[q] = 2u * ((uint32_t)min(tr, p.N - 1 - n0) * p.K0 + 8 * ((lane & 7) ^ ((tr >> 1) & 7)));
+        if constexpr (KN) {
+            const int k = 4 * (2 * w + (q & 1)) + (lane >> 4), first = n0 + (q < 2 ? 0 : panel1);
+            b_off[q] = 2u * ((uint32_t)k * p.N + min(8 * ((lane & 15) ^ bswz16(k)), p.N - 8 - first));
+        } else {
+            const int tr = 8 * (w * R::nB + q) + (lane >> 3);
+            b_off[q] = 2u * ((uint32_t)min(tr, p.N - 1 - n0) * p.K0 + 8 * ((lane & 7) ^ ((tr >> 1) & 7)));
+        }
     }
-    const char *a0 = reinterpret_cast<const char *>(p.A + (p.row_src ? 0LL : (long long)row0 * p.lda));
-    const long long b_first = ((long long)g * p.N + n0) * p.K0;
-    const char *b0 = reinterpret_cast<const char *>(p.B0 + b_first);
-    const char *b1 = p.B1 ? reinterpret_cast<const char *>(p.B1 + b_first) : b0;
+    if constexpr (KN) {
+        const long long first = (long long)g * p.K0 * p.N + n0;
+        b0 = reinterpret_cast<const char *>(p.B0 + first);
+        b1 = USE == ROWS_GATE_UP ? reinterpret_cast<const char *>(p.B1 + first) : b0 + 2 * panel1;
+    } else {
+        const long long first = ((long long)g * p.N + n0) * p.K0;
+        b0 = reinterpret_cast<const char *>(p.B0 + first);
+        b1 = USE == ROWS_DX ? reinterpret_cast<const char *>(p.B1 + first) : b0;
+    }
     // bytes from the descriptor's start to the last row's end
     const uint32_t a_len = 2u * p.lda * (uint32_t)(p.row_src ? p.a_rows : row_end - row0);
     const uint32_t b_len = 2u * p.K0 * (uint32_t)min(kRowsBN, p.N - n0);
@@ -163,11 +195,17 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
     for (int q = 0; q < 2; ++q) second[q] = ((lane & 7) ^ (4 * q + (lane >> 4))) >= 4 ? gather_max_bytes : 0;
     auto copy = [&](int q, int kt, int stage) {
         uint8_t *st = lds + stage * R::stage;
-        const int seg = kt >= nk0 ? 1 : 0, k = kRowsBK * (kt - seg * nk0);  // first column of the step in its matrix
+        const int seg = USE == ROWS_DX && kt >= nk0 ? 1 : 0, k = kRowsBK * (kt - seg * nk0);  // first column of the step in its matrix
         const uint32_t cut = k + kRowsBK > p.K0 ? ~0u : 0u;
         if (q < R::nA) {
             const int ka = 2 * (k + seg * p.K0);
             copy16_buffer(a0 + ka, a_len - ka, a_off[q] | (second[q & 1] & cut), st + (w * R::nA + q) * 1024);
+        } else if constexpr (KN) {
+            // the rows left of K0 (the others of a last half step read zeros)
+            const int s = (q - R::nA) / 2, i = (q - R::nA) % 2;
+            const uint32_t len = 2u * ((uint32_t)min(kRowsBK, p.K0 - k) * p.N - n0 - (s ? panel1 : 0));
+            copy16_buffer((s ? b1 : b0) + 2LL * k * p.N, len, b_off[q - R::nA],
+                          st + R::a_bytes + s * (R::b_bytes / 2) + (2 * w + i) * 1024);
         } else {
             copy16_buffer((seg ? b1 : b0) + 2 * k, b_len - 2 * k, b_off[q - R::nA] | (second[(q - R::nA) & 1] & cut),
                           st + R::a_bytes + (w * R::nB + q - R::nA) * 1024);
@@ -177,14 +215,54 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
     // ---- fragment reads of half h: B blocks, then A row blocks ----
     struct Frag {
         bf16x8 a[MI], b[NB];
+        u32x2 raw[KN ? NB : 1][2];
     };
     const int swz = (i16 >> 1) & 7;  // of row i16 of any 16-row block
     const int a_row = (wr * (BM / 2) + i16) * 128, b_row = R::a_bytes + (64 * wc + i16) * 128;
-    auto read = [&](Frag &f, int r, int stage, int h) {
-        const uint8_t *st = lds + stage * R::stage + 16 * ((4 * h + gq) ^ swz);
-        if (r < NB) f.b[r] = *reinterpret_cast<const bf16x8 *>(st + b_row + r * 2048);
-        else f.a[r - NB] = *reinterpret_cast<const bf16x8 *>(st + a_row + (r - NB) * 2048);
+    // B [K0][N]: the lane's k rows are 32 h + 8 gq + 4 (half of the read pair) +
+    // i16 / 4 of the block's panel; column block j moves the chunk index in
+    // bits that only the swizzle's XOR touches
+    const int k0 = 8 * gq + (i16 >> 2), c0 = ((i16 & 3) >> 1) + (USE == ROWS_GATE_UP ? 4 * wc : 8 * (wc & 1));
+    const uint32_t b_tr = R::a_bytes + (USE == ROWS_GATE_UP ? 0 : (wc >> 1) * (R::b_bytes / 2)) + k0 * 256 +
+                          16 * (c0 ^ bswz16(k0)) + 8 * (i16 & 1);
+    auto read = [&](Frag &f, int r, int stage, auto half) {
+        constexpr int h = decltype(half)::value;
+        const uint8_t *st = lds + stage * R::stage;
+        if constexpr (KN) {
+            if (r < 2 * NB) {
+                const int j = r >> 1;
+                // GATE_UP: blocks 0, 1 of W1's panel and 2, 3 of W3's
+                const uint32_t at = (lds_addr(st) + b_tr) ^ (32 * (USE == ROWS_GATE_UP ? j & 1 : j));
+                constexpr int panel = USE == ROWS_GATE_UP ? R::b_bytes / 2 : 0, kh = 4 * 256;
+                if (j < 2) f.raw[j][r & 1] = r & 1 ? ds_tr16_at<h * 8192 + kh>(at) : ds_tr16_at<h * 8192>(at);
+                else f.raw[j][r & 1] = r & 1 ? ds_tr16_at<h * 8192 + kh + panel>(at) : ds_tr16_at<h * 8192 + panel>(at);
+                return;
+            }
+            r -= 2 * NB;
+        } else {
+            if (r < NB) {
+                f.b[r] = *reinterpret_cast<const bf16x8 *>(st + 16 * ((4 * h + gq) ^ swz) + b_row + r * 2048);
+                return;
+            }
+            r -= NB;
+        }
+        f.a[r] = *reinterpret_cast<const bf16x8 *>(st + 16 * ((4 * h + gq) ^ swz) + a_row + r * 2048);
     };
+    // the reads have completed: hand the transposed ones to the compiler
+    auto land = [&](Frag &f) {
+        wait_lds();
+        if constexpr (KN) {
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                fence(f.raw[j][0]);
+                fence(f.raw[j][1]);
+                f.b[j] = __builtin_bit_cast(
+                    bf16x8, u32x4{f.raw[j][0][0], f.raw[j][0][1], f.raw[j][1][0], f.raw[j][1][1]});
+            }
+        }
+    };
+    constexpr std::integral_constant<int, 0> first_half;
+    constexpr std::integral_constant<int, 1> second_half;
 
     f32x4 acc[MI][NB];
 #pragma unroll
@@ -211,11 +289,11 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
     wait_vm<(S - 1) * NC>();
     __builtin_amdgcn_s_barrier();
 #pragma unroll
-    for (int r = 0; r < NR; ++r) read(fa, r, 0, 0);
-    wait_lds();
+    for (int r = 0; r < NR; ++r) read(fa, r, 0, first_half);
+    land(fa);
     auto kloop = [&](auto act) {
         constexpr int ACT = decltype(act)::value;
-        auto wanted = [](int r) { return ACT > 0 && (r < NB || r - NB < ACT); };
+        auto wanted = [](int r) { return ACT > 0 && (r < BR * NB || r - BR * NB < ACT); };
         int stage = 0;
         for (int kt = k_first; kt <= k_last; ++kt) {
             const int nstage = stage + 1 == S ? 0 : stage + 1;
@@ -226,10 +304,10 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
             for (int c = 0; c < MI; ++c) {
 #pragma unroll
                 for (int r = c * NR / SA; r < (c + 1) * NR / SA && r < NR; ++r)
-                    if (wanted(r)) read(fb, r, stage, 1);
+                    if (wanted(r)) read(fb, r, stage, second_half);
                 mma_rows(fa, c, act);
             }
-            wait_lds();
+            if (ACT > 0) land(fb);
             // second half; the next step's first fragments are read
             constexpr int PRE = MI >= 8 ? 2 : 1, SLOTS = MI - PRE;
 #pragma unroll
@@ -242,10 +320,10 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
                 for (int q = c * NC / SLOTS; q < (c + 1) * NC / SLOTS; ++q) copy(q, src, stage);
 #pragma unroll
                 for (int r = c * NR / SLOTS; r < (c + 1) * NR / SLOTS; ++r)
-                    if (wanted(r)) read(fa, r, nstage, 0);
+                    if (wanted(r)) read(fa, r, nstage, first_half);
                 mma_rows(fb, c + PRE, act);
             }
-            wait_lds();  // every read of the stage is done before anyone refills it
+            if (ACT > 0) land(fa);
             stage = nstage;
         }
     };
@@ -282,7 +360,7 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
         }
         __syncthreads();  // the flag has been read: the LDS is free
     }
-    if constexpr (!BACK) {
+    if constexpr (USE == ROWS_DX) {
 #pragma unroll
         for (int m = 0; m < MI; ++m) {
             const int row = row0 + wr * (BM / 2) + 16 * m + i16;
@@ -290,10 +368,90 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
                 const int col = n0 + 64 * wc + 16 * j + 4 * gq;
-                if (col < p.N) *reinterpret_cast<f32x4 *>(p.C + (long long)row * p.N + col) = acc[m][j];
+                if (col < p.N)
+                    *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(p.C) + (long long)row * p.N + col) = acc[m][j];
             }
         }
-        return;
+    } else if constexpr (USE == ROWS_DOWN) {
+        __syncthreads();  // every wavefront is done with the ring
+        // 16 rows at a time through the wavefront's staging area
+        uint16_t *so = reinterpret_cast<uint16_t *>(lds + w * R::stg);
+#pragma unroll
+        for (int m = 0; m < MI; ++m) {
+            if (m >= nblk) continue;
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+                *reinterpret_cast<u32x2 *>(so + i16 * R::old + 16 * j + 4 * gq) =
+                    u32x2{pack_bf16x2(acc[m][j][0], acc[m][j][1]), pack_bf16x2(acc[m][j][2], acc[m][j][3])};
+            wave_lds_sync();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int piece = lane + 64 * c, r = piece >> 3, col = n0 + 64 * wc + 8 * (piece & 7);
+                const int row = row0 + wr * (BM / 2) + 16 * m + r;
+                if (row < row_end && col < p.N)
+                    *reinterpret_cast<u32x4 *>(reinterpret_cast<uint16_t *>(p.C) + (long long)row * p.N + col) =
+                        *reinterpret_cast<const u32x4 *>(so + r * R::old + 8 * (piece & 7));
+            }
+            wave_lds_sync();
+        }
+    } else if constexpr (USE == ROWS_GATE_UP) {
+        __syncthreads();
+        // the tile's h, codes and scale bytes in LDS, then 16-byte pieces of
+        // rows. A wavefront's 32 columns of a projection are one scale group:
+        // 8 values in each of the four lanes that share lane % 16
+        uint16_t *sh = reinterpret_cast<uint16_t *>(lds);
+#pragma unroll
+        for (int m = 0; m < MI; ++m) {
+            if (m >= nblk) continue;
+            const int r = wr * (BM / 2) + 16 * m + i16;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float h[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[i] = silu_f32(acc[m][j][i]) * acc[m][j + 2][i];
+                *reinterpret_cast<u32x2 *>(sh + r * R::hld + 32 * wc + 16 * j + 4 * gq) =
+                    u32x2{pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3])};
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {  // g, u
+                const f32x4 (&v)[NB] = acc[m];
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = max(top, mx8::amax_bits(v[2 * half + i / 4][i % 4]));
+                top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+                top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+                const int e = mx8::scale_exp(top);
+                const float inv = mx8::pow2(-e);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const f32x4 &x = v[2 * half + q];
+                    *reinterpret_cast<uint32_t *>(lds + R::codes + r * R::qld + 128 * half + 32 * wc + 16 * q + 4 * gq) =
+                        mx8::codes4(mx8::scaled(x[0], inv), mx8::scaled(x[1], inv), mx8::scaled(x[2], inv),
+                                    mx8::scaled(x[3], inv));
+                }
+                if (gq == 0) lds[R::scales + r * 8 + 4 * half + wc] = (uint8_t)(e + 127);
+            }
+        }
+        __syncthreads();
+        uint16_t *C = reinterpret_cast<uint16_t *>(p.C);
+        for (int i = tid; i < BM * 16; i += 512) {
+            const int r = i >> 4, c = i & 15, row = row0 + r;
+            if (row >= row_end) break;  // rows only grow
+            if (n0 + 8 * c < p.N)
+                *reinterpret_cast<u32x4 *>(C + (long long)row * p.N + n0 + 8 * c) =
+                    *reinterpret_cast<const u32x4 *>(sh + r * R::hld + 8 * c);
+            // 8 pieces of 16 codes of each projection (N % 32 == 0)
+            const int half = c >> 3, col = n0 + 16 * (c & 7);
+            if (col < p.N)
+                *reinterpret_cast<u32x4 *>((half ? p.uq_out : p.gq_out) + (long long)row * p.N + col) =
+                    *reinterpret_cast<const u32x4 *>(lds + R::codes + r * R::qld + 16 * c);
+        }
+        for (int i = tid; i < BM * 8; i += 512) {
+            const int r = i >> 3, half = (i >> 2) & 1, q = i & 3, row = row0 + r;
+            if (row < row_end && n0 + 32 * q < p.N)
+                (half ? p.us_out : p.gs_out)[(long long)row * (p.N >> 5) + (n0 >> 5) + q] =
+                    lds[R::scales + r * 8 + 4 * half + q];
+        }
     } else {
         __syncthreads();  // every wavefront is done with the ring
         // ---- SwiGLU backward, 16 rows at a time, through the wavefront's
@@ -402,42 +560,58 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
 }
 
 template <int BM>
-hipError_t launch_rows(const RowsProblem &p, bool back, hipStream_t s) {
-    const int nN = (p.N + kRowsBN - 1) / kRowsBN;
+hipError_t launch_rows(const RowsProblem &p, RowsUse use, hipStream_t s) {
+    const int nN = rows_gemm_columns(p.N, use);
     // items per XCD, and the parts that the last of them may be split into
     const long long per = ((long long)p.max_tiles * nN + kXcds - 1) / kXcds + (p.part ? p.xcd_parts : 0);
     const long long blocks = per * kXcds;
     if (blocks <= 0) return hipSuccess;
     if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-    if (back)
-        hipLaunchKernelGGL((rows_gemm_kernel<BM, true>), dim3((unsigned)blocks), dim3(512), 0, s, p, nN);
-    else
-        hipLaunchKernelGGL((rows_gemm_kernel<BM, false>), dim3((unsigned)blocks), dim3(512), 0, s, p, nN);
+    auto launch = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(512), 0, s, p, nN);
+    };
+    switch (use) {
+    case ROWS_GATE_UP: launch(rows_gemm_kernel<BM, ROWS_GATE_UP>); break;
+    case ROWS_DOWN: launch(rows_gemm_kernel<BM, ROWS_DOWN>); break;
+    case ROWS_BACK: launch(rows_gemm_kernel<BM, ROWS_BACK>); break;
+    case ROWS_DX: launch(rows_gemm_kernel<BM, ROWS_DX>); break;
+    }
     return hipGetLastError();
 }
 
 }  // namespace
 }  // namespace tiled
 
-// 256-row tiles once experts average 192 rows (as the forward's tiles), else 128
-int rows_gemm_bm(long long rows, int groups) { return groups > 0 && rows >= 192LL * groups ? 256 : 128; }
-
-int rows_gemm_xcd_parts(long long max_tiles, int N) {
-    const long long per = (max_tiles * ((N + rows_gemm_bn - 1) / rows_gemm_bn) + tiled::kXcds - 1) / tiled::kXcds;
+// 256-row tiles where experts average 192 rows (as the inference tiles) and
+// there are enough of them for one round of the CUs; else 128, whose items take
+// half as long (8 experts, 3072 rows, H 640, F 416: see the table of cases)
+int rows_gemm_bm(long long rows, int groups, int columns) {
+    const long long tiles = rows / 256 + groups / 2;  // about half a tile of each expert is a rest
+    return groups > 0 && rows >= 192LL * groups && tiles * columns >= tiled::kXcds * tiled::kBlocksPerXcd ? 256 : 128;
+}
+int rows_gemm_columns(int N, RowsUse use) {
+    const int w = use == ROWS_GATE_UP ? rows_gemm_bn / 2 : rows_gemm_bn;
+    return (N + w - 1) / w;
+}
+int rows_gemm_xcd_parts(long long max_tiles, int N, RowsUse use) {
+    const long long per = (max_tiles * rows_gemm_columns(N, use) + tiled::kXcds - 1) / tiled::kXcds;
     return (int)(per * tiled::kRowsParts < tiled::kRowsXcdParts ? per * tiled::kRowsParts : tiled::kRowsXcdParts);
 }
 size_t rows_gemm_part_bytes(int bm, int xcd_parts) {
     return sizeof(float) * (size_t)tiled::kXcds * xcd_parts * bm * rows_gemm_bn;
 }
 
-hipError_t launch_rows_gemm(const RowsProblem &p, bool back, int bm, hipStream_t s) {
-    if (!p.A || !p.B0 || !p.tiles || !p.n_tiles || !p.group_tile_start || p.N < 32 || p.N % 32 || p.K0 < 32 ||
-        p.K0 % 32 || p.gk < 1 || p.lda < (p.B1 ? 2 * p.K0 : p.K0) ||
-        (p.row_src && (p.a_rows < 1 || 2LL * p.a_rows * p.lda > gather_max_bytes)) || (p.part && (!p.part_cnt || p.xcd_parts < 1)))
+hipError_t launch_rows_gemm(const RowsProblem &p, RowsUse use, int bm, hipStream_t s) {
+    const bool two = use == ROWS_GATE_UP || use == ROWS_DX;
+    if (!p.A || !p.B0 || two != (p.B1 != nullptr) || !p.tiles || !p.n_tiles || !p.group_tile_start || p.N < 32 ||
+        p.N % 32 || p.K0 < 32 || p.K0 % 32 || p.gk < 1 || p.lda < (use == ROWS_DX ? 2 * p.K0 : p.K0) ||
+        (p.row_src && (p.a_rows < 1 || 2LL * p.a_rows * p.lda > gather_max_bytes)) ||
+        (p.part && (!p.part_cnt || p.xcd_parts < 1)))
         return hipErrorInvalidValue;
-    if (back ? (!p.gq || !p.gs || !p.uq || !p.us || !p.dGU || !p.Hw || p.B1) : !p.C) return hipErrorInvalidValue;
-    if (bm == 256) return tiled::launch_rows<256>(p, back, s);
-    if (bm == 128) return tiled::launch_rows<128>(p, back, s);
+    if (use == ROWS_BACK ? (!p.gq || !p.gs || !p.uq || !p.us || !p.dGU || !p.Hw) : !p.C) return hipErrorInvalidValue;
+    if (use == ROWS_GATE_UP && (!p.gq_out || !p.gs_out || !p.uq_out || !p.us_out)) return hipErrorInvalidValue;
+    if (bm == 256) return tiled::launch_rows<256>(p, use, s);
+    if (bm == 128) return tiled::launch_rows<128>(p, use, s);
     return hipErrorInvalidValue;
 }
 
