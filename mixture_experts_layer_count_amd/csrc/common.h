@@ -353,19 +353,17 @@ struct RowsProblem {
     const int32_t *w_src;     // row_src for topk_w (NULL: row r)
     uint16_t *dGU, *Hw;
     float *dw_part;
-    // split of the last, partial round: room for xcd_parts parts' sums per XCD
-    // (rows_gemm_part_bytes) and rows_gemm_counters counters, zero at launch
-    // and used by one launch. NULL: no split
+    // split of the last, partial round: rows_gemm_part_bytes bytes for the
+    // parts' sums and rows_gemm_counters counters, zero at launch and used by
+    // one launch. NULL: no split
     float *part = nullptr;
     int32_t *part_cnt = nullptr;
-    int xcd_parts = 0;
 };
 int rows_gemm_bm(long long rows, int groups, int columns);  // rows per tile; columns: column tiles
 constexpr int rows_gemm_bn = 256;  // B columns per tile
 constexpr int rows_gemm_counters = 256;
 int rows_gemm_columns(int N, RowsUse use);  // column tiles
-int rows_gemm_xcd_parts(long long max_tiles, int N, RowsUse use);
-size_t rows_gemm_part_bytes(int bm, int xcd_parts);
+size_t rows_gemm_part_bytes(int bm, RowsUse use, int K0);  // 0: never split
 constexpr uint32_t gather_max_bytes = 0xfffff000u;  // of a gathered matrix: 32-bit offsets
 hipError_t launch_rows_gemm(const RowsProblem &p, RowsUse use, int bm, hipStream_t s);
 

@@ -45,9 +45,10 @@ __device__ __forceinline__ uint32_t amax_bits(float x) {
 }
 // the four values of a code word, times 2^e
 __device__ __forceinline__ f32x4 values4(uint32_t w, float s) {
-    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
-    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
-    return f32x4{lo[0] * s, lo[1] * s, hi[0] * s, hi[1] * s};
+    // the conversion multiplies by the scale's exponent
+    const auto lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, s, false);
+    const auto hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, s, true);
+    return f32x4{lo[0], lo[1], hi[0], hi[1]};
 }
 __device__ __forceinline__ float scale_of(uint8_t byte) { return __uint_as_float((uint32_t)byte << 23); }
 

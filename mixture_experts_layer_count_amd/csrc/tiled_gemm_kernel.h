@@ -216,6 +216,18 @@ __device__ __forceinline__ u32x2 ds_tr16_at(uint32_t addr) {
 }
 __device__ __forceinline__ void fence(u32x2 &v) { asm volatile("" : "+v"(v)); }
 
+// Two 16-column blocks' packed bf16 results of a lane (columns 4 gq .. + 3 of
+// each, gq = lane / 16) -> 8 adjacent columns, 16 (gq % 2) + 8 (gq / 2) .. of
+// the pair: the odd 16-lane rows of the first block change places with the
+// even ones of the second. A 16-byte store of it covers 64 contiguous bytes of
+// 16 rows.
+__device__ __forceinline__ u32x4 pair_columns(const f32x4 &x0, const f32x4 &x1) {
+    const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16x2(x0[0], x0[1]), pack_bf16x2(x1[0], x1[1]), false, false);
+    const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16x2(x0[2], x0[3]), pack_bf16x2(x1[2], x1[3]), false, false);
+    return u32x4{lo[0], hi[0], lo[1], hi[1]};
+}
+__device__ __forceinline__ int pair_column(int gq) { return 16 * (gq & 1) + 8 * (gq >> 1); }
+
 // Map this workgroup to (row tile, column tile) of the work order; false for
 // surplus workgroups. Work order: for each group, for each band of gn column
 // tiles, the group's row tiles x the band's column tiles (column fastest).

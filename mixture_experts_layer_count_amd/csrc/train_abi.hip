@@ -47,13 +47,13 @@ struct Tiles {
 // room for split items of two row products: sums (shared: one runs after the
 // other) and a set of counters each
 struct Parts {
-    int n[2];
+    size_t bytes[2];
     float *sums;
     int32_t *count;
-    void carve(Carver &c, const Tiles &t, int N0, RowsUse use0, int N1, RowsUse use1) {
-        n[0] = rows_gemm_xcd_parts(t.max_tiles, N0, use0);
-        n[1] = rows_gemm_xcd_parts(t.max_tiles, N1, use1);
-        sums = static_cast<float *>(c.take(rows_gemm_part_bytes(t.bm, n[0] > n[1] ? n[0] : n[1])));
+    void carve(Carver &c, const Tiles &t, int K0, RowsUse use0, int K1, RowsUse use1) {
+        bytes[0] = rows_gemm_part_bytes(t.bm, use0, K0);
+        bytes[1] = rows_gemm_part_bytes(t.bm, use1, K1);
+        sums = static_cast<float *>(c.take(bytes[0] > bytes[1] ? bytes[0] : bytes[1]));
         count = static_cast<int32_t *>(c.take(sizeof(int32_t) * 2 * rows_gemm_counters));
     }
 };
@@ -67,9 +67,10 @@ RowsProblem rows_problem(const Tiles &t, const Parts &parts, int which, int G, i
     p.n_groups = G;
     p.max_tiles = t.max_tiles;
     p.M = M;
-    p.part = parts.sums;
-    p.part_cnt = parts.count + which * rows_gemm_counters;
-    p.xcd_parts = parts.n[which];
+    if (parts.bytes[which]) {
+        p.part = parts.sums;
+        p.part_cnt = parts.count + which * rows_gemm_counters;
+    }
     return p;
 }
 
@@ -111,7 +112,7 @@ struct ForwardWs {
     size_t carve(void *ws, long long M, int G, int H, int F) {
         Carver c(ws);
         t.carve(c, M, G, rows_gemm_bm(M, G, columns(F, ROWS_GATE_UP, H, ROWS_DOWN)));
-        parts.carve(c, t, F, ROWS_GATE_UP, H, ROWS_DOWN);
+        parts.carve(c, t, H, ROWS_GATE_UP, F, ROWS_DOWN);
         persist = F <= kPersistDepth && tiled_persist_fits(down_problem(t, (int)M, G, H, F), W_BF16, false, t.bm);
         h = static_cast<uint16_t *>(c.take(2 * (size_t)M * F));
         return c.used;
@@ -129,7 +130,7 @@ struct BackwardWs {
     size_t carve(void *ws, long long T, long long M, int G, int H, int F) {
         Carver c(ws);
         t.carve(c, M, G, rows_gemm_bm(M, G, columns(F, ROWS_BACK, H, ROWS_DX)));
-        parts.carve(c, t, F, ROWS_BACK, H, ROWS_DX);
+        parts.carve(c, t, H, ROWS_BACK, F, ROWS_DX);
         x = static_cast<uint16_t *>(c.take(2 * (size_t)T * H));
         dgu = static_cast<uint16_t *>(c.take(4 * (size_t)M * F));
         hw = static_cast<uint16_t *>(c.take(2 * (size_t)M * F));

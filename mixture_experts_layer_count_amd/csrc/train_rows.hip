@@ -34,9 +34,13 @@
 // copies have landed) both publishes the next stage and frees this one.
 //
 // Tail: the last, partial round of an XCD's items is split over k into up to
-// kRowsParts parts where that shortens it and an item is long (see
-// pick_rows); a part leaves its fp32 sums and the last one to finish adds them
-// in part order, so results do not depend on which that is.
+// kRowsParts parts, as many as one round of its CUs takes, where an item is
+// long (8 experts of 4096 x 14336, 8192 rows: DX 2150 -> 1890 us, BACK 1195 ->
+// 1140; 32 experts of 7168 x 2048, 4096 rows: GATE_UP 560 -> 511). Parts in a
+// second round lose: the weights' bytes bound such a launch, and the CUs left
+// in a partial round get them faster (BACK of those 32 experts, 18 items left:
+// 293 us, as 54 parts 310). A part leaves its fp32 sums and the last one to
+// finish adds them in part order, so results do not depend on which that is.
 #include "mx8.h"
 #include "tiled_gemm_kernel.h"
 
@@ -51,7 +55,6 @@ constexpr int kRowsBN = rows_gemm_bn;
 constexpr int kRowsBK = 64;
 constexpr int kRowsParts = 4;        // parts of a split item at most
 constexpr int kRowsPartSteps = 32;   // and steps a part has at least (a part's sums cost about 10 steps)
-constexpr int kRowsXcdParts = 64;    // parts (and their fp32 sums) per XCD at most
 
 template <int BM>
 struct RowsRing {
@@ -63,7 +66,7 @@ struct RowsRing {
     static constexpr int nB = kRowsBN / 64;
     static constexpr int per_tile = nA + nB;
     static constexpr int MI = BM / 32;   // 16-row blocks per wavefront
-    // epilogue staging per wavefront: a 16 x 64 block of each output (bf16,
+    // BACK's staging per wavefront: a 16 x 64 block of each output (bf16,
     // padded rows) and of each code matrix
     static constexpr int old = 64 + 8, cld = 64 + 16;
     static constexpr int stg = 3 * 16 * old * 2 + 2 * 16 * cld;
@@ -78,9 +81,8 @@ struct RowsRing {
 };
 
 // This workgroup's item, or part of one. Items are in tile_of's order, a
-// contiguous run of them per XCD; the run's last `tail` items (one partial
-// round of the XCD's CUs) are split into the number of parts that ends the
-// round soonest: ceil(tail parts / CUs) / parts rounds.
+// contiguous run of them per XCD; the run's last `tail` items, one partial
+// round of the XCD's CUs, are split.
 __device__ __forceinline__ bool pick_rows(const RowsProblem &p, int nN, int nk, Unit &u) {
     GemmProblem order{};
     order.tiles = p.tiles;
@@ -92,17 +94,7 @@ __device__ __forceinline__ bool pick_rows(const RowsProblem &p, int nN, int nk, 
     const int first = xcd * per, n = min(per, n_work - first);
     if (n <= 0) return false;
     const int tail = n % kBlocksPerXcd, full = n - tail;
-    int parts = 1;
-    if (p.part && tail > 0) {
-        int rounds = 1;  // of 1 / parts
-        for (int q = 2; q <= kRowsParts; ++q) {
-            const int r = (tail * q + kBlocksPerXcd - 1) / kBlocksPerXcd;
-            if (tail * q <= p.xcd_parts && q * kRowsPartSteps <= nk && r * parts < rounds * q) {
-                parts = q;
-                rounds = r;
-            }
-        }
-    }
+    const int parts = p.part && tail > 0 ? max(min(min(kRowsParts, kBlocksPerXcd / tail), nk / kRowsPartSteps), 1) : 1;
     int item = slot;
     if (slot >= full) {
         const int v = slot - full;
@@ -111,7 +103,7 @@ __device__ __forceinline__ bool pick_rows(const RowsProblem &p, int nN, int nk, 
         u.part = v % parts;
         u.parts = parts;
         u.tail_slot = xcd * kBlocksPerXcd + v / parts;
-        u.part_slot = xcd * p.xcd_parts + v;
+        u.part_slot = xcd * kBlocksPerXcd + v;
     }
     tile_of(order, nN, n_tiles, first + item, u.mt, u.nt);
     return true;
@@ -335,7 +327,7 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
     if (u.parts > 1) {
         // leave this part's sums ([accumulator][thread] vectors); the last part
         // to count itself adds all of them in part order
-        if (MOE_BOUNDS_FAIL(u.part_slot < kXcds * p.xcd_parts && u.part_slot >= u.part, BOUNDS_TAIL_SLOT)) return;
+        if (MOE_BOUNDS_FAIL(u.part_slot < rows_gemm_counters && u.part_slot >= u.part, BOUNDS_TAIL_SLOT)) return;
         f32x4 *mine = reinterpret_cast<f32x4 *>(p.part) + (long long)u.part_slot * (MI * NB * 512);
 #pragma unroll
         for (int i = 0; i < MI * NB; ++i) mine[i * 512 + tid] = acc[i / NB][i % NB];
@@ -373,26 +365,16 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
             }
         }
     } else if constexpr (USE == ROWS_DOWN) {
-        __syncthreads();  // every wavefront is done with the ring
-        // 16 rows at a time through the wavefront's staging area
-        uint16_t *so = reinterpret_cast<uint16_t *>(lds + w * R::stg);
+        uint16_t *C = reinterpret_cast<uint16_t *>(p.C);
 #pragma unroll
         for (int m = 0; m < MI; ++m) {
-            if (m >= nblk) continue;
+            const int row = row0 + wr * (BM / 2) + 16 * m + i16;
 #pragma unroll
-            for (int j = 0; j < NB; ++j)
-                *reinterpret_cast<u32x2 *>(so + i16 * R::old + 16 * j + 4 * gq) =
-                    u32x2{pack_bf16x2(acc[m][j][0], acc[m][j][1]), pack_bf16x2(acc[m][j][2], acc[m][j][3])};
-            wave_lds_sync();
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int piece = lane + 64 * c, r = piece >> 3, col = n0 + 64 * wc + 8 * (piece & 7);
-                const int row = row0 + wr * (BM / 2) + 16 * m + r;
-                if (row < row_end && col < p.N)
-                    *reinterpret_cast<u32x4 *>(reinterpret_cast<uint16_t *>(p.C) + (long long)row * p.N + col) =
-                        *reinterpret_cast<const u32x4 *>(so + r * R::old + 8 * (piece & 7));
+            for (int j = 0; j < NB; j += 2) {
+                const u32x4 v = pair_columns(acc[m][j], acc[m][j + 1]);
+                const int col = n0 + 64 * wc + 16 * j + pair_column(gq);
+                if (row < row_end && col < p.N) *reinterpret_cast<u32x4 *>(C + (long long)row * p.N + col) = v;
             }
-            wave_lds_sync();
         }
     } else if constexpr (USE == ROWS_GATE_UP) {
         __syncthreads();
@@ -455,7 +437,9 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
     } else {
         __syncthreads();  // every wavefront is done with the ring
         // ---- SwiGLU backward, 16 rows at a time, through the wavefront's
-        // staging area (its LDS operations complete in order) ----
+        // staging area (its LDS operations complete in order): whole 128-byte
+        // lines out (64-byte pieces straight from the registers, as DOWN
+        // stores, took 1 us more a tile of 20: three outputs) ----
         uint8_t *stg = lds + w * R::stg;
         uint16_t *so = reinterpret_cast<uint16_t *>(stg);
         uint8_t *sc = stg + 3 * 16 * R::old * 2;
@@ -521,7 +505,8 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
                     dw = fmaf(pv, h, dw);
                     const float pw = cur.w * pv;
                     du[i] = pw * gsv;
-                    dg[i] = pw * uv[i] * s * (1.0f + gv[i] * (1.0f - s));
+                    // s (1 + g (1 - s)) = s + g s (1 - s)
+                    dg[i] = pw * uv[i] * fmaf(gsv, 1.0f - s, s);
                     hw[i] = cur.w * h;
                 }
                 uint16_t *o = so + i16 * R::old + 16 * j + 4 * gq;
@@ -563,7 +548,7 @@ template <int BM>
 hipError_t launch_rows(const RowsProblem &p, RowsUse use, hipStream_t s) {
     const int nN = rows_gemm_columns(p.N, use);
     // items per XCD, and the parts that the last of them may be split into
-    const long long per = ((long long)p.max_tiles * nN + kXcds - 1) / kXcds + (p.part ? p.xcd_parts : 0);
+    const long long per = ((long long)p.max_tiles * nN + kXcds - 1) / kXcds + (p.part ? kBlocksPerXcd : 0);
     const long long blocks = per * kXcds;
     if (blocks <= 0) return hipSuccess;
     if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
@@ -593,12 +578,11 @@ int rows_gemm_columns(int N, RowsUse use) {
     const int w = use == ROWS_GATE_UP ? rows_gemm_bn / 2 : rows_gemm_bn;
     return (N + w - 1) / w;
 }
-int rows_gemm_xcd_parts(long long max_tiles, int N, RowsUse use) {
-    const long long per = (max_tiles * rows_gemm_columns(N, use) + tiled::kXcds - 1) / tiled::kXcds;
-    return (int)(per * tiled::kRowsParts < tiled::kRowsXcdParts ? per * tiled::kRowsParts : tiled::kRowsXcdParts);
-}
-size_t rows_gemm_part_bytes(int bm, int xcd_parts) {
-    return sizeof(float) * (size_t)tiled::kXcds * xcd_parts * bm * rows_gemm_bn;
+static_assert(rows_gemm_counters == tiled::kXcds * tiled::kBlocksPerXcd, "one slot per CU");
+size_t rows_gemm_part_bytes(int bm, RowsUse use, int K0) {
+    // none where the steps are too few to split
+    if (K0 * (use == ROWS_DX ? 2LL : 1LL) < 2LL * tiled::kRowsPartSteps * tiled::kRowsBK) return 0;
+    return sizeof(float) * (size_t)rows_gemm_counters * bm * rows_gemm_bn;
 }
 
 hipError_t launch_rows_gemm(const RowsProblem &p, RowsUse use, int bm, hipStream_t s) {
@@ -606,7 +590,7 @@ hipError_t launch_rows_gemm(const RowsProblem &p, RowsUse use, int bm, hipStream
     if (!p.A || !p.B0 || two != (p.B1 != nullptr) || !p.tiles || !p.n_tiles || !p.group_tile_start || p.N < 32 ||
         p.N % 32 || p.K0 < 32 || p.K0 % 32 || p.gk < 1 || p.lda < (use == ROWS_DX ? 2 * p.K0 : p.K0) ||
         (p.row_src && (p.a_rows < 1 || 2LL * p.a_rows * p.lda > gather_max_bytes)) ||
-        (p.part && (!p.part_cnt || p.xcd_parts < 1)))
+        (p.part && !p.part_cnt))
         return hipErrorInvalidValue;
     if (use == ROWS_BACK ? (!p.gq || !p.gs || !p.uq || !p.us || !p.dGU || !p.Hw) : !p.C) return hipErrorInvalidValue;
     if (use == ROWS_GATE_UP && (!p.gq_out || !p.gs_out || !p.uq_out || !p.us_out)) return hipErrorInvalidValue;

@@ -47,10 +47,8 @@ struct WRing {
     static constexpr int S = 4;
     static constexpr int nC = 4;           // copies per wavefront and step (2 of each operand)
     static constexpr int MI = 8, NB = 4;
-    static constexpr int old = 64 + 8;     // epilogue staging (bf16), 16 rows a wavefront
-    static constexpr int stg = S * stage, stg_bytes = 16 * old * 2;
     static constexpr int window = 16;      // steps per window of row numbers (4 rows a wavefront and step)
-    static constexpr int rows = stg + 8 * stg_bytes, rows_bytes = 4 * 4 * window;
+    static constexpr int rows = S * stage, rows_bytes = 4 * 4 * window;
     // experts by falling row count: index (uint16), first row and end (int)
     static constexpr int order = rows + 8 * 2 * rows_bytes;
     static constexpr int range = order + 2 * kMaxGroups;
@@ -303,12 +301,13 @@ __global__ __launch_bounds__(512, 1) void weights_gemm_kernel(WeightsProblem p, 
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    // ---- a finished tile: row block by row block through the wavefront's
-    // staging area, or (fp32) straight from the accumulators, which are
-    // cleared. Buffer stores: those outside the matrix get an offset past the
-    // buffer's range and are dropped by the hardware, so every wavefront
-    // issues exactly kStores of them whatever the tile ----
-    constexpr int kStores = F32 ? MI * NB : 2 * MI;
+    // ---- a finished tile, straight from the accumulators (which are cleared):
+    // bf16 as 8 adjacent columns a lane, after one exchange between lanes;
+    // through LDS the epilogue took 2.2 us a tile. Buffer stores: those outside
+    // the matrix get an offset past the buffer's range and are dropped by the
+    // hardware, so every wavefront issues exactly kStores of them whatever the
+    // tile ----
+    constexpr int kStores = F32 ? MI * NB : MI * NB / 2;
     constexpr int kOut = 0x7fffffff;
     auto tile_out = [&](const WItem &it) {
         constexpr int size = F32 ? 4 : 2;
@@ -320,44 +319,38 @@ __global__ __launch_bounds__(512, 1) void weights_gemm_kernel(WeightsProblem p, 
         asm volatile("" : "+v"(nd), "+v"(ln));
         const int l16 = ln & 15, lq = ln >> 4;
         const int rows = p.MD - it.m0 - 128 * wr, cols = p.ND - it.n0 - 64 * wc;
-        uint16_t *stg = reinterpret_cast<uint16_t *>(lds + R::stg + w * R::stg_bytes);
 #pragma unroll
         for (int m = 0; m < MI; ++m) {
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                const int row = 16 * m + l16, col = 16 * j + 4 * lq;
+            for (int j = 0; j < NB; j += F32 ? 1 : 2) {
+                const int row = 16 * m + l16, col = 16 * j + (F32 ? 4 * lq : pair_column(lq));
                 int off = (row * nd + col) * size;
                 asm volatile("" : "+v"(off));  // formed first: the choice is then no branch
                 off = (row < rows) & (col < cols) ? off : kOut;
-                f32x4 v = acc[m][j];
                 if constexpr (F32) {
+                    f32x4 v = acc[m][j];
                     if (ACC && off != kOut) v += *reinterpret_cast<const f32x4 *>(C + off);
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rsrc, off, 0, 0);
+                    acc[m][j] = f32x4{};
                 } else {
-                    if (ACC && off != kOut) {
-                        const u32x2 old = *reinterpret_cast<const u32x2 *>(C + off);
-                        v += f32x4{bf16_lo(old[0]), bf16_hi(old[0]), bf16_lo(old[1]), bf16_hi(old[1])};
+                    f32x4 v0 = acc[m][j], v1 = acc[m][j + 1];
+                    if (ACC) {
+                        // what C holds, in the accumulators' layout
+                        f32x4 *const v[2] = {&v0, &v1};
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int c = 16 * (j + i) + 4 * lq;
+                            if (row < rows && c < cols) {
+                                const u32x2 old = *reinterpret_cast<const u32x2 *>(C + (row * nd + c) * size);
+                                *v[i] += f32x4{bf16_lo(old[0]), bf16_hi(old[0]), bf16_lo(old[1]), bf16_hi(old[1])};
+                            }
+                        }
                     }
-                    *reinterpret_cast<u32x2 *>(stg + l16 * R::old + col) =
-                        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                    __builtin_amdgcn_raw_buffer_store_b128(pair_columns(v0, v1), rsrc, off, 0, 0);
+                    acc[m][j] = acc[m][j + 1] = f32x4{};
                 }
             }
-            if constexpr (!F32) {
-                wave_lds_sync();
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int piece = ln + 64 * c, r = piece >> 3, col = 8 * (piece & 7), row = 16 * m + r;
-                    const u32x4 v = *reinterpret_cast<const u32x4 *>(stg + r * R::old + col);
-                    int off = (row * nd + col) * size;
-                    asm volatile("" : "+v"(off));
-                    off = (row < rows) & (col < cols) ? off : kOut;
-                    __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, off, 0, 0);
-                }
-                wave_lds_sync();
-            }
-#pragma unroll
-            for (int j = 0; j < NB; ++j) acc[m][j] = f32x4{};
         }
     };
 
