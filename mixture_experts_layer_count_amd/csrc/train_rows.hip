@@ -569,7 +569,7 @@ hipError_t launch_rows(const RowsProblem &p, RowsUse use, hipStream_t s) {
 
 // 256-row tiles where experts average 192 rows (as the inference tiles) and
 // there are enough of them for one round of the CUs; else 128, whose items take
-// half as long (8 experts, 3072 rows, H 640, F 416: see the table of cases)
+// half as long (8 experts, T 1536, k 2, H 640, F 416)
 int rows_gemm_bm(long long rows, int groups, int columns) {
     const long long tiles = rows / 256 + groups / 2;  // about half a tile of each expert is a rest
     return groups > 0 && rows >= 192LL * groups && tiles * columns >= tiled::kXcds * tiled::kBlocksPerXcd ? 256 : 128;

@@ -84,6 +84,7 @@ __global__ __launch_bounds__(512, 1) void weights_gemm_kernel(WeightsProblem p, 
                                                               Divisor group_tiles, Divisor band_tiles) {
     typedef WRing R;
     constexpr int S = R::S, MI = R::MI, NB = R::NB, NC = R::nC, NR = 2 * (MI + NB);
+    constexpr int kStores = F32 ? MI * NB : MI * NB / 2;  // a finished tile's, per wavefront
     __shared__ __attribute__((aligned(1024))) uint8_t lds[R::lds];
     uint16_t *order = reinterpret_cast<uint16_t *>(lds + R::order);
     int *range = reinterpret_cast<int *>(lds + R::range);
@@ -191,9 +192,10 @@ __global__ __launch_bounds__(512, 1) void weights_gemm_kernel(WeightsProblem p, 
     };
     // the gathered operand's rows: byte offsets of the current window's rows
     // (16 steps x the wavefront's 4) lie in LDS; the next window's row numbers
-    // are on their way there. wk: steps copied since they were sent for
+    // are on their way there. newer: vector-memory operations since they were
+    // sent for
     const int32_t *src = GATHER == GATHER_A ? p.a_src : p.b_src;
-    int buf = 0, wk = 0;
+    int buf = 0, newer = 0;
     uint8_t *my_rows = lds + R::rows + w * 2 * R::rows_bytes;
     auto fetch_rows = [&](const WItem &it, int k, int b) {
         if (GATHER == GATHER_NONE || it.hi == it.lo) return;
@@ -221,18 +223,21 @@ __global__ __launch_bounds__(512, 1) void weights_gemm_kernel(WeightsProblem p, 
     // the one after it is sent for
     auto advance = [&]() {
         ++ck;
-        ++wk;
+        newer += NC;
         a_ptr += GATHER == GATHER_A ? 0 : 32 * lda2;
         b_ptr += GATHER == GATHER_B ? 0 : 32 * ldb2;
         const bool next_item = ck == cnk;
         if (next_item || (ck & (R::window - 1)) == 0) {
             if (GATHER != GATHER_NONE) {
-                // at least NC wk copies are newer than the window's: it has
-                // landed when no more than that are outstanding
-                if (wk >= 3) wait_vm<3 * NC>();
+                // the window has landed when no more than `newer` operations
+                // are outstanding: the S - 1 steps in flight, and a finished
+                // tile's stores where they are among them (waiting for those
+                // took 1 us of each 4-step item)
+                if (newer >= (S - 1) * NC + kStores) wait_vm<(S - 1) * NC + kStores>();
+                else if (newer >= (S - 1) * NC) wait_vm<(S - 1) * NC>();
                 else wait_vm<0>();
             }
-            wk = 0;
+            newer = 0;
             buf ^= 1;
             if (next_item) {
                 ci = cn;
@@ -307,7 +312,6 @@ __global__ __launch_bounds__(512, 1) void weights_gemm_kernel(WeightsProblem p, 
     // the matrix get an offset past the buffer's range and are dropped by the
     // hardware, so every wavefront issues exactly kStores of them whatever the
     // tile ----
-    constexpr int kStores = F32 ? MI * NB : MI * NB / 2;
     constexpr int kOut = 0x7fffffff;
     auto tile_out = [&](const WItem &it) {
         constexpr int size = F32 ? 4 : 2;
@@ -424,6 +428,7 @@ __global__ __launch_bounds__(512, 1) void weights_gemm_kernel(WeightsProblem p, 
         }
         if (!ACC || mi.lo < mi.hi) {
             tile_out(mi);
+            newer += kStores;
             relax = ACC ? 0 : S - 1;
         }
         ++mj;

@@ -313,6 +313,12 @@ FFN_CASES = [
     (1000, 96, 96, 3, 1, True, 30.0),   # every token to one expert, the others empty
     (4700, 64, 32, 1, 1, False, 0),     # more rows than one window of row numbers
     (4300, 32, 64, 2, 2, True, 0),
+    # 256-row tiles: gate/up and dH; dX; a short down projection
+    (8200, 128, 2080, 2, 1, True, 0.3), (8200, 2080, 128, 2, 1, True, 0.3), (8200, 2048, 160, 2, 1, False, 0),
+    # sums long enough for a split tail: gate/up and dH over H (2 and 4 parts), down and dX over F
+    (200, 4128, 64, 2, 1, True, 0), (70, 8256, 96, 2, 2, True, 0), (150, 64, 4160, 2, 2, True, 0.5),
+    # several weight-gradient tiles for each workgroup, experts of 0 to 4 steps
+    (190, 1056, 1120, 12, 2, True, 0.4),
 ]
 
 
@@ -336,17 +342,17 @@ def test_ffn_train(T, H, F, E, k, gathered, skew):
     assert dX is None and torch.equal(dw, got[1]) and torch.equal(dW1, got[2]) and torch.equal(dW2, got[4])
 
 
-def test_ffn_train_accumulate():
-    say("[train] ffn gradients added to f32 and bf16 buffers, and to another path's dX")
-    c = _ffn_case(200, 160, 96, 6, 2, skew=0.7)
-    c["offsets"] = c["offsets"].copy()
+@pytest.mark.parametrize("T,H,F,E,skew", [(200, 160, 96, 6, 0.7), (120, 1056, 800, 11, 0.7)])
+def test_ffn_train_accumulate(T, H, F, E, skew):
+    say(f"[train] ffn gradients added to f32 and bf16 buffers, and to another path's dX: H={H} F={F} E={E}")
+    c = _ffn_case(T, H, F, E, 2, skew=skew)
     d = _dev(c)
     _, ck = _forward(d)
     empty = np.diff(c["offsets"]) == 0
     for dt, half in ((torch.float32, 4 * U), (torch.bfloat16, HALF)):
         g = torch.Generator().manual_seed(4)
         base = {n: torch.randn(d[w].shape, generator=g).to(dt) for n, w in (("dW1", "W1"), ("dW3", "W3"), ("dW2", "W2"))}
-        add = torch.randn(200, 160, generator=g).bfloat16()
+        add = torch.randn(T, H, generator=g).bfloat16()
         bufs = tuple(base[n].cuda() for n in ("dW1", "dW3", "dW2"))
         out = add.cuda()
         got = _backward(d, ck, dW=bufs, dX_add=out)
