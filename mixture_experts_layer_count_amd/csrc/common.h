@@ -380,12 +380,26 @@ struct WeightsProblem {
     moe_dtype c_dt;
     int accumulate;                // add to what C holds
 };
-hipError_t launch_weights_gemm(const WeightsProblem &p, hipStream_t s);
+// dW1 and dW3 (w13), then dW2, in one launch; C0 NULL: that product is left out
+hipError_t launch_weights_gemm(const WeightsProblem &w13, const WeightsProblem &w2, hipStream_t s);
 
-// dX[t] = sum_j rows[assign_row[t k + j]] (+ add[t]) and dw[t k + j] = sum
-// over column tiles of dw_part[tile][row]; assign_row NULL: row t (k == 1).
-// Rows outside [0, min(M, *n_rows)) contribute nothing. dX or dw may be NULL.
-hipError_t launch_gather_grads(const float *rows, const float *dw_part, int n_part, const int32_t *assign_row, int T,
-                               int k, const int32_t *n_rows, int M, int H, const void *add, void *dX, float *dw, hipStream_t s);
+// What the backward pass does token by token; each of dX, dw and x may be NULL.
+// dX[t] = sum_j rows[assign_row[t k + j]] (+ add[t]); dw[t k + j] = sum over
+// column tiles of dw_part[tile][assign_row[t k + j]]; x = the values of the
+// checkpoint xq, xs. assign_row NULL: row t (k == 1). Rows outside
+// [0, min(M, *n_rows)) contribute nothing.
+struct GatherProblem {
+    const int32_t *assign_row, *n_rows;
+    int T, k, M, H;
+    const float *rows;     // [M][H]
+    const uint16_t *add;   // [T][H] or NULL
+    uint16_t *dX;          // [T][H]
+    const float *dw_part;  // [n_part][M]
+    int n_part;
+    float *dw;             // [T][k]
+    const uint8_t *xq, *xs;
+    uint16_t *x;           // [T][H]
+};
+hipError_t launch_gather_grads(const GatherProblem &p, hipStream_t s);
 
 }  // namespace moe

@@ -310,9 +310,23 @@ moe_status moe_ffn_train_backward(const void *dY, const float *topk_w, const int
             d.C = w.rows;
             MOE_TRY(launch_rows_gemm(d, ROWS_DX, w.t.bm, stream));
         }
-        MOE_TRY(launch_gather_grads(w.rows, w.dw_part, rows_gemm_columns(F, ROWS_BACK), assign_row, T, k,
-                                    offsets + G, M, H, dX_add, dX, dtopk_w, stream));
-        if (dW1) MOE_TRY(launch_mx8_unpack(ckpt->xq, ckpt->xs, T, H, MOE_BF16, w.x, stream));
+        GatherProblem g{};
+        g.assign_row = assign_row;
+        g.n_rows = offsets + G;
+        g.T = T;
+        g.k = k;
+        g.M = M;
+        g.H = H;
+        g.rows = w.rows;
+        g.add = static_cast<const uint16_t *>(dX_add);
+        g.dX = static_cast<uint16_t *>(dX);
+        g.dw_part = w.dw_part;
+        g.n_part = rows_gemm_columns(F, ROWS_BACK);
+        g.dw = dtopk_w;
+        g.xq = ckpt->xq;
+        g.xs = ckpt->xs;
+        g.x = dW1 ? w.x : nullptr;
+        MOE_TRY(launch_gather_grads(g, stream));
     }
     // with T == 0 every expert is empty: zeros (or, accumulating, nothing)
     WeightsProblem q{};
@@ -323,32 +337,27 @@ moe_status moe_ffn_train_backward(const void *dY, const float *topk_w, const int
     q.M = M;
     q.c_dt = dw_dt;
     q.accumulate = accumulate;
-    if (dW1) {
-        q.A = w.x;
-        q.a_src = row_src;
-        q.lda = H;
-        q.MD = H;
-        q.B = w.dgu;
-        q.ldb = 2 * F;
-        q.ND = F;
-        q.C0 = dW1;
-        q.C1 = dW3;
-        MOE_TRY(launch_weights_gemm(q, stream));
-    }
-    if (dW2) {
-        q.A = w.hw;
-        q.a_src = nullptr;
-        q.lda = F;
-        q.MD = F;
-        q.B = T > 0 ? static_cast<const uint16_t *>(dY) : w.hw;
-        q.b_src = row_src;
-        q.ldb = H;
-        q.ND = H;
-        q.C0 = dW2;
-        q.C1 = nullptr;
-        MOE_TRY(launch_weights_gemm(q, stream));
-    }
-    return MOE_OK;
+    q.a_src = T > 0 ? row_src : nullptr;
+    q.A = w.x;
+    q.lda = H;
+    q.MD = H;
+    q.B = w.dgu;
+    q.ldb = 2 * F;
+    q.ND = F;
+    q.C0 = dW1;
+    q.C1 = dW3;
+    WeightsProblem q2 = q;
+    q2.a_src = nullptr;
+    q2.b_src = q.a_src;
+    q2.A = w.hw;
+    q2.lda = F;
+    q2.MD = F;
+    q2.B = T > 0 ? static_cast<const uint16_t *>(dY) : w.hw;
+    q2.ldb = H;
+    q2.ND = H;
+    q2.C0 = dW2;
+    q2.C1 = nullptr;
+    return hip_status(launch_weights_gemm(q, q2, stream));
 }
 
 }  // extern "C"

@@ -1,11 +1,14 @@
-// Token gradients of the FFN backward: the sum over a token's k expert rows,
+// What the FFN backward does token by token, between its products: the sum over
+// a token's k expert rows,
 //   dX[t] = sum_j rows[assign_row[t k + j]] (+ add[t]),
-// in fp32 in ascending j, rounded once; and the routing weights' gradients,
-//   dw[t, j] = sum over column tiles of dw_part[tile][assign_row[t k + j]].
+// in fp32 in ascending j, rounded once; the routing weights' gradients,
+//   dw[t, j] = sum over column tiles of dw_part[tile][assign_row[t k + j]];
+// and the token's row read back from its checkpoint for the weight gradients.
 // HBM-bound: fp32 rows read once, bf16 written. One block per token and 2048
-// columns, 8 columns (two 16-byte loads a row) a thread. Rows outside [0, *n_rows)
-// (picks that the permutation left out) contribute nothing.
-#include "common.h"
+// columns, 8 columns (two 16-byte loads a row) a thread; three launches of
+// their own took 7 us more of 24 (8 experts, T 1536, k 2, H 640). Rows outside
+// [0, *n_rows) (picks that the permutation left out) contribute nothing.
+#include "mx8.h"
 
 namespace moe {
 
@@ -13,69 +16,67 @@ MOE_BOUNDS_FILE(train_gather)
 
 namespace {
 
-__global__ __launch_bounds__(256) void gather_grads_kernel(const float *rows, const int32_t *assign_row, int k,
-                                                           const int32_t *n_rows, int M, int H, const uint16_t *add, uint16_t *dX) {
+__global__ __launch_bounds__(256) void gather_grads_kernel(GatherProblem p) {
     const int t = blockIdx.x, c = (blockIdx.y * 256 + threadIdx.x) * 8;
-    if (c >= H) return;
-    M = min(M, *n_rows);
+    const int M = min(p.M, *p.n_rows);
+    const long long o = (long long)t * p.H + c;
+    u32x2 code;
+    float scale;
+    if (p.x && c < p.H) {  // on their way while the rows are summed
+        code = *reinterpret_cast<const u32x2 *>(p.xq + o);
+        scale = mx8::scale_of(p.xs[o / mx8::kGroup]);
+    }
+    if (p.dw && blockIdx.y == 0 && (int)threadIdx.x < p.k) {
+        const long long a = (long long)t * p.k + threadIdx.x;
+        const int r = p.assign_row ? p.assign_row[a] : t;
+        float v = 0.0f;
+        if (r >= 0 && r < M)
+            for (int q = 0; q < p.n_part; ++q) v += p.dw_part[(long long)q * p.M + r];
+        p.dw[a] = v;
+    }
+    if (c >= p.H) return;
+    if (p.x) {
+        const f32x4 a = mx8::values4(code[0], scale), b = mx8::values4(code[1], scale);
+        *reinterpret_cast<u32x4 *>(p.x + o) = u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
+                                                    pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])};
+    }
+    if (!p.dX) return;
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    for (int j = 0; j < k; ++j) {
-        const int r = assign_row ? assign_row[(long long)t * k + j] : t;
+    for (int j = 0; j < p.k; ++j) {
+        const int r = p.assign_row ? p.assign_row[(long long)t * p.k + j] : t;
         if (r < 0 || r >= M) continue;
-        const f32x4 *p = reinterpret_cast<const f32x4 *>(rows + (long long)r * H + c);
-        const f32x4 a = p[0], b = p[1];
+        const f32x4 *row = reinterpret_cast<const f32x4 *>(p.rows + (long long)r * p.H + c);
+        const f32x4 a = row[0], b = row[1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[i] += a[i];
             v[4 + i] += b[i];
         }
     }
-    const long long o = (long long)t * H + c;
-    if (add) {
-        const u32x4 s = *reinterpret_cast<const u32x4 *>(add + o);
+    if (p.add) {
+        const u32x4 s = *reinterpret_cast<const u32x4 *>(p.add + o);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[2 * i] += bf16_lo(s[i]);
             v[2 * i + 1] += bf16_hi(s[i]);
         }
     }
-    *reinterpret_cast<u32x4 *>(dX + o) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
-}
-
-__global__ __launch_bounds__(256) void gather_dw_kernel(const float *part, int n_part, const int32_t *assign_row,
-                                                        long long A, const int32_t *n_rows, int M, float *dw) {
-    const long long a = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (a >= A) return;
-    const int r = assign_row ? assign_row[a] : (int)a;
-    float v = 0.0f;
-    if (r >= 0 && r < min(M, *n_rows))
-        for (int q = 0; q < n_part; ++q) v += part[(long long)q * M + r];
-    dw[a] = v;
+    *reinterpret_cast<u32x4 *>(p.dX + o) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                 pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
 }
 
 }  // namespace
 
-hipError_t launch_gather_grads(const float *rows, const float *dw_part, int n_part, const int32_t *assign_row, int T,
-                               int k, const int32_t *n_rows, int M, int H, const void *add, void *dX, float *dw, hipStream_t s) {
-    if (T < 1 || k < 1 || !n_rows || H % 8 || (!assign_row && k != 1)) return hipErrorInvalidValue;
-    if (dX) {
-        if (!rows) return hipErrorInvalidValue;
-        hipLaunchKernelGGL(gather_grads_kernel, dim3((unsigned)T, (unsigned)((H + 2047) / 2048)), dim3(256), 0, s, rows,
-                           assign_row, k, n_rows, M, H, static_cast<const uint16_t *>(add), static_cast<uint16_t *>(dX));
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    if (dw) {
-        if (!dw_part) return hipErrorInvalidValue;
-        const long long A = (long long)T * k;
-        hipLaunchKernelGGL(gather_dw_kernel, dim3((unsigned)((A + 255) / 256)), dim3(256), 0, s, dw_part, n_part,
-                           assign_row, A, n_rows, M, dw);
-        return hipGetLastError();
-    }
-    return hipSuccess;
+hipError_t launch_gather_grads(const GatherProblem &p, hipStream_t s) {
+    if (p.T < 1 || p.k < 1 || p.k > 256 || !p.n_rows || p.H % 32 || (!p.assign_row && p.k != 1) || (p.dX && !p.rows) ||
+        (p.dw && !p.dw_part) || (p.x && (!p.xq || !p.xs)))
+        return hipErrorInvalidValue;
+    if (!p.dX && !p.dw && !p.x) return hipSuccess;
+    const unsigned columns = p.dX || p.x ? (unsigned)((p.H + 2047) / 2048) : 1;
+    hipLaunchKernelGGL(gather_grads_kernel, dim3((unsigned)p.T, columns), dim3(256), 0, s, p);
+    return hipGetLastError();
 }
 
 }  // namespace moe

@@ -2,7 +2,7 @@
 // Weight gradients of the grouped FFN: for every expert g,
 //   dW_g[m][n] = sum over its rows r of A(r)[m] B(r)[n]
 // in one launch: dW1 and dW3 (A = the token rows read back from their
-// checkpoint, B = [dg | du]) or dW2 (A = w h, B = dY), the token operand
+// checkpoint, B = [dg | du]), then dW2 (A = w h, B = dY), the token operand
 // gathered by row. The sum runs over rows, so both operands are contiguous
 // across it: LDS tiles keep the matrices' [row][column] layout and both MFMA
 // operands are read with ds_read_b64_tr_b16.
@@ -79,68 +79,79 @@ struct WItem {
     __device__ __forceinline__ int steps() const { return hi > lo ? (hi - lo + 31) >> 5 : 1; }
 };
 
+// one product and its tile counts; its runs follow those of the one before it
+struct WWork {
+    WeightsProblem p;
+    int nM, nN, items, first_run;
+    Divisor group_tiles, band_tiles;
+};
+struct WPair {
+    WWork w[2];
+    Divisor gk;
+};
+
+// ---- experts by falling row count (equal counts by index), to LDS ----
+__device__ __forceinline__ void sort_experts(const WeightsProblem &p, uint8_t *lds) {
+    uint16_t *order = reinterpret_cast<uint16_t *>(lds + WRing::order);
+    int *range = reinterpret_cast<int *>(lds + WRing::range);
+    const int tid = threadIdx.x;
+    int *count = reinterpret_cast<int *>(lds);
+    int lo[kMaxGroups / 512], hi[kMaxGroups / 512];
+#pragma unroll
+    for (int i = 0; i < kMaxGroups / 512; ++i) {
+        const int g = tid + 512 * i;
+        if (g < p.G) {
+            lo[i] = min(max(p.offsets[g], 0), p.M);
+            hi[i] = min(max(p.offsets[g + 1], lo[i]), p.M);
+            count[g] = hi[i] - lo[i];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMaxGroups / 512; ++i) {
+        const int g = tid + 512 * i;
+        if (g < p.G) {
+            const int mine = hi[i] - lo[i];
+            int rank = 0;
+            for (int o = 0; o < p.G; ++o) {
+                const int c = count[o];
+                rank += (c > mine) | ((c == mine) & (o < g));
+            }
+            order[rank] = (uint16_t)g;
+            range[2 * rank] = lo[i];
+            range[2 * rank + 1] = hi[i];
+        }
+    }
+    __syncthreads();
+}
+
 template <bool F32, bool ACC, Gather GATHER>
-__global__ __launch_bounds__(512, 1) void weights_gemm_kernel(WeightsProblem p, int nM, int nN, Divisor gk,
-                                                              Divisor group_tiles, Divisor band_tiles) {
+__device__ __forceinline__ void weights_gemm(const WWork &work, const Divisor &gk, uint8_t *lds) {
     typedef WRing R;
     constexpr int S = R::S, MI = R::MI, NB = R::NB, NC = R::nC, NR = 2 * (MI + NB);
     constexpr int kStores = F32 ? MI * NB : MI * NB / 2;  // a finished tile's, per wavefront
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[R::lds];
-    uint16_t *order = reinterpret_cast<uint16_t *>(lds + R::order);
-    int *range = reinterpret_cast<int *>(lds + R::range);
+    const WeightsProblem &p = work.p;
+    const uint16_t *order = reinterpret_cast<const uint16_t *>(lds + R::order);
+    const int *range = reinterpret_cast<const int *>(lds + R::range);
 
     const int tid = threadIdx.x;
     const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wr = w / 4, wc = w % 4;
     const int i16 = lane & 15, gq = lane >> 4;
 
-    // ---- experts by falling row count (equal counts by index) ----
-    {
-        int *count = reinterpret_cast<int *>(lds);
-        int lo[kMaxGroups / 512], hi[kMaxGroups / 512];
-#pragma unroll
-        for (int i = 0; i < kMaxGroups / 512; ++i) {
-            const int g = tid + 512 * i;
-            if (g < p.G) {
-                lo[i] = min(max(p.offsets[g], 0), p.M);
-                hi[i] = min(max(p.offsets[g + 1], lo[i]), p.M);
-                count[g] = hi[i] - lo[i];
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kMaxGroups / 512; ++i) {
-            const int g = tid + 512 * i;
-            if (g < p.G) {
-                const int mine = hi[i] - lo[i];
-                int rank = 0;
-                for (int o = 0; o < p.G; ++o) {
-                    const int c = count[o];
-                    rank += (c > mine) | ((c == mine) & (o < g));
-                }
-                order[rank] = (uint16_t)g;
-                range[2 * rank] = lo[i];
-                range[2 * rank + 1] = hi[i];
-            }
-        }
-        __syncthreads();
-    }
-
     // ---- this workgroup's items: number `slot` of every run that its XCD takes ----
-    const int mats = p.C1 ? 2 : 1, nT = nN * mats, per_group = nM * nT;
-    const int items = p.G * per_group;  // the launcher keeps it below 2^31
+    const int nM = work.nM, nN = work.nN, nT = nN * (p.C1 ? 2 : 1), per_group = nM * nT, items = work.items;
     const int xcd = blockIdx.x % kXcds, slot = blockIdx.x / kXcds;
-    auto item_id = [&](int j) {
-        const int run = j * kXcds + ((j & 1) ? kXcds - 1 - xcd : xcd);
-        return (long long)run * kBlocksPerXcd + slot;
-    };
+    auto run_of = [&](int j) { return j * kXcds + ((j & 1) ? kXcds - 1 - xcd : xcd) - work.first_run; };
+    const int j0 = work.first_run / kXcds + (run_of(work.first_run / kXcds) < 0);  // its first of this product
+    auto item_id = [&](int j) { return (long long)run_of(j0 + j) * kBlocksPerXcd + slot; };
     // item j; past the last one an item without rows (copied, never multiplied)
     auto item_at = [&](int j) {
         WItem it{0, 0, 0, 0, 0, 0};
         const long long id = item_id(j);
         if (id < items) {
-            const int e = (int)group_tiles((uint32_t)id), t = (int)id - e * per_group;
+            const int e = (int)work.group_tiles((uint32_t)id), t = (int)id - e * per_group;
             it.g = __builtin_amdgcn_readfirstlane((int)order[e]);
-            const int band = (int)band_tiles(t), in = t - band * kBand * nT, deep = min(kBand, nM - kBand * band);
+            const int band = (int)work.band_tiles(t), in = t - band * kBand * nT, deep = min(kBand, nM - kBand * band);
             static_assert(kBand == 4, "in / deep");
             const int n = deep == 4 ? in >> 2 : deep == 3 ? (int)(((uint64_t)in * 0xaaaaaaabu) >> 33) : in >> (deep - 1);
             it.m0 = 256 * (kBand * band + in - n * deep);
@@ -437,34 +448,64 @@ __global__ __launch_bounds__(512, 1) void weights_gemm_kernel(WeightsProblem p, 
         left = mi.steps();
         mn = item_at(mj + 1);
     }
-    wait_vm<0>();  // the copies past the last item land before the workgroup ends
+    wait_vm<0>();  // the copies past the last item land before the ring is used again or the workgroup ends
+}
+
+template <bool F32, bool ACC, bool GATHERED>
+__global__ __launch_bounds__(512, 1) void weights_gemm_kernel(WPair q) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[WRing::lds];
+    sort_experts(q.w[0].p, lds);
+    weights_gemm<F32, ACC, GATHERED ? GATHER_A : GATHER_NONE>(q.w[0], q.gk, lds);
+    __syncthreads();
+    weights_gemm<F32, ACC, GATHERED ? GATHER_B : GATHER_NONE>(q.w[1], q.gk, lds);
 }
 
 }  // namespace
 }  // namespace tiled
 
-hipError_t launch_weights_gemm(const WeightsProblem &p, hipStream_t s) {
+hipError_t launch_weights_gemm(const WeightsProblem &w13, const WeightsProblem &w2, hipStream_t s) {
     using namespace tiled;
-    if (!p.A || !p.B || !p.offsets || !p.C0 || p.G < 1 || p.G > kMaxGroups || p.M < 0 || p.MD < 32 || p.MD % 32 ||
-        p.ND < 32 || p.ND % 32 || p.gk < 1 || p.gk > 64 || (p.a_src && p.b_src) || p.lda < p.MD ||
-        p.ldb < (p.C1 ? 2 : 1) * p.ND ||
-        ((p.a_src || p.b_src) && (p.src_rows < 1 || 2LL * p.src_rows * (p.a_src ? p.lda : p.ldb) > gather_max_bytes)) || (p.c_dt != MOE_F32 && p.c_dt != MOE_BF16))
-        return hipErrorInvalidValue;
-    const int nM = (p.MD + 255) / 256, nN = (p.ND + 255) / 256;
-    const long long items = (long long)p.G * nM * nN * (p.C1 ? 2 : 1);
-    if (items > 0x7fffffffLL) return hipErrorInvalidValue;
-    const int nT = nN * (p.C1 ? 2 : 1);
+    WPair q{{{w13, 0, 0, 0, 0, 1, 1}, {w2, 0, 0, 0, 0, 1, 1}}, w13.gk};
+    long long runs = 0;
+    for (WWork &w : q.w) {
+        const WeightsProblem &p = w.p;
+        if (!p.offsets || p.offsets != w13.offsets || p.G != w13.G || p.M != w13.M || p.gk != w13.gk ||
+            p.c_dt != w13.c_dt || p.accumulate != w13.accumulate)
+            return hipErrorInvalidValue;
+        w.first_run = (int)runs;
+        if (!p.C0) continue;  // not asked for: no items
+        if (!p.A || !p.B || p.G < 1 || p.G > kMaxGroups || p.M < 0 || p.MD < 32 || p.MD % 32 || p.ND < 32 ||
+            p.ND % 32 || p.gk < 1 || p.gk > 64 || p.lda < p.MD || p.ldb < (p.C1 ? 2 : 1) * p.ND ||
+            (p.c_dt != MOE_F32 && p.c_dt != MOE_BF16))
+            return hipErrorInvalidValue;
+        // the gathered operand: A of the first product, B of the second
+        const bool first = &w == q.w;
+        if ((first ? p.b_src : p.a_src) || (w13.a_src == nullptr) != (w2.b_src == nullptr) ||
+            (w13.a_src && (p.src_rows < 1 || 2LL * p.src_rows * (first ? p.lda : p.ldb) > gather_max_bytes)))
+            return hipErrorInvalidValue;
+        const int nT = (p.ND + 255) / 256 * (p.C1 ? 2 : 1);
+        w.nM = (p.MD + 255) / 256;
+        w.nN = (p.ND + 255) / 256;
+        const long long items = (long long)p.G * w.nM * nT;
+        if (items > 0x7fffffffLL) return hipErrorInvalidValue;
+        w.items = (int)items;
+        w.group_tiles = Divisor(w.nM * nT);
+        w.band_tiles = Divisor(kBand * nT);
+        runs += (items + kBlocksPerXcd - 1) / kBlocksPerXcd;
+    }
+    if (runs == 0) return hipSuccess;
     auto launch = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3(kXcds * kBlocksPerXcd), dim3(512), 0, s, p, nM, nN, Divisor(p.gk),
-                           Divisor(nM * nT), Divisor(kBand * nT));
+        hipLaunchKernelGGL(kernel, dim3(kXcds * kBlocksPerXcd), dim3(512), 0, s, q);
     };
-    const bool f32 = p.c_dt == MOE_F32;
-#define MOE_WEIGHTS(G)                                                                                           \
-    (f32 ? (p.accumulate ? launch(weights_gemm_kernel<true, true, G>) : launch(weights_gemm_kernel<true, false, G>)) \
-         : (p.accumulate ? launch(weights_gemm_kernel<false, true, G>) : launch(weights_gemm_kernel<false, false, G>)))
-    if (p.a_src) MOE_WEIGHTS(GATHER_A);
-    else if (p.b_src) MOE_WEIGHTS(GATHER_B);
-    else MOE_WEIGHTS(GATHER_NONE);
+#define MOE_WEIGHTS(F32, ACC)                                                         \
+    (w13.a_src ? launch(weights_gemm_kernel<F32, ACC, true>) : launch(weights_gemm_kernel<F32, ACC, false>))
+    if (w13.c_dt == MOE_F32) {
+        if (w13.accumulate) MOE_WEIGHTS(true, true);
+        else MOE_WEIGHTS(true, false);
+    } else {
+        if (w13.accumulate) MOE_WEIGHTS(false, true);
+        else MOE_WEIGHTS(false, false);
+    }
 #undef MOE_WEIGHTS
     return hipGetLastError();
 }
