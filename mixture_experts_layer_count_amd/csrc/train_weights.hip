@@ -68,6 +68,18 @@ struct Divisor {
     __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (uint32_t)(((uint64_t)n * mul) >> shift); }
 };
 
+// Two 16-byte pieces of row l16 (lane % 16) in every lane -> of row l16 % 8,
+// then of row 8 + l16 % 8: the first piece in lanes below 8, the second in the
+// others. A row's 8 lanes then store a whole 128-byte line at a time.
+__device__ __forceinline__ void whole_lines(u32x4 &a, u32x4 &b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t x = a[i];
+        a[i] = __builtin_amdgcn_update_dpp(x, b[i], 0x128, 0xf, 0xc, false);     // row_ror:8
+        b[i] = __builtin_amdgcn_update_dpp(b[i], x, 0x128, 0xf, 0x3, false);
+    }
+}
+
 // which operand's rows are gathered
 enum Gather { GATHER_NONE, GATHER_A, GATHER_B };
 
@@ -144,25 +156,39 @@ __device__ __forceinline__ void weights_gemm(const WWork &work, const Divisor &g
     auto run_of = [&](int j) { return j * kXcds + ((j & 1) ? kXcds - 1 - xcd : xcd) - work.first_run; };
     const int j0 = work.first_run / kXcds + (run_of(work.first_run / kXcds) < 0);  // its first of this product
     auto item_id = [&](int j) { return (long long)run_of(j0 + j) * kBlocksPerXcd + slot; };
-    // item j; past the last one an item without rows (copied, never multiplied)
-    auto item_at = [&](int j) {
-        WItem it{0, 0, 0, 0, 0, 0};
-        const long long id = item_id(j);
+    if (item_id(0) >= items) return;
+    // 64 items from `base` on, one a lane (read back lane by lane: through LDS
+    // and scalar divisions each change of items took 0.8 us); past the last one
+    // items without rows (copied, never multiplied)
+    int base = 0, l_lo, l_hi, l_tile, l_g;
+    auto load_items = [&]() {
+        l_lo = l_hi = l_tile = l_g = 0;
+        const long long id = item_id(base + lane);
         if (id < items) {
             const int e = (int)work.group_tiles((uint32_t)id), t = (int)id - e * per_group;
-            it.g = __builtin_amdgcn_readfirstlane((int)order[e]);
             const int band = (int)work.band_tiles(t), in = t - band * kBand * nT, deep = min(kBand, nM - kBand * band);
             static_assert(kBand == 4, "in / deep");
             const int n = deep == 4 ? in >> 2 : deep == 3 ? (int)(((uint64_t)in * 0xaaaaaaabu) >> 33) : in >> (deep - 1);
-            it.m0 = 256 * (kBand * band + in - n * deep);
-            it.half = n >= nN ? 1 : 0;
-            it.n0 = 256 * (n - it.half * nN);
-            it.lo = __builtin_amdgcn_readfirstlane(range[2 * e]);
-            it.hi = __builtin_amdgcn_readfirstlane(range[2 * e + 1]);
+            l_g = order[e];
+            l_lo = range[2 * e];
+            l_hi = range[2 * e + 1];
+            l_tile = (kBand * band + in - n * deep) << 16 | n;
         }
+    };
+    auto item_at = [&](int j) {
+        WItem it;
+        it.lo = __builtin_amdgcn_readlane(l_lo, j - base);
+        it.hi = __builtin_amdgcn_readlane(l_hi, j - base);
+        it.g = __builtin_amdgcn_readlane(l_g, j - base);
+        const uint32_t tile = __builtin_amdgcn_readlane(l_tile, j - base);
+        const int n = tile & 0xffff;
+        it.half = n >= nN ? 1 : 0;
+        it.m0 = 256 * (int)(tile >> 16);
+        it.n0 = 256 * (n - it.half * nN);
         return it;
     };
-    if (item_id(0) >= items) return;
+    load_items();
+    int mj = 0;  // number of the multiplied item
 
     // ---- the copied position: copy q of an operand and wavefront w fills rows
     // 4 w + 2 q + lane / 32 of the step, the lane's 16-byte chunk being the one
@@ -202,8 +228,8 @@ __device__ __forceinline__ void weights_gemm(const WWork &work, const Divisor &g
         if (GATHER == GATHER_B) b_bytes = (uint32_t)p.src_rows * ldb2 - 2u * ci.n0;
     };
     // the gathered operand's rows: byte offsets of the current window's rows
-    // (16 steps x the wavefront's 4) lie in LDS; the next window's row numbers
-    // are on their way there. newer: vector-memory operations since they were
+    // (16 steps x the wavefront's 4), one a lane; the next window's row numbers
+    // are on their way to LDS. newer: vector-memory operations since they were
     // sent for
     const int32_t *src = GATHER == GATHER_A ? p.a_src : p.b_src;
     int buf = 0, newer = 0;
@@ -213,22 +239,24 @@ __device__ __forceinline__ void weights_gemm(const WWork &work, const Divisor &g
         const int r = it.lo + 32 * (k + (lane >> 2)) + 4 * w + (lane & 3);
         copy4(src + min(r, it.hi - 1), my_rows + b * R::rows_bytes);
     };
+    uint32_t l_row = kNoRow;
     auto take_rows = [&]() {
         if (GATHER == GATHER_NONE) return;
-        uint32_t *row = reinterpret_cast<uint32_t *>(my_rows + buf * R::rows_bytes) + lane;
-        uint32_t got = gk(*row);
+        uint32_t got = gk(*(reinterpret_cast<const uint32_t *>(my_rows + buf * R::rows_bytes) + lane));
         const int r = ci.lo + 32 * ((ck & -R::window) + (lane >> 2)) + 4 * w + (lane & 3);
         if (r < ci.hi && MOE_BOUNDS_FAIL(got < (uint32_t)p.src_rows, BOUNDS_A_ROW)) got = 0;
-        *row = r < ci.hi ? got * (GATHER == GATHER_A ? lda2 : ldb2) : kNoRow;
-        wave_lds_sync();
+        l_row = r < ci.hi ? got * (GATHER == GATHER_A ? lda2 : ldb2) : kNoRow;
     };
     uint32_t row_off[2] = {0, 0};  // of the gathered operand's two copies of the step
     auto step_rows = [&]() {
         if (GATHER == GATHER_NONE) return;
-        const uint32_t *row = reinterpret_cast<const uint32_t *>(my_rows + buf * R::rows_bytes) +
-                              4 * (ck & (R::window - 1)) + (lane >> 5);
-        row_off[0] = row[0];
-        row_off[1] = row[2];
+        const int first = 4 * (ck & (R::window - 1));
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const uint32_t lo = __builtin_amdgcn_readlane(l_row, first + 2 * q);
+            const uint32_t hi = __builtin_amdgcn_readlane(l_row, first + 2 * q + 1);
+            row_off[q] = lane < 32 ? lo : hi;
+        }
     };
     // to the next step: at a window's end the next window becomes current and
     // the one after it is sent for
@@ -255,6 +283,10 @@ __device__ __forceinline__ void weights_gemm(const WWork &work, const Divisor &g
                 ++cj;
                 ck = 0;
                 cnk = ci.steps();
+                if (cj + 1 - base >= 64) {
+                    base = mj;  // at most S + 1 items behind
+                    load_items();
+                }
                 cn = item_at(cj + 1);
                 set_item();
             }
@@ -338,32 +370,42 @@ __device__ __forceinline__ void weights_gemm(const WWork &work, const Divisor &g
         for (int m = 0; m < MI; ++m) {
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int j = 0; j < NB; j += F32 ? 1 : 2) {
-                const int row = 16 * m + l16, col = 16 * j + (F32 ? 4 * lq : pair_column(lq));
-                int off = (row * nd + col) * size;
-                asm volatile("" : "+v"(off));  // formed first: the choice is then no branch
-                off = (row < rows) & (col < cols) ? off : kOut;
-                if constexpr (F32) {
-                    f32x4 v = acc[m][j];
-                    if (ACC && off != kOut) v += *reinterpret_cast<const f32x4 *>(C + off);
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rsrc, off, 0, 0);
-                    acc[m][j] = f32x4{};
-                } else {
-                    f32x4 v0 = acc[m][j], v1 = acc[m][j + 1];
-                    if (ACC) {
-                        // what C holds, in the accumulators' layout
-                        f32x4 *const v[2] = {&v0, &v1};
+            for (int j = 0; j < NB; j += F32 ? 2 : 4) {
+                f32x4 v[4];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int c = 16 * (j + i) + 4 * lq;
-                            if (row < rows && c < cols) {
-                                const u32x2 old = *reinterpret_cast<const u32x2 *>(C + (row * nd + c) * size);
-                                *v[i] += f32x4{bf16_lo(old[0]), bf16_hi(old[0]), bf16_lo(old[1]), bf16_hi(old[1])};
-                            }
+                for (int i = 0; i < (F32 ? 2 : 4); ++i) {
+                    v[i] = acc[m][j + i];
+                    acc[m][j + i] = f32x4{};
+                    if (!ACC) continue;
+                    // what C holds, in the accumulators' layout
+                    const int row = 16 * m + l16, c = 16 * (j + i) + 4 * lq;
+                    if (row < rows && c < cols) {
+                        const char *old = C + (row * nd + c) * size;
+                        if constexpr (F32) {
+                            v[i] += *reinterpret_cast<const f32x4 *>(old);
+                        } else {
+                            const u32x2 o = *reinterpret_cast<const u32x2 *>(old);
+                            v[i] += f32x4{bf16_lo(o[0]), bf16_hi(o[0]), bf16_lo(o[1]), bf16_hi(o[1])};
                         }
                     }
-                    __builtin_amdgcn_raw_buffer_store_b128(pair_columns(v0, v1), rsrc, off, 0, 0);
-                    acc[m][j] = acc[m][j + 1] = f32x4{};
+                }
+                u32x4 x0, x1;
+                if constexpr (F32) {
+                    x0 = __builtin_bit_cast(u32x4, v[0]);
+                    x1 = __builtin_bit_cast(u32x4, v[1]);
+                } else {
+                    x0 = pair_columns(v[0], v[1]);
+                    x1 = pair_columns(v[2], v[3]);
+                }
+                whole_lines(x0, x1);
+                const int col = 16 * j + (F32 ? 16 * (l16 >> 3) + 4 * lq : 32 * (l16 >> 3) + pair_column(lq));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int row = 16 * m + 8 * i + (l16 & 7);
+                    int off = (row * nd + col) * size;
+                    asm volatile("" : "+v"(off));  // formed first: the choice is then no branch
+                    off = (row < rows) & (col < cols) ? off : kOut;
+                    __builtin_amdgcn_raw_buffer_store_b128(i ? x1 : x0, rsrc, off, 0, 0);
                 }
             }
         }
@@ -393,7 +435,7 @@ __device__ __forceinline__ void weights_gemm(const WWork &work, const Divisor &g
 
     // ---- the multiplied position ----
     WItem mi = item_at(0), mn = item_at(1);
-    int mj = 0, left = mi.steps(), stage = 0;
+    int left = mi.steps(), stage = 0;
     int relax = 0;  // steps whose awaited copies are older than a finished tile's stores
     auto step = [&](Frag &cur, Frag &nxt) {
         const int nstage = stage + 1 == S ? 0 : stage + 1;
