@@ -228,6 +228,18 @@ __device__ __forceinline__ u32x4 pair_columns(const f32x4 &x0, const f32x4 &x1) 
 }
 __device__ __forceinline__ int pair_column(int gq) { return 16 * (gq & 1) + 8 * (gq >> 1); }
 
+// Two 16-byte pieces of row l16 (lane % 16) in every lane -> of row l16 % 8,
+// then of row 8 + l16 % 8: the first piece in lanes below 8, the second in the
+// others. A row's 8 lanes then store 128 contiguous bytes at a time.
+__device__ __forceinline__ void whole_lines(u32x4 &a, u32x4 &b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t x = a[i];
+        a[i] = __builtin_amdgcn_update_dpp(x, b[i], 0x128, 0xf, 0xc, false);     // row_ror:8
+        b[i] = __builtin_amdgcn_update_dpp(b[i], x, 0x128, 0xf, 0x3, false);
+    }
+}
+
 // Map this workgroup to (row tile, column tile) of the work order; false for
 // surplus workgroups. Work order: for each group, for each band of gn column
 // tiles, the group's row tiles x the band's column tiles (column fastest).

@@ -66,10 +66,10 @@ struct RowsRing {
     static constexpr int nB = kRowsBN / 64;
     static constexpr int per_tile = nA + nB;
     static constexpr int MI = BM / 32;   // 16-row blocks per wavefront
-    // BACK's staging per wavefront: a 16 x 64 block of each output (bf16,
-    // padded rows) and of each code matrix
-    static constexpr int old = 64 + 8, cld = 64 + 16;
-    static constexpr int stg = 3 * 16 * old * 2 + 2 * 16 * cld;
+    // BACK's staging per wavefront: a 16 x 64 block of each code matrix (padded
+    // rows) and its scale bytes
+    static constexpr int cld = 64 + 16;
+    static constexpr int stg = 2 * 16 * cld + 64;
     static constexpr int dw = 8 * stg;   // [4][BM] floats behind it
     // GATE_UP's: rows of 128 bf16 h, then of both projections' 128 codes
     // (padded), then of 4 scale bytes each
@@ -352,29 +352,41 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
         }
         __syncthreads();  // the flag has been read: the LDS is free
     }
+    // a 16 x 64 block of bf16 results, whole lines (of 64-byte pieces each is two
+    // requests to L2)
+    auto store_lines = [&](uint16_t *C, int ld, int m, const f32x4 (&x)[NB]) {
+        u32x4 v[2] = {pair_columns(x[0], x[1]), pair_columns(x[2], x[3])};
+        whole_lines(v[0], v[1]);
+        const int col = n0 + 64 * wc + 32 * (i16 >> 3) + pair_column(gq);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = row0 + wr * (BM / 2) + 16 * m + 8 * i + (i16 & 7);
+            if (row < row_end && col < p.N) *reinterpret_cast<u32x4 *>(C + (long long)row * ld + col) = v[i];
+        }
+    };
     if constexpr (USE == ROWS_DX) {
 #pragma unroll
         for (int m = 0; m < MI; ++m) {
-            const int row = row0 + wr * (BM / 2) + 16 * m + i16;
-            if (row >= row_end) continue;
+            if (m >= nblk) continue;
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                const int col = n0 + 64 * wc + 16 * j + 4 * gq;
-                if (col < p.N)
-                    *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(p.C) + (long long)row * p.N + col) = acc[m][j];
+            for (int j = 0; j < NB; j += 2) {
+                u32x4 v[2] = {__builtin_bit_cast(u32x4, acc[m][j]), __builtin_bit_cast(u32x4, acc[m][j + 1])};
+                whole_lines(v[0], v[1]);
+                const int col = n0 + 64 * wc + 16 * (j + (i16 >> 3)) + 4 * gq;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int row = row0 + wr * (BM / 2) + 16 * m + 8 * i + (i16 & 7);
+                    if (row < row_end && col < p.N)
+                        *reinterpret_cast<u32x4 *>(reinterpret_cast<float *>(p.C) + (long long)row * p.N + col) = v[i];
+                }
             }
         }
     } else if constexpr (USE == ROWS_DOWN) {
         uint16_t *C = reinterpret_cast<uint16_t *>(p.C);
 #pragma unroll
         for (int m = 0; m < MI; ++m) {
-            const int row = row0 + wr * (BM / 2) + 16 * m + i16;
-#pragma unroll
-            for (int j = 0; j < NB; j += 2) {
-                const u32x4 v = pair_columns(acc[m][j], acc[m][j + 1]);
-                const int col = n0 + 64 * wc + 16 * j + pair_column(gq);
-                if (row < row_end && col < p.N) *reinterpret_cast<u32x4 *>(C + (long long)row * p.N + col) = v;
-            }
+            if (m >= nblk) continue;
+            store_lines(C, p.N, m, acc[m]);
         }
     } else if constexpr (USE == ROWS_GATE_UP) {
         __syncthreads();
@@ -435,105 +447,87 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
                     lds[R::scales + r * 8 + 4 * half + q];
         }
     } else {
-        __syncthreads();  // every wavefront is done with the ring
-        // ---- SwiGLU backward, 16 rows at a time, through the wavefront's
-        // staging area (its LDS operations complete in order): whole 128-byte
-        // lines out (64-byte pieces straight from the registers, as DOWN
-        // stores, took 1 us more a tile of 20: three outputs) ----
-        uint8_t *stg = lds + w * R::stg;
-        uint16_t *so = reinterpret_cast<uint16_t *>(stg);
-        uint8_t *sc = stg + 3 * 16 * R::old * 2;
+        // ---- SwiGLU backward, 16 rows at a time; the codes come kAhead blocks
+        // ahead of their use (one ahead each block waited for memory: 20 us a
+        // tile) and change from rows of 16 to the accumulators' layout through
+        // the wavefront's staging area ----
+        constexpr int kAhead = MI < 4 ? MI : 4;
+        uint8_t *sc = lds + w * R::stg, *ss = sc + 2 * 16 * R::cld;
         float *sdw = reinterpret_cast<float *>(lds + R::dw);
-        const int c0 = n0 + 64 * wc;
+        const int c0 = n0 + 64 * wc, base = row0 + wr * (BM / 2);
         // code loads: lane -> row lane / 4 of the block, 16 codes at 16 (lane % 4)
+        // and one of its scale bytes: g's two, then u's
         const int lr = lane >> 2, lc = 16 * (lane & 3);
-        const int ngr = p.N >> 5;
         struct Codes {
             u32x4 g, u;
-            uint8_t gs[2], us[2];
-            float w;
+            uint8_t s;
         };
-        auto load = [&](Codes &c, int m) {
-            const int base = row0 + wr * (BM / 2) + 16 * m;
-            const int r = base + lr;
+        Codes codes[kAhead];
+        auto load = [&](int m) {
+            Codes &c = codes[m % kAhead];
+            const int r = base + 16 * m + lr, group = (c0 >> 5) + (lane & 1);
             c.g = c.u = u32x4{0, 0, 0, 0};
-            if (r < row_end && c0 + lc < p.N) {
+            c.s = 0;
+            if (r >= row_end) return;
+            if (c0 + lc < p.N) {
                 const long long o = (long long)r * p.N + c0 + lc;
                 c.g = *reinterpret_cast<const u32x4 *>(p.gq + o);
                 c.u = *reinterpret_cast<const u32x4 *>(p.uq + o);
             }
-            const int rs = base + i16;
-            c.w = 0.0f;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) c.gs[q] = c.us[q] = 0;
-            if (rs < row_end) {
-                c.w = p.topk_w ? p.topk_w[p.w_src ? p.w_src[rs] : rs] : 1.0f;
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    if (c0 + 32 * q < p.N) {
-                        const long long o = (long long)rs * ngr + (c0 >> 5) + q;
-                        c.gs[q] = p.gs[o];
-                        c.us[q] = p.us[o];
-                    }
-            }
+            if (group < p.N >> 5) c.s = (lane & 2 ? p.us : p.gs)[(long long)r * (p.N >> 5) + group];
         };
-        Codes cur;
-        load(cur, 0);
+        // the wavefront's routing weights, one row a lane
+        float row_w[(MI + 3) / 4];
+#pragma unroll
+        for (int i = 0; i < (MI + 3) / 4; ++i) {
+            const int r = base + 64 * i + lane;
+            row_w[i] = 0.0f;
+            if (r < row_end && 64 * i + lane < BM / 2) row_w[i] = p.topk_w ? p.topk_w[p.w_src ? p.w_src[r] : r] : 1.0f;
+        }
+#pragma unroll
+        for (int m = 0; m < kAhead; ++m) load(m);
+        __syncthreads();  // every wavefront is done with the ring
 #pragma unroll
         for (int m = 0; m < MI; ++m) {
             if (m >= nblk) {  // no rows of the group
                 if (gq == 0) sdw[wc * BM + wr * (BM / 2) + 16 * m + i16] = 0.0f;
                 continue;
             }
-            Codes nxt = cur;
-            if (m + 1 < MI) load(nxt, m + 1);
+            const Codes &cur = codes[m % kAhead];
             *reinterpret_cast<u32x4 *>(sc + lr * R::cld + lc) = cur.g;
-            *reinterpret_cast<u32x4 *>(sc + 16 * R::cld + lr * R::cld + lc) = cur.u;
+            *reinterpret_cast<u32x4 *>(sc + (16 + lr) * R::cld + lc) = cur.u;
+            ss[lane] = cur.s;
+            if (m + kAhead < MI) load(m + kAhead);
             wave_lds_sync();
+            const uint32_t sb = *reinterpret_cast<const uint32_t *>(ss + 4 * i16);
+            const float wt = __shfl(row_w[m / 4], 16 * (m % 4) + i16);
             float dw = 0.0f;
+            f32x4 dg[NB], du[NB], hw[NB];
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
                 const uint32_t gw = *reinterpret_cast<const uint32_t *>(sc + i16 * R::cld + 16 * j + 4 * gq);
                 const uint32_t uw = *reinterpret_cast<const uint32_t *>(sc + (16 + i16) * R::cld + 16 * j + 4 * gq);
-                const f32x4 gv = mx8::values4(gw, mx8::scale_of(cur.gs[j / 2]));
-                const f32x4 uv = mx8::values4(uw, mx8::scale_of(cur.us[j / 2]));
-                float dg[4], du[4], hw[4];
+                const f32x4 gv = mx8::values4(gw, mx8::scale_of((uint8_t)(sb >> (8 * (j / 2)))));
+                const f32x4 uv = mx8::values4(uw, mx8::scale_of((uint8_t)(sb >> (16 + 8 * (j / 2)))));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * gv[i]));
                     const float gsv = gv[i] * s, h = gsv * uv[i], pv = acc[m][j][i];
                     dw = fmaf(pv, h, dw);
-                    const float pw = cur.w * pv;
-                    du[i] = pw * gsv;
+                    const float pw = wt * pv;
+                    du[j][i] = pw * gsv;
                     // s (1 + g (1 - s)) = s + g s (1 - s)
-                    dg[i] = pw * uv[i] * fmaf(gsv, 1.0f - s, s);
-                    hw[i] = cur.w * h;
+                    dg[j][i] = pw * uv[i] * fmaf(gsv, 1.0f - s, s);
+                    hw[j][i] = wt * h;
                 }
-                uint16_t *o = so + i16 * R::old + 16 * j + 4 * gq;
-                *reinterpret_cast<u32x2 *>(o) = u32x2{pack_bf16x2(dg[0], dg[1]), pack_bf16x2(dg[2], dg[3])};
-                *reinterpret_cast<u32x2 *>(o + 16 * R::old) = u32x2{pack_bf16x2(du[0], du[1]), pack_bf16x2(du[2], du[3])};
-                *reinterpret_cast<u32x2 *>(o + 32 * R::old) = u32x2{pack_bf16x2(hw[0], hw[1]), pack_bf16x2(hw[2], hw[3])};
             }
+            wave_lds_sync();
+            store_lines(p.dGU, 2 * p.N, m, dg);
+            store_lines(p.dGU + p.N, 2 * p.N, m, du);
+            store_lines(p.Hw, p.N, m, hw);
             dw += __shfl_xor(dw, 16);
             dw += __shfl_xor(dw, 32);
             if (gq == 0) sdw[wc * BM + wr * (BM / 2) + 16 * m + i16] = c0 < p.N ? dw : 0.0f;
-            // 16-byte pieces of the staged rows: 8 a row, 2 a lane and output
-            wave_lds_sync();
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int piece = lane + 64 * c, r = piece >> 3, col = 8 * (piece & 7);
-                const int row = row0 + wr * (BM / 2) + 16 * m + r;
-                const uint16_t *o = so + r * R::old + col;
-                if (row < row_end && c0 + col < p.N) {
-                    uint16_t *dgu = p.dGU + (long long)row * 2 * p.N + c0 + col;
-                    *reinterpret_cast<u32x4 *>(dgu) = *reinterpret_cast<const u32x4 *>(o);
-                    *reinterpret_cast<u32x4 *>(dgu + p.N) = *reinterpret_cast<const u32x4 *>(o + 16 * R::old);
-                    *reinterpret_cast<u32x4 *>(p.Hw + (long long)row * p.N + c0 + col) =
-                        *reinterpret_cast<const u32x4 *>(o + 32 * R::old);
-                }
-            }
-            wave_lds_sync();
-            cur = nxt;
         }
         if (!p.dw_part) return;
         __syncthreads();

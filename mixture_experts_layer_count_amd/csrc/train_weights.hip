@@ -68,18 +68,6 @@ struct Divisor {
     __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (uint32_t)(((uint64_t)n * mul) >> shift); }
 };
 
-// Two 16-byte pieces of row l16 (lane % 16) in every lane -> of row l16 % 8,
-// then of row 8 + l16 % 8: the first piece in lanes below 8, the second in the
-// others. A row's 8 lanes then store a whole 128-byte line at a time.
-__device__ __forceinline__ void whole_lines(u32x4 &a, u32x4 &b) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t x = a[i];
-        a[i] = __builtin_amdgcn_update_dpp(x, b[i], 0x128, 0xf, 0xc, false);     // row_ror:8
-        b[i] = __builtin_amdgcn_update_dpp(b[i], x, 0x128, 0xf, 0x3, false);
-    }
-}
-
 // which operand's rows are gathered
 enum Gather { GATHER_NONE, GATHER_A, GATHER_B };
 
