@@ -28,6 +28,8 @@
 // and 8 of B through its XCD's L2 (tile rows one by one read 33: 5 % slower),
 // and workgroups differ by at most about one item's work whatever the
 // experts' row counts.
+#include <type_traits>
+
 #include "tiled_gemm_kernel.h"
 
 namespace moe {
@@ -325,76 +327,86 @@ __device__ __forceinline__ void weights_gemm(const WWork &work, const Divisor &g
     };
 
     f32x4 acc[MI][NB];
-#pragma unroll
-    for (int m = 0; m < MI; ++m)
-#pragma unroll
-        for (int j = 0; j < NB; ++j) acc[m][j] = f32x4{};
-    auto mma_rows = [&](const Frag &f, int m) {
+    // FIRST: an item's first step, whose sums begin at zero
+    auto mma_rows = [&](auto first, const Frag &f, int m) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < NB; ++j)
-            acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.b[j], f.a[m], acc[m][j], 0, 0, 0);
+            acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.b[j], f.a[m], decltype(first)::value ? f32x4{} : acc[m][j],
+                                                                0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    // ---- a finished tile, straight from the accumulators (which are cleared):
-    // bf16 as 8 adjacent columns a lane, after one exchange between lanes;
-    // through LDS the epilogue took 2.2 us a tile. Buffer stores: those outside
-    // the matrix get an offset past the buffer's range and are dropped by the
-    // hardware, so every wavefront issues exactly kStores of them whatever the
-    // tile ----
+    // ---- a finished tile, straight from the accumulators: 16-byte pieces of
+    // whole 128-byte lines after two exchanges between lanes (through LDS the
+    // epilogue took as long). VALU-bound, so the addresses are left to the
+    // scalar unit: a lane's offset holds for the whole tile, the rows move the
+    // descriptor. MD and ND are multiples of 32: a block of 16 rows
+    // is inside the matrix or outside (a descriptor of length 0), a lane's
+    // columns likewise (an offset past the range), and the hardware drops
+    // those stores, so every wavefront issues exactly kStores of them ----
     constexpr int kOut = 0x7fffffff;
     auto tile_out = [&](const WItem &it) {
-        constexpr int size = F32 ? 4 : 2;
+        constexpr int size = F32 ? 4 : 2, NP = F32 ? NB / 2 : 1;  // NP: 128-byte pieces of a wavefront's row
         const long long first = (((long long)it.g * p.MD + it.m0 + 128 * wr) * p.ND + it.n0 + 64 * wc) * size;
-        char *C = reinterpret_cast<char *>(it.half ? p.C1 : p.C0) + first;
-        const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(C, 0, kOut, kBufferWord3);
+        const char *held = reinterpret_cast<const char *>(it.half ? p.C1 : p.C0) + first;
+        // uniform, which the compiler does not see (it would loop over the lanes)
+        const uint64_t at = reinterpret_cast<uint64_t>(held);
+        char *C = reinterpret_cast<char *>((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32)) << 32 |
+                                           (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at));
         // re-read here, so that the offsets are not kept through the K loop
-        int nd = p.ND, ln = lane;
-        asm volatile("" : "+v"(nd), "+v"(ln));
+        int ln = lane;
+        asm volatile("" : "+v"(ln));
         const int l16 = ln & 15, lq = ln >> 4;
         const int rows = p.MD - it.m0 - 128 * wr, cols = p.ND - it.n0 - 64 * wc;
+        int off[NP];
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+            const int col = 32 * q + (F32 ? 16 * (l16 >> 3) + 4 * lq : 32 * (l16 >> 3) + pair_column(lq));
+            off[q] = ((l16 & 7) * p.ND + col) * size;
+            asm volatile("" : "+v"(off[q]));  // formed first: the choice is then no branch
+            off[q] = col < cols ? off[q] : kOut;
+        }
 #pragma unroll
         for (int m = 0; m < MI; ++m) {
             __builtin_amdgcn_sched_barrier(0);
+            // rows 16 m .. + 7, and the 8 after them. (Not by the stores' scalar
+            // offset: with one, a store of 16 bytes read a data register that
+            // the next instruction had already overwritten)
+            const int len = 16 * m < rows ? kOut : 0;
+            const __amdgpu_buffer_rsrc_t lines[2] = {
+                __builtin_amdgcn_make_buffer_rsrc(C + 16LL * m * p.ND * size, 0, len, kBufferWord3),
+                __builtin_amdgcn_make_buffer_rsrc(C + (16LL * m + 8) * p.ND * size, 0, len, kBufferWord3)};
+            f32x4 v[NB];
 #pragma unroll
-            for (int j = 0; j < NB; j += F32 ? 2 : 4) {
-                f32x4 v[4];
-#pragma unroll
-                for (int i = 0; i < (F32 ? 2 : 4); ++i) {
-                    v[i] = acc[m][j + i];
-                    acc[m][j + i] = f32x4{};
-                    if (!ACC) continue;
-                    // what C holds, in the accumulators' layout
-                    const int row = 16 * m + l16, c = 16 * (j + i) + 4 * lq;
-                    if (row < rows && c < cols) {
-                        const char *old = C + (row * nd + c) * size;
-                        if constexpr (F32) {
-                            v[i] += *reinterpret_cast<const f32x4 *>(old);
-                        } else {
-                            const u32x2 o = *reinterpret_cast<const u32x2 *>(old);
-                            v[i] += f32x4{bf16_lo(o[0]), bf16_hi(o[0]), bf16_lo(o[1]), bf16_hi(o[1])};
-                        }
+            for (int j = 0; j < NB; ++j) {
+                v[j] = acc[m][j];
+                if (!ACC) continue;
+                // what C holds, in the accumulators' layout
+                const int row = 16 * m + l16, c = 16 * j + 4 * lq;
+                if (row < rows && c < cols) {
+                    const char *old = held + (row * p.ND + c) * size;
+                    if constexpr (F32) {
+                        v[j] += *reinterpret_cast<const f32x4 *>(old);
+                    } else {
+                        const u32x2 o = *reinterpret_cast<const u32x2 *>(old);
+                        v[j] += f32x4{bf16_lo(o[0]), bf16_hi(o[0]), bf16_lo(o[1]), bf16_hi(o[1])};
                     }
                 }
+            }
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
                 u32x4 x0, x1;
                 if constexpr (F32) {
-                    x0 = __builtin_bit_cast(u32x4, v[0]);
-                    x1 = __builtin_bit_cast(u32x4, v[1]);
+                    x0 = __builtin_bit_cast(u32x4, v[2 * q]);
+                    x1 = __builtin_bit_cast(u32x4, v[2 * q + 1]);
                 } else {
                     x0 = pair_columns(v[0], v[1]);
                     x1 = pair_columns(v[2], v[3]);
                 }
                 whole_lines(x0, x1);
-                const int col = 16 * j + (F32 ? 16 * (l16 >> 3) + 4 * lq : 32 * (l16 >> 3) + pair_column(lq));
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int row = 16 * m + 8 * i + (l16 & 7);
-                    int off = (row * nd + col) * size;
-                    asm volatile("" : "+v"(off));  // formed first: the choice is then no branch
-                    off = (row < rows) & (col < cols) ? off : kOut;
-                    __builtin_amdgcn_raw_buffer_store_b128(i ? x1 : x0, rsrc, off, 0, 0);
-                }
+                __builtin_amdgcn_raw_buffer_store_b128(x0, lines[0], off[q], 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b128(x1, lines[1], off[q], 0, 0);
             }
         }
     };
@@ -425,10 +437,10 @@ __device__ __forceinline__ void weights_gemm(const WWork &work, const Divisor &g
     WItem mi = item_at(0), mn = item_at(1);
     int left = mi.steps(), stage = 0;
     int relax = 0;  // steps whose awaited copies are older than a finished tile's stores
-    auto step = [&](Frag &cur, Frag &nxt) {
+    auto step = [&](auto first, Frag &cur, Frag &nxt) {
         const int nstage = stage + 1 == S ? 0 : stage + 1;
-        mma_rows(cur, 0);
-        mma_rows(cur, 1);
+        mma_rows(first, cur, 0);
+        mma_rows(first, cur, 1);
         // the next step's copies have landed when no more than the S - 2 newer
         // steps' (and, for S - 1 steps after a tile, its stores) are outstanding
         if (relax > 0) {
@@ -448,19 +460,21 @@ __device__ __forceinline__ void weights_gemm(const WWork &work, const Divisor &g
 #pragma unroll
             for (int r = c * NR / SLOTS; r < (c + 1) * NR / SLOTS; ++r) read(nxt, r, nstage);
             if (c == SLOTS - 1) advance();
-            mma_rows(cur, c + 2);
+            mma_rows(first, cur, c + 2);
         }
         land(nxt);
         stage = nstage;
     };
     for (;;) {
-        int k = left;
+        step(std::true_type{}, fa, fb);
+        int k = left - 1;
         for (; k > 1; k -= 2) {
-            step(fa, fb);
-            step(fb, fa);
+            step(std::false_type{}, fb, fa);
+            step(std::false_type{}, fa, fb);
         }
         if (k > 0) {
-            step(fa, fb);
+            step(std::false_type{}, fb, fa);
+        } else {
             // once per item: the fragment sets change roles by a copy
 #pragma unroll
             for (int m = 0; m < MI; ++m) fa.a[m] = fb.a[m];
