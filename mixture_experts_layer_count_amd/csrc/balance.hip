@@ -19,6 +19,10 @@
 // smallest power of two that covers E, so a layer of 8 experts puts 32 tokens
 // on a wavefront and 256 experts one.
 //
+// Measured (sums, second kernel, gradient): 64 tokens of 8 experts 3, 4 and
+// 3.7 us; 8192 of 128 5.9, 6 and 8.2; 65536 of 256 18.5 (67 MB and the picks at
+// 3.7 TB/s), 5.3 and 31 (136 MB at 4.4 TB/s).
+//
 // The sums over tokens are formed in a fixed order, so results are identical
 // run to run: a block sums the tokens of one chunk, sequence by sequence, and
 // writes one partial row per (chunk x, sequence b) it holds, at slot x + b

@@ -5,7 +5,8 @@
 // owns 16 consecutive values: two (fp32: four) 16-byte loads, one 16-byte
 // code store; the two threads of a group exchange their maxima with one
 // shuffle, and one of them stores the group's scale byte (32 contiguous bytes
-// a wavefront).
+// a wavefront). 32768 x 4096 bf16: packed in 69 us (5.9 TB/s), read back in 64
+// (6.4 TB/s; the 256 MB cache holds part of it).
 #include "mx8.h"
 
 namespace moe {

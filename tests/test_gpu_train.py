@@ -64,6 +64,23 @@ def test_checkpoint_bit_exact(R, C, ld, dt):
         np.testing.assert_array_equal(f64(moe.checkpoint_unpack(Q, S, out)), train.checkpoint_values(q, s))
 
 
+def test_checkpoint_strided_and_empty():
+    say("[train] checkpoint of a view with gaps between rows, of one row, of none")
+    x = torch.randn(9, 3 * 160, generator=torch.Generator().manual_seed(8)).bfloat16().cuda()
+    view = x.view(9, 3, 160)[:, 1, :96]
+    Q, S = moe.checkpoint_pack(view)
+    q, s = moe.checkpoint_pack(view.contiguous())
+    assert torch.equal(Q, q) and torch.equal(S, s)
+    Q, S = moe.checkpoint_pack(view[4:5])
+    assert torch.equal(Q, q[4:5]) and torch.equal(S, s[4:5])
+    Q, S = moe.checkpoint_pack(x[:0])
+    assert Q.shape == (0, 480) and S.shape == (0, 15) and moe.checkpoint_unpack(Q, S).shape == (0, 480)
+    with pytest.raises(moe.MoEError):
+        moe.checkpoint_pack(x[:1].expand(9, 480))       # rows on top of each other
+    with pytest.raises(moe.MoEError):
+        moe.checkpoint_pack(x.view(-1)[4:4 + 480].view(5, 96))  # off the 16-byte boundary
+
+
 def test_checkpoint_every_code():
     Q = torch.arange(256, dtype=torch.uint8).reshape(8, 32).cuda()
     S = torch.tensor([[120], [127], [1], [10], [200], [240], [127], [64]], dtype=torch.uint8).cuda()
@@ -317,6 +334,8 @@ FFN_CASES = [
     (8200, 128, 2080, 2, 1, True, 0.3), (8200, 2080, 128, 2, 1, True, 0.3), (8200, 2048, 160, 2, 1, False, 0),
     # sums long enough for a split tail: gate/up and dH over H (2 and 4 parts), down and dX over F
     (200, 4128, 64, 2, 1, True, 0), (70, 8256, 96, 2, 2, True, 0), (150, 64, 4160, 2, 2, True, 0.5),
+    # the most experts, the most picks
+    (60, 64, 96, 1024, 4, True, 0), (9, 32, 64, 70, 64, True, 0),
     # several weight-gradient tiles for each workgroup, experts of 0 to 4 steps
     (190, 1056, 1120, 12, 2, True, 0.4),
 ]
