@@ -5,6 +5,7 @@
 
 #include "abi_util.h"
 #include "common.h"
+#include "train.h"
 
 using namespace moe;
 

@@ -34,7 +34,7 @@
 
 #include <type_traits>
 
-#include "common.h"
+#include "train.h"
 
 namespace moe {
 namespace {

@@ -12,7 +12,7 @@
 // checkpoints on the bf16 matrix cores with no second rounding.
 #pragma once
 
-#include "common.h"
+#include "train.h"
 
 namespace moe {
 namespace mx8 {

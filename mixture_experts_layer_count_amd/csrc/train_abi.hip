@@ -3,6 +3,7 @@
 // forward and backward. Argument validation, workspace layout and launch
 // order; nothing here synchronises with the device or allocates.
 #include "abi_util.h"
+#include "train.h"
 
 using namespace moe;
 

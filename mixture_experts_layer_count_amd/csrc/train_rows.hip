@@ -51,7 +51,7 @@
 // 293 us, as 54 parts 310). A part leaves its fp32 sums and the last one to
 // finish adds them in part order, so results do not depend on which that is.
 #include "mx8.h"
-#include "tiled_gemm_kernel.h"
+#include "train_kernel.h"
 
 namespace moe {
 

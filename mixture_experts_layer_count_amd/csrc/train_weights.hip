@@ -37,7 +37,7 @@
 // experts' row counts.
 #include <type_traits>
 
-#include "tiled_gemm_kernel.h"
+#include "train_kernel.h"
 
 namespace moe {
 

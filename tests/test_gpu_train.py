@@ -431,6 +431,20 @@ def test_ffn_train_rows_behind_the_last_group():
     assert not got[1].reshape(-1)[torch.as_tensor(dropped, device="cuda").long()].any()
 
 
+def test_ffn_train_every_pick_left_out():
+    say("[train] ffn whose permutation left every pick out")
+    c = _ffn_case(40, 64, 96, 3, 2)
+    d = _dev(c)
+    _, ck = _forward(d)
+    d["offsets"] = torch.zeros(4, dtype=torch.int32, device="cuda")
+    Yp, _ = _forward(d)
+    assert Yp.shape == (80, 64)
+    dX, dw, dW1, dW3, dW2 = _backward(d, ck)
+    assert not any(t.any() for t in (dX, dw, dW1, dW3, dW2))
+    add = torch.randn(40, 64).bfloat16().cuda()
+    assert torch.equal(_backward(d, ck, need=("dX",), dX_add=add)[0], add)
+
+
 def test_ffn_train_nan_stays_in_its_expert():
     say("[train] a NaN row reaches its token and its expert only")
     c = _ffn_case(300, 64, 96, 6, 1)
