@@ -445,6 +445,55 @@ def test_ffn_train_every_pick_left_out():
     assert torch.equal(_backward(d, ck, need=("dX",), dX_add=add)[0], add)
 
 
+def _sub(c, ck, e, rows, tokens, cols=slice(None)):
+    """Rows of expert e (and columns of F) as a problem of their own, k = 1 and
+    in row order: its case and its checkpoint."""
+    n = len(rows)
+    groups = slice(None) if cols == slice(None) else slice(cols.start // 32, cols.stop // 32)
+    sub = {"X": c["X"][tokens].cpu(), "dY": c["dY"][tokens].cpu(), "W1": c["W1"][e:e + 1, :, cols].cpu(),
+           "W3": c["W3"][e:e + 1, :, cols].cpu(), "W2": c["W2"][e:e + 1, cols].cpu(), "k": 1,
+           "w": c["w"].reshape(-1)[c["row_src"].long()[rows]].reshape(n, 1).cpu(), "offsets": np.array([0, n]),
+           "row_src": None, "assign_row": None}
+    part = moe.FFNCheckpoint(*(t[tokens] for t in ck[:2]), ck.gq[rows][:, cols], ck.gs[rows][:, groups],
+                             ck.uq[rows][:, cols], ck.us[rows][:, groups])
+    return sub, part
+
+
+@pytest.mark.parametrize("T,H,F,E,k", [(70000, 64, 4096, 8, 8),     # 2.3e9 values of g
+                                       (300, 8192, 4128, 64, 1)])   # 2.2e9 of a weight matrix
+def test_ffn_train_past_32_bits(T, H, F, E, k):
+    say(f"[train] ffn with offsets past 32 bits: T={T} H={H} F={F} E={E} k={k}")
+    g = torch.Generator(device="cuda").manual_seed(T)
+    bf = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    c = {"X": bf(T, H), "dY": bf(T, H), "W1": bf(E, H, F).mul_(0.05), "W3": bf(E, H, F).mul_(0.05),
+         "W2": bf(E, F, H).mul_(0.05), "k": k}
+    z, idx = torch.topk(torch.randn(T, E, generator=g, device="cuda"), k, dim=1)
+    c["w"] = torch.softmax(z, 1)
+    _, c["offsets"], c["row_src"], c["assign_row"], _ = moe.permute(idx.int(), E)
+    off = c["offsets"].tolist()
+    Yp, ck = _forward(c)
+    got = _backward(c, ck)
+    # the last expert's last rows: forward
+    e = max(i for i in range(E) if off[i + 1] > off[i])
+    rows = torch.arange(max(off[e], off[e + 1] - 40), off[e + 1], device="cuda")
+    token = lambda r: c["row_src"].long()[r] // k  # noqa: E731
+    sub, part = _sub(c, ck, e, rows, token(rows))
+    _check_forward(sub, Yp[rows], part)
+    # the last tokens' gradients, over all their experts
+    t = torch.arange(T - 12, T, device="cuda")
+    r = torch.sort(c["assign_row"].long().reshape(T, k)[t].reshape(-1))[0]
+    many = {n: c[n][t].cpu() for n in ("X", "dY", "w")} | {n: c[n].cpu() for n in ("W1", "W3", "W2")} | {
+        "k": k, "row_src": (c["row_src"].long()[r] - (T - 12) * k).cpu().numpy(), "assign_row": None,
+        "offsets": np.searchsorted(r.cpu().numpy(), np.array(off))} if k > 1 else None
+    if many:
+        _check_backward(many, moe.FFNCheckpoint(*(x[t] for x in ck[:2]), *(x[r] for x in ck[2:])),
+                        (got[0][t], got[1][t], None, None, None))
+    # the last expert's weight gradients, its last 32 columns of F
+    rows = torch.arange(off[e], off[e + 1], device="cuda")
+    sub, part = _sub(c, ck, e, rows, token(rows), slice(F - 32, F))
+    _check_backward(sub, part, (None, None, got[2][e:e + 1, :, F - 32:], got[3][e:e + 1, :, F - 32:], got[4][e:e + 1, F - 32:]))
+
+
 def test_ffn_train_nan_stays_in_its_expert():
     say("[train] a NaN row reaches its token and its expert only")
     c = _ffn_case(300, 64, 96, 6, 1)
