@@ -6,7 +6,7 @@
 // the device too: no device-to-host copy, and the whole layer stays capturable
 // in a HIP graph. The GEMM grids are sized for the worst case
 // (ceil(M / bm) + G tiles) and surplus workgroups exit at once.
-#include "common.h"
+#include "schedule.h"
 
 namespace moe {
 namespace {
@@ -16,35 +16,7 @@ __global__ __launch_bounds__(1024) void build_tiles_kernel(const int32_t *offset
                                                            int32_t *group_tile_start, int32_t *zero,
                                                            int n_zero) {
     __shared__ int scan_lds[16];
-    for (int i = threadIdx.x; i < n_zero; i += 1024) zero[i] = 0;
-    const int NG = G + (extra_rows > 0 ? 1 : 0);
-    int carry = 0;
-    // groups in rounds of 1024; each thread emits its group's tiles
-    for (int g0 = 0; g0 < NG; g0 += 1024) {
-        const int g = g0 + threadIdx.x;
-        int lo = 0, hi = 0, n = 0;
-        if (g < NG) {
-            lo = offsets[g];
-            hi = g < G ? offsets[g + 1] : lo + extra_rows;
-            n = (hi - lo + bm - 1) / bm;
-            if (n < 0) n = 0;
-        }
-        int total = 0;
-        const int first = block_exclusive_scan(n, scan_lds, &total) + carry;
-        if (g < NG && group_tile_start) group_tile_start[g] = first;
-        for (int i = 0; i < n; ++i) {
-            int *t = tiles + 4 * (first + i);
-            t[0] = g;
-            t[1] = lo + i * bm;
-            t[2] = min(lo + (i + 1) * bm, hi);
-            t[3] = 0;
-        }
-        carry += total;
-    }
-    if (threadIdx.x == 0) {
-        *n_tiles = carry;
-        if (group_tile_start) group_tile_start[NG] = carry;
-    }
+    build_tiles(offsets, G, extra_rows, bm, tiles, n_tiles, group_tile_start, zero, n_zero, scan_lds);
 }
 
 }  // namespace

@@ -21,6 +21,16 @@ __device__ __forceinline__ void wave_lds_sync() {
 // codes Q [R][C] and scale bytes S [R][C/32]
 hipError_t launch_mx8_pack(const void *X, moe_dtype x_dt, long long ldx, long long R, int C, uint8_t *Q, uint8_t *S,
                            hipStream_t s);
+// dense bf16 rows packed, and in the same launch a tile list as
+// launch_build_tiles forms it
+struct TilesJob {
+    const int32_t *offsets;
+    int G, bm;
+    int32_t *tiles, *n_tiles, *start, *zero;
+    int n_zero;
+};
+hipError_t launch_mx8_pack_tiles(const void *X, long long R, int C, uint8_t *Q, uint8_t *S, const TilesJob &tiles,
+                                 hipStream_t s);
 hipError_t launch_mx8_unpack(const uint8_t *Q, const uint8_t *S, long long R, int C, moe_dtype y_dt, void *Y,
                              hipStream_t s);
 

@@ -40,8 +40,8 @@ struct Tiles {
         n_tiles = static_cast<int32_t *>(c.take(sizeof(int32_t)));
         start = static_cast<int32_t *>(c.take(sizeof(int32_t) * (G + 1)));
     }
-    hipError_t build(const int32_t *offsets, int G, hipStream_t s, int32_t *zero = nullptr, int n_zero = 0) const {
-        return launch_build_tiles(offsets, G, 0, bm, tiles, n_tiles, start, s, zero, n_zero);
+    TilesJob job(const int32_t *offsets, int G, int32_t *zero, int n_zero) const {
+        return {offsets, G, bm, tiles, n_tiles, start, zero, n_zero};
     }
 };
 
@@ -220,8 +220,8 @@ moe_status moe_ffn_train_forward(const void *X, const int32_t *row_src, int k, i
     ForwardWs w;
     if (bad16(ws) || ws_bytes < w.carve(ws, M, G, H, F)) return MOE_ERR_WORKSPACE_TOO_SMALL;
 
-    MOE_TRY(launch_mx8_pack(X, MOE_BF16, H, T, H, ckpt->xq, ckpt->xs, stream));
-    MOE_TRY(w.t.build(offsets, G, stream, w.parts.count, 2 * rows_gemm_counters));
+    MOE_TRY(launch_mx8_pack_tiles(X, T, H, ckpt->xq, ckpt->xs,
+                                  w.t.job(offsets, G, w.parts.count, 2 * rows_gemm_counters), stream));
     RowsProblem up = rows_problem(w.t, w.parts, 0, G, M, k);
     up.A = static_cast<const uint16_t *>(X);
     up.row_src = row_src;
@@ -280,7 +280,8 @@ moe_status moe_ffn_train_backward(const void *dY, const float *topk_w, const int
     if (bad16(ws) || ws_bytes < w.carve(ws, T, M, G, H, F)) return MOE_ERR_WORKSPACE_TOO_SMALL;
 
     if (T > 0) {
-        MOE_TRY(w.t.build(offsets, G, stream, w.parts.count, 2 * rows_gemm_counters));
+        MOE_TRY(launch_build_tiles(offsets, G, 0, w.t.bm, w.t.tiles, w.t.n_tiles, w.t.start, stream, w.parts.count,
+                                   2 * rows_gemm_counters));
         // p = dY W2^T, then dg, du, w h and the routing weights' partial sums
         RowsProblem b = rows_problem(w.t, w.parts, 0, G, M, k);
         b.A = static_cast<const uint16_t *>(dY);
