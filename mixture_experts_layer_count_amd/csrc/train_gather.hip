@@ -8,6 +8,9 @@
 // 5.0 TB/s). One block per token and 2048 columns, 8 columns (two 16-byte loads
 // a row) a thread. As three launches: 12 us, so 5.4 (T 1536, k 2, H 640). Rows
 // outside [0, *n_rows) (picks that the permutation left out) contribute nothing.
+// A grid's dimension holds fewer than 2^32 threads (beyond, a launch takes their
+// number mod 2^32 and reports nothing), and T may pass 2^24: the tokens go to
+// the grid's z in runs of kRun.
 #include "mx8.h"
 
 namespace moe {
@@ -16,8 +19,11 @@ MOE_BOUNDS_FILE(train_gather)
 
 namespace {
 
+constexpr int kRun = 1 << 16;  // tokens along x
+
 __global__ __launch_bounds__(256) void gather_grads_kernel(GatherProblem p) {
-    const int t = blockIdx.x, c = (blockIdx.y * 256 + threadIdx.x) * 8;
+    const int t = blockIdx.z * kRun + blockIdx.x, c = (blockIdx.y * 256 + threadIdx.x) * 8;
+    if (t >= p.T) return;
     const int M = min(p.M, *p.n_rows);
     const long long o = (long long)t * p.H + c;
     u32x2 code;
@@ -75,7 +81,9 @@ hipError_t launch_gather_grads(const GatherProblem &p, hipStream_t s) {
         return hipErrorInvalidValue;
     if (!p.dX && !p.dw && !p.x) return hipSuccess;
     const unsigned columns = p.dX || p.x ? (unsigned)((p.H + 2047) / 2048) : 1;
-    hipLaunchKernelGGL(gather_grads_kernel, dim3((unsigned)p.T, columns), dim3(256), 0, s, p);
+    const unsigned runs = (unsigned)((p.T + (long long)kRun - 1) / kRun);
+    hipLaunchKernelGGL(gather_grads_kernel, dim3((unsigned)(p.T < kRun ? p.T : kRun), columns, runs), dim3(256), 0, s,
+                       p);
     return hipGetLastError();
 }
 
