@@ -64,6 +64,10 @@ constexpr int kRowsBN = rows_gemm_bn;
 constexpr int kRowsBK = 64;
 constexpr int kRowsParts = 4;        // parts of a split item at most
 constexpr int kRowsPartSteps = 32;   // and steps a part has at least (a part's sums cost about 10 steps)
+// Workgroups along x, the others along y: one dimension of a grid holds fewer
+// than 2^32 threads (beyond, a launch takes their number mod 2^32 and reports
+// nothing). A multiple of the XCDs, so that the order over them goes on
+constexpr uint32_t kRowsRun = 4096;
 
 template <int BM>
 struct RowsRing {
@@ -99,7 +103,8 @@ __device__ __forceinline__ bool pick_rows(const RowsProblem &p, int nN, int nk, 
     order.group_tile_start = p.group_tile_start;
     const int n_tiles = *p.n_tiles, n_work = n_tiles * nN;
     const int per = (n_work + kXcds - 1) / kXcds;
-    const int xcd = blockIdx.x % kXcds, slot = blockIdx.x / kXcds;
+    const uint32_t block = blockIdx.y * kRowsRun + blockIdx.x;
+    const int xcd = block % kXcds, slot = block / kXcds;
     const int first = xcd * per, n = min(per, n_work - first);
     if (n <= 0) return false;
     const int tail = n % kBlocksPerXcd, full = n - tail;
@@ -552,11 +557,12 @@ hipError_t launch_rows(const RowsProblem &p, RowsUse use, hipStream_t s) {
     const int nN = rows_gemm_columns(p.N, use);
     // items per XCD, and the parts that the last of them may be split into
     const long long per = ((long long)p.max_tiles * nN + kXcds - 1) / kXcds + (p.part ? kBlocksPerXcd : 0);
-    const long long blocks = per * kXcds;
+    const long long blocks = per * kXcds, runs = (blocks + kRowsRun - 1) / kRowsRun;
     if (blocks <= 0) return hipSuccess;
-    if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+    if (runs > 0xffff) return hipErrorInvalidValue;
     auto launch = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(512), 0, s, p, nN);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(runs > 1 ? kRowsRun : blocks), (unsigned)runs), dim3(512), 0, s, p,
+                           nN);
     };
     switch (use) {
     case ROWS_GATE_UP: launch(rows_gemm_kernel<BM, ROWS_GATE_UP>); break;

@@ -49,3 +49,26 @@ def test_ffn_train_tokens_times_a_block_past_32_bits():
     _check_forward(sub, Yp[last], part)
     _check_backward(sub, part, (got[0][last], got[1][last], *got[2:]))
     assert not got[0][:T - n].any() and not got[1][:T - n].any()
+
+
+def test_ffn_train_column_tiles_of_many_experts():
+    """1024 experts of 2^20 columns, the last four with a row each: the row and
+    column tiles that the gate and up product could have, times their threads,
+    do not fit 32 bits. (The three weight matrices share one buffer: only the
+    last experts' are read.)"""
+    T, H, F, E = 4, 32, 1 << 20, 1024
+    say(f"[limits] ffn T={T} H={H} F={F} E={E}")
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GiB of free memory")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    W = torch.empty(E * H * F, dtype=torch.bfloat16, device="cuda")
+    last = 0.05 * torch.randn(T * H * F, generator=g, device="cuda", dtype=torch.bfloat16)
+    W[-T * H * F:] = last
+    X = torch.randn(T, H, generator=g, device="cuda", dtype=torch.bfloat16)
+    offsets = torch.clamp(torch.arange(E + 1, dtype=torch.int32, device="cuda") - (E - T), min=0)
+    Yp, ck = moe.ffn_train_forward(X, offsets, W.view(E, H, F), W.view(E, H, F), W.view(E, F, H))
+    torch.cuda.synchronize()
+    last = last.cpu()
+    sub = {"X": X.cpu(), "W1": last.view(T, H, F), "W3": last.view(T, H, F), "W2": last.view(T, F, H), "k": 1,
+           "row_src": None, "offsets": np.arange(T + 1)}
+    _check_forward(sub, Yp, ck)
