@@ -16,6 +16,7 @@ namespace {
 using namespace mx8;
 
 constexpr int kPer = 16;  // values per thread
+constexpr long long kMaxThreads = 0xffffffffLL;  // of a launch (beyond, it takes their number mod 2^32)
 
 // 16 values of X at element offset o
 template <bool F32>
@@ -112,7 +113,7 @@ hipError_t launch_mx8_pack(const void *X, moe_dtype x_dt, long long ldx, long lo
         return hipErrorInvalidValue;
     if (R == 0) return hipSuccess;
     const long long n = R * C, blocks = (n / kPer + 255) / 256;
-    if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+    if (blocks > kMaxThreads / 256) return hipErrorInvalidValue;
     if (x_dt == MOE_F32)
         hipLaunchKernelGGL(mx8_pack_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, s, X, ldx, n, C, Q, S);
     else
@@ -126,7 +127,7 @@ hipError_t launch_mx8_pack_tiles(const void *X, long long R, int C, uint8_t *Q, 
         (tiles.n_zero > 0 && !tiles.zero))
         return hipErrorInvalidValue;
     const long long n = R * C, blocks = (n / kPer + 1023) / 1024 + 1;
-    if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+    if (blocks > kMaxThreads / 1024) return hipErrorInvalidValue;
     hipLaunchKernelGGL(mx8_pack_tiles_kernel, dim3((unsigned)blocks), dim3(1024), 0, s, X, n, C, Q, S, tiles);
     return hipGetLastError();
 }
@@ -137,7 +138,7 @@ hipError_t launch_mx8_unpack(const uint8_t *Q, const uint8_t *S, long long R, in
         return hipErrorInvalidValue;
     if (R == 0) return hipSuccess;
     const long long n = R * C, blocks = (n / kPer + 255) / 256;
-    if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+    if (blocks > kMaxThreads / 256) return hipErrorInvalidValue;
     if (y_dt == MOE_F32)
         hipLaunchKernelGGL(mx8_unpack_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, s, Q, S, n, Y);
     else

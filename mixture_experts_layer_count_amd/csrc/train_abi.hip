@@ -11,6 +11,10 @@ namespace {
 
 constexpr int kMaxSeqs = 65535;
 
+// Values of a checkpoint: one launch of 256 threads per 4096 values, and a
+// grid's dimension holds fewer than 2^32 threads
+constexpr long long kMaxCheckpoint = (1LL << 36) - 4096;
+
 // null, or not on the 16-byte boundary that the kernels' wide accesses need
 bool bad16(const void *p) { return !p || (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
 bool off16(const void *p) { return p && bad16(p); }
@@ -182,8 +186,8 @@ moe_status moe_route_backward(const float *logits, const int32_t *topk_idx, cons
 moe_status moe_checkpoint_pack(const void *X, moe_dtype x_dt, long long ldx, long long R, int C, uint8_t *Q, uint8_t *S,
                                hipStream_t stream) {
     if (R < 0 || C < 1 || ldx < C) return MOE_ERR_INVALID_ARG;
-    if ((x_dt != MOE_F32 && x_dt != MOE_BF16) || C % 32 || C > kMaxDim || R > 0x7fffffffLL ||
-        ldx % (x_dt == MOE_F32 ? 4 : 8) || R * (C / 16) > 0x7fffffffLL * 256)
+    if ((x_dt != MOE_F32 && x_dt != MOE_BF16) || C % 32 || C > kMaxDim || R > kMaxCheckpoint / C ||
+        ldx % (x_dt == MOE_F32 ? 4 : 8))
         return MOE_ERR_UNSUPPORTED;
     if (R == 0) return MOE_OK;
     if (bad16(X) || bad16(Q) || !S) return MOE_ERR_INVALID_ARG;
@@ -193,8 +197,7 @@ moe_status moe_checkpoint_pack(const void *X, moe_dtype x_dt, long long ldx, lon
 moe_status moe_checkpoint_unpack(const uint8_t *Q, const uint8_t *S, long long R, int C, moe_dtype y_dt, void *Y,
                                  hipStream_t stream) {
     if (R < 0 || C < 1) return MOE_ERR_INVALID_ARG;
-    if ((y_dt != MOE_F32 && y_dt != MOE_BF16) || C % 32 || C > kMaxDim || R > 0x7fffffffLL ||
-        R * (C / 16) > 0x7fffffffLL * 256)
+    if ((y_dt != MOE_F32 && y_dt != MOE_BF16) || C % 32 || C > kMaxDim || R > kMaxCheckpoint / C)
         return MOE_ERR_UNSUPPORTED;
     if (R == 0) return MOE_OK;
     if (bad16(Q) || !S || bad16(Y)) return MOE_ERR_INVALID_ARG;

@@ -1,0 +1,19 @@
+"""The training entry points on the host: sizes whose launches would pass 2^32
+threads along a grid's dimension are refused before anything is launched. No
+GPU is needed."""
+import ctypes
+
+import mixture_experts_layer_count_amd as moe
+
+UNSUPPORTED = 2
+F32, BF16 = 0, 1
+FAKE = ctypes.c_void_p(0x1000)  # never dereferenced: validation fails first
+
+
+def test_checkpoint_values_past_a_launch():
+    """A launch packs 4096 values with 256 threads: 2^36 values need 2^32."""
+    pack, unpack = moe.lib().moe_checkpoint_pack, moe.lib().moe_checkpoint_unpack
+    for R, C in ((1 << 16, 1 << 20), ((1 << 31) - 1, 64), (1 << 31, 32), (1 << 62, 32), ((1 << 36) // 96, 96)):
+        for dt in (F32, BF16):
+            assert pack(FAKE, dt, C, R, C, FAKE, FAKE, None) == UNSUPPORTED, (R, C)
+            assert unpack(FAKE, FAKE, R, C, dt, FAKE, None) == UNSUPPORTED, (R, C)
