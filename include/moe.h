@@ -356,8 +356,8 @@ moe_status moe_ep_local_experts(const moe_ep_record *recv_meta, int n, int E, in
  * be -inf (an expert masked out: p = 0); a row of only -inf has p = 0 and
  * lse = 0. A NaN or +inf logit makes the losses NaN. T == 0 writes zeros.
  * fp32; sums in a fixed order, identical run to run.
- * E <= 1024, k <= 64, B <= 65535. Workspace: moe_balance_loss_workspace_bytes
- * bytes (device, any contents). */
+ * E <= 1024, k <= min(E, 64), B <= 65535, T <= 2^30 - 64, T*E < 2^31.
+ * Workspace: moe_balance_loss_workspace_bytes bytes (device, any contents). */
 size_t moe_balance_loss_workspace_bytes(int T, int E, int B);
 moe_status moe_balance_loss(const float *logits, const int32_t *topk_idx, int T, int E, int k,
                             const int32_t *seq_offsets, int B, float alpha, float beta, float *loss, int32_t *counts,

@@ -489,7 +489,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(BalanceArgs a,
 // tokens per block: enough blocks for every CU, at least 16 tokens each, and
 // at most 64 (the partial rows stay below a sixteenth of the logits)
 int chunk_tokens(int T) {
-    int c = (T + 1023) / 1024;
+    int c = (int)((T + 1023LL) / 1024);
     c = (c + 15) / 16 * 16;
     return c < 16 ? 16 : c > 64 ? 64 : c;
 }

@@ -10,6 +10,9 @@ using namespace moe;
 namespace {
 
 constexpr int kMaxSeqs = 65535;
+// Tokens of the router's calls: up to 64 of them for each 256-thread workgroup,
+// fewer than 2^32 threads
+constexpr int kMaxRouterTokens = (1 << 30) - 64;
 
 // Values of a checkpoint: one launch of 256 threads per 4096 values, and a
 // grid's dimension holds fewer than 2^32 threads
@@ -21,7 +24,7 @@ bool off16(const void *p) { return p && bad16(p); }
 
 moe_status check_router(int T, int E, int k, int B, const int32_t *seq_offsets) {
     if (T < 0 || E < 1 || k < 1 || k > E || B < 1 || (!seq_offsets && B != 1)) return MOE_ERR_INVALID_ARG;
-    if (E > 1024 || k > 64 || B > kMaxSeqs) return MOE_ERR_UNSUPPORTED;
+    if (E > 1024 || k > 64 || B > kMaxSeqs || T > kMaxRouterTokens) return MOE_ERR_UNSUPPORTED;
     if ((long long)T * E > 0x7fffffffLL || (long long)T * k > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }

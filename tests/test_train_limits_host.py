@@ -17,3 +17,15 @@ def test_checkpoint_values_past_a_launch():
         for dt in (F32, BF16):
             assert pack(FAKE, dt, C, R, C, FAKE, FAKE, None) == UNSUPPORTED, (R, C)
             assert unpack(FAKE, FAKE, R, C, dt, FAKE, None) == UNSUPPORTED, (R, C)
+
+
+def test_router_tokens_past_a_launch():
+    """64 tokens take 256 threads at most: 2^30 tokens need 2^32."""
+    loss, back = moe.lib().moe_balance_loss, moe.lib().moe_route_backward
+    for T, E in (((1 << 30) - 63, 1), (1 << 30, 1), ((1 << 31) - 1, 1), ((1 << 30) - 1, 2)):
+        assert loss(FAKE, FAKE, T, E, 1, None, 1, 0.1, 0.1, FAKE, FAKE, FAKE, FAKE, 1 << 50, None) == UNSUPPORTED, T
+        assert back(FAKE, FAKE, FAKE, FAKE, T, E, 1, None, 1, FAKE, 0.1, 0.1, None, FAKE, None) == UNSUPPORTED, T
+    # the workspace of sizes near the limit, formed in 64 bits
+    ws = moe.lib().moe_balance_loss_workspace_bytes
+    assert 0 < ws((1 << 30) - 1024, 1, 1) <= ws((1 << 30) - 64, 1, 1)
+    assert ws((1 << 31) - 1, 1, 1) < 1 << 30  # partial rows of 64 tokens
