@@ -7,7 +7,6 @@ namespace moe {
 
 unsigned bounds_take_train_rows();
 unsigned bounds_take_train_weights();
-unsigned bounds_take_train_gather();
 
 // Between LDS writes and reads by other lanes of the same wavefront, whose LDS
 // operations complete in order: no instruction, but without it the compiler

@@ -15,8 +15,6 @@
 
 namespace moe {
 
-MOE_BOUNDS_FILE(train_gather)
-
 namespace {
 
 constexpr int kRun = 1 << 16;  // tokens along x

@@ -158,8 +158,11 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
         const int tr = 8 * (w * R::nA + q) + (lane >> 3);
         int r = row0 + tr;
         if (r >= row_end) r = row0;  // rows past the tile's end copy a valid row (never stored)
-        int src = p.row_src ? p.row_src[r] / p.gk : r - row0;
-        if (p.row_src && MOE_BOUNDS_FAIL(src >= 0 && src < p.a_rows, BOUNDS_A_ROW)) src = 0;
+        int src = p.row_src ? p.row_src[r] : r - row0;
+        if (p.row_src) {
+            if (MOE_BOUNDS_FAIL(src >= 0 && src < p.a_rows * p.gk, BOUNDS_A_ROW)) src = 0;
+            src /= p.gk;
+        }
         a_off[q] = 2u * ((uint32_t)src * p.lda + 8 * ((lane & 7) ^ ((tr >> 1) & 7)));
     }
     const char *a0 = reinterpret_cast<const char *>(p.A + (p.row_src ? 0LL : (long long)row0 * p.lda));
@@ -496,7 +499,10 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
         for (int i = 0; i < (MI + 3) / 4; ++i) {
             const int r = base + 64 * i + lane;
             row_w[i] = 0.0f;
-            if (r < row_end && 64 * i + lane < BM / 2) row_w[i] = p.topk_w ? p.topk_w[p.w_src ? p.w_src[r] : r] : 1.0f;
+            if (r >= row_end || 64 * i + lane >= BM / 2) continue;
+            int a = p.w_src ? p.w_src[r] : r;
+            if (MOE_BOUNDS_FAIL(a >= 0 && a < p.M, BOUNDS_A_ROW)) a = 0;
+            row_w[i] = p.topk_w ? p.topk_w[a] : 1.0f;
         }
 #pragma unroll
         for (int m = 0; m < kAhead; ++m) load(m);

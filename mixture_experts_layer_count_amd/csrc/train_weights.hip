@@ -239,10 +239,10 @@ __device__ __forceinline__ void weights_gemm(const WWork &work, const Divisor &g
     uint32_t l_row = kNoRow;
     auto take_rows = [&]() {
         if (GATHER == GATHER_NONE) return;
-        uint32_t got = gk(*(reinterpret_cast<const uint32_t *>(my_rows + buf * R::rows_bytes) + lane));
+        uint32_t got = *(reinterpret_cast<const uint32_t *>(my_rows + buf * R::rows_bytes) + lane);
         const int r = ci.lo + 32 * ((ck & -R::window) + (lane >> 2)) + 4 * w + (lane & 3);
-        if (r < ci.hi && MOE_BOUNDS_FAIL(got < (uint32_t)p.src_rows, BOUNDS_A_ROW)) got = 0;
-        l_row = r < ci.hi ? got * (GATHER == GATHER_A ? lda2 : ldb2) : kNoRow;
+        if (r < ci.hi && MOE_BOUNDS_FAIL(got < (uint32_t)p.src_rows * p.gk, BOUNDS_A_ROW)) got = 0;
+        l_row = r < ci.hi ? gk(got) * (GATHER == GATHER_A ? lda2 : ldb2) : kNoRow;
     };
     uint32_t row_off[2] = {0, 0};  // of the gathered operand's two copies of the step
     auto step_rows = [&]() {
