@@ -418,6 +418,13 @@ moe_status moe_ffn_train_forward(const void *X, const int32_t *row_src, int k, i
                                  int H, int F, const void *W1, const void *W3, const void *W2, moe_dtype dt, void *Yp,
                                  const moe_ffn_checkpoint *ckpt, void *ws, size_t ws_bytes, hipStream_t stream);
 
+/* The kernels that the FFN's calls of these sizes take (a host call, for tests
+ * and profiles): rows per tile of the forward's and of the backward's row
+ * products, and whether the forward's down projection is the inference path's
+ * persistent kernel (1) or a row product (0). */
+moe_status moe_ffn_train_plan(int T, int k, int G, int H, int F, int *forward_rows, int *backward_rows,
+                              int *persistent_down);
+
 /* Backward pass of moe_ffn_train_forward followed by moe_combine. For row r
  * holding assignment a = t*k + j (a = row_src[r]), w = topk_w[a] and the
  * checkpoint's values x, g, u (s = 1/(1 + exp(-g)), h = g s u):

@@ -55,6 +55,7 @@ SIGNATURES = {
     "moe_checkpoint_unpack": (_I, [_P, _P, ctypes.c_longlong, _I, _I, _P, _P]),
     "moe_ffn_train_forward_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
     "moe_ffn_train_forward": (_I, [_P, _P, _I, _I, _P, _I, _I, _I, _P, _P, _P, _I, _P, _P, _P, _SZ, _P]),
+    "moe_ffn_train_plan": (_I, [_I, _I, _I, _I, _I, _P, _P, _P]),
     "moe_ffn_train_backward_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
     "moe_ffn_train_backward": (_I, [_P, _P, _P, _P, _I, _I, _P, _I, _I, _I, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P,
                                     _P, _I, _I, _P, _SZ, _P]),

@@ -261,6 +261,23 @@ moe_status moe_ffn_train_forward(const void *X, const int32_t *row_src, int k, i
 }
 
 // ---------------------------------------------------------------------------
+moe_status moe_ffn_train_plan(int T, int k, int G, int H, int F, int *forward_rows, int *backward_rows,
+                              int *persistent_down) {
+    const moe_status st = check_train_ffn(true, k, T, G, H, F, MOE_BF16);
+    if (st != MOE_OK) return st;
+    if (!forward_rows || !backward_rows || !persistent_down) return MOE_ERR_INVALID_ARG;
+    const long long M = (long long)T * k;
+    ForwardWs f;
+    BackwardWs b;
+    f.carve(nullptr, M, G, H, F);
+    b.carve(nullptr, T, M, G, H, F);
+    *forward_rows = f.t.bm;
+    *backward_rows = b.t.bm;
+    *persistent_down = f.persist;
+    return MOE_OK;
+}
+
+// ---------------------------------------------------------------------------
 size_t moe_ffn_train_backward_workspace_bytes(int T, int k, int G, int H, int F) {
     if (check_train_ffn(true, k, T, G, H, F, MOE_BF16) != MOE_OK) return 0;
     BackwardWs w;

@@ -331,6 +331,7 @@ FFN_CASES = [
     (4700, 64, 32, 1, 1, False, 0),     # more rows than one window of row numbers
     (4300, 32, 64, 2, 2, True, 0),
     # 256-row tiles: gate/up and dH; dX; a short down projection
+    # (128-row tiles by now: the height follows from both products of a pass; test_gpu_train_tall.py has 256)
     (8200, 128, 2080, 2, 1, True, 0.3), (8200, 2080, 128, 2, 1, True, 0.3), (8200, 2048, 160, 2, 1, False, 0),
     # sums long enough for a split tail: gate/up and dH over H (2 and 4 parts), down and dX over F
     (200, 4128, 64, 2, 1, True, 0), (70, 8256, 96, 2, 2, True, 0), (150, 64, 4160, 2, 2, True, 0.5),

@@ -5,7 +5,7 @@ import ctypes
 
 import mixture_experts_layer_count_amd as moe
 
-UNSUPPORTED = 2
+INVALID, UNSUPPORTED = 1, 2
 F32, BF16 = 0, 1
 FAKE = ctypes.c_void_p(0x1000)  # never dereferenced: validation fails first
 
@@ -29,3 +29,18 @@ def test_router_tokens_past_a_launch():
     ws = moe.lib().moe_balance_loss_workspace_bytes
     assert 0 < ws((1 << 30) - 1024, 1, 1) <= ws((1 << 30) - 64, 1, 1)
     assert ws((1 << 31) - 1, 1, 1) < 1 << 30  # partial rows of 64 tokens
+
+
+def test_train_plan():
+    """The tile heights and the down product of given sizes; refusals as the FFN calls'."""
+    v = [ctypes.c_int(-1) for _ in range(3)]
+    out = [ctypes.byref(x) for x in v]
+    plan = moe.lib().moe_ffn_train_plan
+    for sizes, want in (((4096, 2, 8, 4096, 14336), [256, 256, 0]), ((4096, 1, 32, 7168, 2048), [128, 128, 0]),
+                        ((8192, 8, 128, 2048, 768), [256, 256, 1]), ((1536, 2, 8, 640, 416), [128, 128, 0]),
+                        ((0, 1, 1, 32, 32), [128, 128, 0])):
+        assert plan(*sizes, *out) == 0 and [x.value for x in v] == want, sizes
+    assert plan(64, 65, 8, 256, 96, *out) == UNSUPPORTED and plan(64, 2, 8, 250, 96, *out) == UNSUPPORTED
+    assert plan(-1, 2, 8, 256, 96, *out) == INVALID and plan(64, 0, 8, 256, 96, *out) == INVALID
+    for i in range(3):
+        assert plan(64, 2, 8, 256, 96, *(None if j == i else o for j, o in enumerate(out))) == INVALID
