@@ -8,6 +8,7 @@ import torch
 import mixture_experts_layer_count_amd as moe
 from mixture_experts_layer_count_amd import _lib
 from _gpu import say
+import test_gpu_train_tall as tall
 from test_gpu_train import _backward, _dev, _ffn_case, _forward
 
 pytestmark = pytest.mark.gpu
@@ -46,4 +47,27 @@ def test_debug_build_catches_row_src(debug_lib, bad):
         _backward(planted, ck, need=("dtopk_w",))
         assert debug_lib.moe_debug_bounds() == _lib.MOE_BOUNDS_A_ROW
     for a, b in zip((Yp, dX, dw, *dW), ref):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,H,F,E,k,skew,kernels", [
+    (17000, 544, 608, 7, 2, 0.8, (256, 256, False)),
+    (16500, 512, 320, 4, 2, 0.3, (256, 256, True)),
+    (33000, 288, 4128, 3, 1, 0.1, (256, 256, False)),   # split last rounds of DOWN and DX
+    (200, 4128, 64, 2, 1, 0.1, (128, 128, False)),      # and of 128-row GATE_UP and BACK
+    (9000, 64, 96, 2, 1, 0.2, (128, 128, False)),       # experts of more rows than one window of row numbers
+])
+def test_debug_build_tall_and_split(debug_lib, T, H, F, E, k, skew, kernels):
+    say(f"[train bounds] ffn T={T} H={H} F={F} E={E} k={k}")
+    assert tall.plan(T, H, F, E, k) == kernels
+    d = tall._case(T, H, F, E, k, skew)
+    Yp, ck = tall._forward(d)
+    got = tall._backward(d, ck)
+    torch.cuda.synchronize()
+    with _lib.use_library(debug_lib):
+        debug_lib.moe_debug_bounds()
+        Yd, cd = tall._forward(d)
+        gd = tall._backward(d, cd)
+        assert debug_lib.moe_debug_bounds() == 0
+    for a, b in zip((Yp, *ck, *got), (Yd, *cd, *gd)):
         assert torch.equal(a, b)
