@@ -521,10 +521,11 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
             wave_lds_sync();
             const uint32_t sb = *reinterpret_cast<const uint32_t *>(ss + 4 * i16);
             const float wt = __shfl(row_w[m / 4], 16 * (m % 4) + i16);
-            float dw = 0.0f;
+            float dw = 0.0f, dw_half = 0.0f;
             f32x4 dg[NB], du[NB], hw[NB];
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
+                if (j == NB / 2) dw_half = dw;
                 const uint32_t gw = *reinterpret_cast<const uint32_t *>(sc + i16 * R::cld + 16 * j + 4 * gq);
                 const uint32_t uw = *reinterpret_cast<const uint32_t *>(sc + (16 + i16) * R::cld + 16 * j + 4 * gq);
                 const f32x4 gv = mx8::values4(gw, mx8::scale_of((uint8_t)(sb >> (8 * (j / 2)))));
@@ -545,6 +546,8 @@ __global__ __launch_bounds__(512, 1) void rows_gemm_kernel(RowsProblem p, int nN
             store_lines(p.dGU, 2 * p.N, m, dg);
             store_lines(p.dGU + p.N, 2 * p.N, m, du);
             store_lines(p.Hw, p.N, m, hw);
+            // columns past N (N % 32 == 0) have h = 0, but their p may be infinite
+            if (c0 + 32 >= p.N) dw = dw_half;
             dw += __shfl_xor(dw, 16);
             dw += __shfl_xor(dw, 32);
             if (gq == 0) sdw[wc * BM + wr * (BM / 2) + 16 * m + i16] = c0 < p.N ? dw : 0.0f;

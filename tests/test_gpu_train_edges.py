@@ -1,0 +1,40 @@
+"""GPU: values and calls at the edges of what the training operators document."""
+import pytest
+import torch
+
+import mixture_experts_layer_count_amd as moe
+from _gpu import say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    moe.lib()
+
+
+@pytest.mark.parametrize("F", [32, 96, 160, 288, 480])
+def test_infinite_gradient_beside_part_full_columns(F):
+    """A column tile that the matrix ends inside holds columns that do not
+    exist. An infinite dY with positive weights and activations makes the
+    routing weight's gradient +inf, and every other output what the formula
+    says; the missing columns add nothing (not inf * 0)."""
+    say(f"[train edges] infinite dY, F={F}")
+    T, H = 20, 64
+    g = torch.Generator().manual_seed(F)
+    pos = lambda *s: (0.1 + torch.rand(*s, generator=g)).bfloat16().cuda()  # noqa: E731
+    X, W1, W3, W2, dY = pos(T, H), pos(1, H, F), pos(1, H, F), pos(1, F, H), pos(T, H)
+    off = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    _, ck = moe.ffn_train_forward(X, off, W1, W3, W2)
+    t = 7
+    dY[t, 3] = float("inf")
+    dX, dw, dW1, dW3, dW2 = moe.ffn_train_backward(dY, ck, off, W1, W3, W2)
+    rest = [i for i in range(T) if i != t]
+    # g, u > 0: p, dg and du are +inf in every column, and so are their sums
+    assert torch.isfinite(dw[rest]).all() and torch.isfinite(dX[rest]).all()
+    assert (dw[t] == float("inf")).all() and (dX[t] == float("inf")).all()
+    assert (dW1 == float("inf")).all() and (dW3 == float("inf")).all()
+    assert (dW2[0, :, 3] == float("inf")).all()
+    assert torch.isfinite(dW2[0][:, [i for i in range(H) if i != 3]]).all()
