@@ -357,7 +357,8 @@ moe_status moe_ep_local_experts(const moe_ep_record *recv_meta, int n, int E, in
  * lse = 0. A NaN or +inf logit makes the losses NaN. T == 0 writes zeros.
  * fp32; sums in a fixed order, identical run to run.
  * E <= 1024, k <= min(E, 64), B <= 65535, T <= 2^30 - 64, T*E < 2^31.
- * Workspace: moe_balance_loss_workspace_bytes bytes (device, any contents). */
+ * Workspace: moe_balance_loss_workspace_bytes bytes (device, any contents,
+ * 4-byte aligned). */
 size_t moe_balance_loss_workspace_bytes(int T, int E, int B);
 moe_status moe_balance_loss(const float *logits, const int32_t *topk_idx, int T, int E, int k,
                             const int32_t *seq_offsets, int B, float alpha, float beta, float *loss, int32_t *counts,
@@ -412,7 +413,7 @@ typedef struct moe_ffn_checkpoint {
  * (Yp, gq, gs, uq, us). dt: BF16 (X, weights and Yp). H, F multiples of 32;
  * G <= 1024; k <= 64; the token matrix (T*H values) below 4 GiB. Tensors
  * 16-byte aligned. T == 0 returns MOE_OK.
- * Workspace: moe_ffn_train_forward_workspace_bytes bytes. */
+ * Workspace: moe_ffn_train_forward_workspace_bytes bytes (16-byte aligned). */
 size_t moe_ffn_train_forward_workspace_bytes(int T, int k, int G, int H, int F);
 moe_status moe_ffn_train_forward(const void *X, const int32_t *row_src, int k, int T, const int32_t *offsets, int G,
                                  int H, int F, const void *W1, const void *W3, const void *W2, moe_dtype dt, void *Yp,
@@ -442,7 +443,7 @@ moe_status moe_ffn_train_plan(int T, int k, int G, int H, int F, int *forward_ro
  * (experts without rows are left as they were; with 0 they get zeros, also
  * when T == 0). dX_add [T, H] bf16 or NULL: another path's gradient (the
  * shared expert's, the residual's); may be dX itself.
- * Workspace: moe_ffn_train_backward_workspace_bytes bytes. */
+ * Workspace: moe_ffn_train_backward_workspace_bytes bytes (16-byte aligned). */
 size_t moe_ffn_train_backward_workspace_bytes(int T, int k, int G, int H, int F);
 moe_status moe_ffn_train_backward(const void *dY, const float *topk_w, const int32_t *row_src,
                                   const int32_t *assign_row, int k, int T, const int32_t *offsets, int G, int H, int F,

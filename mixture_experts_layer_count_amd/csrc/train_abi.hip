@@ -168,7 +168,9 @@ moe_status moe_balance_loss(const float *logits, const int32_t *topk_idx, int T,
     const moe_status st = check_router(T, E, k, B, seq_offsets);
     if (st != MOE_OK) return st;
     if ((T > 0 && (!logits || !topk_idx)) || !loss || !counts || !seq_counts) return MOE_ERR_INVALID_ARG;
-    if (!ws || ws_bytes < balance_ws_bytes(T, E, B)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    // 4-byte aligned: it holds a counter
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 3) || ws_bytes < balance_ws_bytes(T, E, B))
+        return MOE_ERR_WORKSPACE_TOO_SMALL;
     return hip_status(launch_balance_loss(logits, topk_idx, T, E, k, seq_offsets, B, alpha, beta, loss, counts,
                                           seq_counts, ws, stream));
 }

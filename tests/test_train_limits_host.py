@@ -5,7 +5,7 @@ import ctypes
 
 import mixture_experts_layer_count_amd as moe
 
-INVALID, UNSUPPORTED = 1, 2
+INVALID, UNSUPPORTED, WS_SMALL = 1, 2, 3
 F32, BF16 = 0, 1
 FAKE = ctypes.c_void_p(0x1000)  # never dereferenced: validation fails first
 
@@ -44,3 +44,11 @@ def test_train_plan():
     assert plan(-1, 2, 8, 256, 96, *out) == INVALID and plan(64, 0, 8, 256, 96, *out) == INVALID
     for i in range(3):
         assert plan(64, 2, 8, 256, 96, *(None if j == i else o for j, o in enumerate(out))) == INVALID
+
+
+def test_balance_loss_workspace_alignment():
+    """The workspace holds counters and fp32 sums: off the 4-byte boundary it is refused."""
+    loss = moe.lib().moe_balance_loss
+    for at in (0x1001, 0x1002, 0x1003):
+        assert loss(FAKE, FAKE, 64, 8, 2, None, 1, 0.1, 0.1, FAKE, FAKE, FAKE, ctypes.c_void_p(at), 1 << 50,
+                    None) == WS_SMALL
