@@ -782,6 +782,8 @@ def ffn_train_backward(dY, ckpt, offsets, W1, W3, W2, topk_w=None, row_src=None,
         if "dW" not in need:
             raise ValueError("dW buffers need dW")
         grads = tuple(dW)
+        if len(grads) != 3:
+            raise ValueError("dW must be (dW1, dW3, dW2)")
         dw_dtype = grads[0].dtype
     if dw_dtype not in _DW_DTYPES:
         raise TypeError(f"weight gradients must be float32 or bfloat16, got {dw_dtype}")

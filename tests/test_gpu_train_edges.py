@@ -38,3 +38,21 @@ def test_infinite_gradient_beside_part_full_columns(F):
     assert (dW1 == float("inf")).all() and (dW3 == float("inf")).all()
     assert (dW2[0, :, 3] == float("inf")).all()
     assert torch.isfinite(dW2[0][:, [i for i in range(H) if i != 3]]).all()
+
+
+def test_weight_gradient_buffers_come_in_threes():
+    """dW is (dW1, dW3, dW2): another number of buffers is refused by name, and
+    nothing is added to any of them."""
+    say("[train edges] dW of two and of four buffers")
+    T, H, F = 8, 64, 32
+    g = torch.Generator().manual_seed(1)
+    bf = lambda *s: torch.randn(*s, generator=g).bfloat16().cuda()  # noqa: E731
+    X, W1, W3, W2, dY = bf(T, H), bf(1, H, F), bf(1, H, F), bf(1, F, H), bf(T, H)
+    off = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    _, ck = moe.ffn_train_forward(X, off, W1, W3, W2)
+    bufs = [torch.ones_like(w) for w in (W1, W3, W2, W1)]
+    for n in (0, 1, 2, 4):
+        with pytest.raises(ValueError, match="dW1, dW3, dW2"):
+            moe.ffn_train_backward(dY, ck, off, W1, W3, W2, dW=bufs[:n])
+    torch.cuda.synchronize()
+    assert all((b == 1).all() for b in bufs)
