@@ -386,7 +386,8 @@ moe_status moe_route_backward(const float *logits, const int32_t *topk_idx, cons
  *   S[r, c] = e + 127 (E8M0 byte),  Q[r, j] = E4M3(x[j] * 2^-e), round to
  *   nearest, ties to even (nothing saturates; NaN and infinities give NaN).
  * Unpacking gives decode(Q) * 2^(S - 127), exact in bf16 and fp32 (values
- * below 2^-126 may be flushed to zero). X [R, ldx] F32 or BF16, its first C
+ * below 2^-126 may be flushed to zero); the scale byte 255, which packing never
+ * writes, makes its values NaN. X [R, ldx] F32 or BF16, its first C
  * columns; C a multiple of 32, at most 2^20, and R * C at most 2^36 - 4096;
  * ldx >= C, ldx * element size a multiple of 16;
  * Q [R, C], S [R, C/32]; Y [R, C]. X, Q and Y 16-byte aligned. Bit-exact. */

@@ -56,3 +56,12 @@ def test_weight_gradient_buffers_come_in_threes():
             moe.ffn_train_backward(dY, ck, off, W1, W3, W2, dW=bufs[:n])
     torch.cuda.synchronize()
     assert all((b == 1).all() for b in bufs)
+
+
+def test_scale_byte_of_no_number():
+    """E8M0's byte 255 stands for no number: every value under it is NaN."""
+    say("[train edges] scale byte 255")
+    Q = torch.arange(256, dtype=torch.uint8).reshape(8, 32).cuda()
+    S = torch.full((8, 1), 255, dtype=torch.uint8, device="cuda")
+    for dt in (torch.bfloat16, torch.float32):
+        assert torch.isnan(moe.checkpoint_unpack(Q, S, dt)).all()
