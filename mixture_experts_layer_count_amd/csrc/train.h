@@ -80,7 +80,9 @@ struct RowsProblem {
     float *part = nullptr;
     int32_t *part_cnt = nullptr;
 };
-int rows_gemm_bm(long long rows, int groups, int columns);  // rows per tile; columns: column tiles
+// rows per tile of a pass's products; columns: the fewer of their column tiles
+enum RowsPass { ROWS_FORWARD, ROWS_BACKWARD };
+int rows_gemm_bm(RowsPass pass, long long rows, int groups, int columns);
 constexpr int rows_gemm_bn = 256;  // B columns per tile
 constexpr int rows_gemm_counters = 256;
 int rows_gemm_columns(int N, RowsUse use);  // column tiles

@@ -119,7 +119,7 @@ struct ForwardWs {
     uint16_t *h;  // [M][F]
     size_t carve(void *ws, long long M, int G, int H, int F) {
         Carver c(ws);
-        t.carve(c, M, G, rows_gemm_bm(M, G, columns(F, ROWS_GATE_UP, H, ROWS_DOWN)));
+        t.carve(c, M, G, rows_gemm_bm(ROWS_FORWARD, M, G, columns(F, ROWS_GATE_UP, H, ROWS_DOWN)));
         parts.carve(c, t, H, ROWS_GATE_UP, F, ROWS_DOWN);
         persist = F <= kPersistDepth && tiled_persist_fits(down_problem(t, (int)M, G, H, F), W_BF16, false, t.bm);
         h = static_cast<uint16_t *>(c.take(2 * (size_t)M * F));
@@ -137,7 +137,7 @@ struct BackwardWs {
     float *dw_part; // [column tiles of F][M]
     size_t carve(void *ws, long long T, long long M, int G, int H, int F) {
         Carver c(ws);
-        t.carve(c, M, G, rows_gemm_bm(M, G, columns(F, ROWS_BACK, H, ROWS_DX)));
+        t.carve(c, M, G, rows_gemm_bm(ROWS_BACKWARD, M, G, columns(F, ROWS_BACK, H, ROWS_DX)));
         parts.carve(c, t, H, ROWS_BACK, F, ROWS_DX);
         x = static_cast<uint16_t *>(c.take(2 * (size_t)T * H));
         dgu = static_cast<uint16_t *>(c.take(4 * (size_t)M * F));

@@ -585,12 +585,26 @@ hipError_t launch_rows(const RowsProblem &p, RowsUse use, hipStream_t s) {
 }  // namespace
 }  // namespace tiled
 
-// 256-row tiles where experts average 192 rows (as the inference tiles) and
-// there are enough of them for one round of the CUs; else 128, whose items take
-// half as long (8 experts, T 1536, k 2, H 640, F 416)
-int rows_gemm_bm(long long rows, int groups, int columns) {
+// 256-row tiles read B half as often and have half as many items to start and
+// end; 128-row ones leave fewer rows of an expert's last tile empty. Taken: 256
+// where both hold, else 128.
+//  * Experts average kTallRows rows. Whole calls, 128 against 256 (us; experts
+//    x H x F): forward at 192 rows an expert 271 to 320 (16 x 4096 x 2048), 425
+//    to 438 (128 x 2048 x 768), 836 to 853 (8 x 4096 x 14336), at 224 335 to
+//    320, 458 to 451, 965 to 875, at 384 426 to 365, 660 to 608, 1389 to 1166;
+//    backward at 224 678 to 688, 997 to 1017, 2020 to 2060, at 288 771 to 740,
+//    1152 to 1151, 2377 to 2324, at 384 856 to 819, 1386 to 1392, 2807 to 2597.
+//    (64 experts of 2048 x 768, the shape that gains least: 4 % slower at 256
+//    in the forward, 1 % at 288 in the backward.)
+//  * 128-row tiles would need a second round of the CUs. Forward at 128 tiles
+//    of 256 rows 45 to 58 (4 x 1024 x 512), 126 to 142 (4 x 1536 x 2048), at 144
+//    70 to 59, 153 to 146; backward at 126 132 to 156 (8 x 768 x 768), 258 to
+//    281, at 144 178 to 165, 302 to 310, at 200 210 to 203, 391 to 402.
+int rows_gemm_bm(RowsPass pass, long long rows, int groups, int columns) {
+    const long long kTallRows = pass == ROWS_FORWARD ? 224 : 288;
     const long long tiles = rows / 256 + groups / 2;  // about half a tile of each expert is a rest
-    return groups > 0 && rows >= 192LL * groups && tiles * columns >= tiled::kXcds * tiled::kBlocksPerXcd ? 256 : 128;
+    const long long cus = tiled::kXcds * tiled::kBlocksPerXcd;
+    return groups > 0 && rows >= kTallRows * groups && 2 * tiles * columns > cus ? 256 : 128;
 }
 int rows_gemm_columns(int N, RowsUse use) {
     const int w = use == ROWS_GATE_UP ? rows_gemm_bn / 2 : rows_gemm_bn;

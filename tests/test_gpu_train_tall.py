@@ -1,9 +1,8 @@
 """GPU: the expert FFN's training passes where they take 256-row tiles.
 
-The tile height follows from the sizes of the whole pass (experts of 192 rows
+The tile height follows from the sizes of the whole pass (the rows of an expert
 on average, and row tiles times the fewer column tiles of the pass's two
-products enough for the chip), so each case first asks the library which
-kernels it takes, and for the split cases works out that their last round is
+products), so each case first asks the library which kernels it takes, and for the split cases works out that their last round is
 split. The oracle is the definition in 64 bits on the GPU; bounds are formed
 from its own terms: u = 2^-24 for each fp32 operation of a sum (at most its
 length times u times the sum of magnitudes), half = 2^-8 for each rounding to
@@ -153,7 +152,10 @@ CASES = [
     (40000, 288, 352, 1, 1, 0.0, (256, 256, False), {}),      # in row order
     # the persistent down product
     (16500, 512, 320, 4, 2, 0.3, (256, 256, True), {}),
-    (4200, 2048, 1024, 4, 2, 0.1, (256, 128, True), {}),
+    (4200, 2048, 1024, 4, 2, 0.1, (256, 256, True), {}),
+    # 256 rows in one pass only: by the tiles (forward 192, backward 96), by the rows (256 an expert)
+    (6000, 1024, 512, 4, 2, 0.1, (256, 128, True), {}),
+    (16384, 512, 512, 64, 1, 0.0, (256, 128, True), {}),
     # sums long enough for a split last round: over H, and over F
     (22000, 4128, 800, 4, 1, 0.1, (256, 256, False), {"GATE_UP": 2, "BACK": 2}),
     (33000, 288, 4128, 3, 1, 0.1, (256, 256, False), {"DOWN": 2, "DX": 4}),
