@@ -108,8 +108,13 @@ GemmProblem down_problem(const Tiles &t, int M, int G, int H, int F) {
 }
 
 // down projections of at most this depth take the persistent kernel where it
-// fits: its items overlap, which counts while they are short (F 768: 257 to
-// 287 us against 286 to 326 on 65536 rows, H 2048)
+// fits: its items overlap, which counts while they are short. Whole forwards,
+// row product against persistent (us): 65536 rows, 128 experts, H 2048, F 512
+// 559 to 529, 768 762 to 734, 1024 957 to 934, 1536 1396 to 1389, 2048 1802 to
+// 1800; 32768 rows, 16 experts, H 2048, F 512 265 to 256, 1024 446 to 436, 2048
+// 799 to 801; 32 experts, H 4096, F 512 515 to 491, 1024 841 to 825, 2048 1526
+// to 1506. Deeper ones are as fast either way, and the row product splits its
+// last round where that is short
 constexpr int kPersistDepth = 1024;
 
 struct ForwardWs {
