@@ -13,15 +13,18 @@
 // renormalised top-k weights, a softmax over the k kept logits). A row whose
 // logits are all -inf has p = 0 and lse = 0.
 //
-// Bound: HBM (logits read once each way, gradients written once) for many
-// tokens, launch latency for few. A token's logits are held by LPT lanes, V = 4
+// Bound: instruction issue for many tokens (at 256 experts the VALU issues in
+// 0.8 of the CUs' busy cycles, 104 instructions a token in the sums and 187 in
+// the gradient, much of it lane reductions of six dependent steps that serve one
+// token of a wavefront; the logits come at less than a copy's 4.9 TB/s), launch
+// latency for few. A token's logits are held by LPT lanes, V = 4
 // (16-byte loads) or 1 consecutive experts a lane, NI such pieces: LPT is the
 // smallest power of two that covers E, so a layer of 8 experts puts 32 tokens
 // on a wavefront and 256 experts one.
 //
-// Measured (sums, second kernel, gradient): 64 tokens of 8 experts 3, 4 and
-// 3.7 us; 8192 of 128 5.9, 6 and 8.2; 65536 of 256 18.5 (67 MB and the picks at
-// 3.7 TB/s), 5.3 and 31 (136 MB at 4.4 TB/s).
+// Measured (sums, second kernel, gradient; medians): 64 tokens of 8 experts 3.0,
+// 3.8 and 3.8 us; 8192 of 128 5.9, 7.2 and 8.2; 65536 of 256 19.6 (67 MB and the
+// picks at 3.5 TB/s), 5.3 and 32.5 (140 MB at 4.3 TB/s).
 //
 // The sums over tokens are formed in a fixed order, so results are identical
 // run to run: a block sums the tokens of one chunk, sequence by sequence, and

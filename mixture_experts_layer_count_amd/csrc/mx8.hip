@@ -5,8 +5,9 @@
 // owns 16 consecutive values: two (fp32: four) 16-byte loads, one 16-byte
 // code store; the two threads of a group exchange their maxima with one
 // shuffle, and one of them stores the group's scale byte (32 contiguous bytes
-// a wavefront). 32768 x 4096 bf16: packed in 69 us (5.9 TB/s), read back in 64
-// (6.4 TB/s; the 256 MB cache holds part of it).
+// a wavefront). 32768 x 4096, medians: bf16 packed in 83 us (4.9 TB/s; at best
+// 69), read back in 66 (6.2 TB/s; the 256 MB cache holds part of it); fp32
+// packed in 119 (5.7 TB/s), read back in 174 (3.9 TB/s, 537 MB of it written).
 #include "mx8.h"
 #include "schedule.h"
 

@@ -33,11 +33,14 @@
 // first while the second is, so one barrier a step (after the next step's
 // copies have landed) both publishes the next stage and frees this one.
 //
-// Measured: 8 experts, 8192 rows, H 4096, F 14336: BACK 1040 us (925 TFLOP/s,
-// 0.44 of the matrix cores' cycles at 2.1 GHz), DX 1890 (1018); 128 experts,
-// 65536 rows, H 2048, F 768: GATE_UP 480-575, BACK 320, DX 565 (730 TFLOP/s: a
-// quarter of the tiles' rows are past an expert's end); 32 experts, 4096 rows,
-// H 7168, F 2048: GATE_UP 495, DOWN 235, BACK 325, DX 493 (2.4 GB at 4.9 TB/s,
+// Measured (medians): 8 experts, 8192 rows, H 4096, F 14336: BACK 1052 us (914
+// TFLOP/s, 0.44 of the matrix cores' cycles at 2.0 GHz), DX 1895 (1015); 128
+// experts, 65536 rows, H 2048, F 768: GATE_UP 587 (at best 473), BACK 343, DX 591
+// (698 TFLOP/s, 0.35 of the cycles. A quarter of the tiles' rows are past an
+// expert's end, but empty blocks are left out by 64 rows and 6 % of the
+// multiplied ones are empty: the rest is a tile's start of about 6 us, BACK's
+// epilogue of 15 and DX's stores, beside 24 to 32 steps); 32 experts, 4096 rows,
+// H 7168, F 2048: GATE_UP 506, DOWN 244, BACK 328, DX 493 (2.4 GB at 4.9 TB/s,
 // a copy's rate). Time stamps show 13 to 18 % of the CUs' time between items
 // and after the last, yet a persistent form that removed it took as long: the
 // card runs at its power limit, and idle CUs leave their share to the others.

@@ -23,11 +23,14 @@
 // rows, filling the ring and storing.) dW2's items follow in the same launch:
 // its own launch took 33 us of 117 (8 experts, T 1536, k 2, H 640, F 416).
 //
-// Measured, all three gradients in bf16: 128 experts, 65536 rows, H 2048,
-// F 768: 728 us (850 TFLOP/s); 8 experts, 8192 rows, H 4096, F 14336: 2650 us
-// (1089 TFLOP/s; 0.52 of the matrix cores' cycles at 2.0 of 2.4 GHz, the power
-// limit's clock); 32 experts, 4096 rows, H 7168, F 2048: 790 us, 3.4 GB of
-// memory traffic at 4.3 TB/s. A step takes 0.97 to 1.2 us, a tile's stores 2.4.
+// Measured, all three gradients in bf16 (medians): 128 experts, 65536 rows,
+// H 2048, F 768: 801 us (772 TFLOP/s; at best 746); 8 experts, 8192 rows, H 4096,
+// F 14336: 2765 us (1044 TFLOP/s; 0.52 of the matrix cores' cycles at 2.0 of 2.4
+// GHz, the power limit's clock); 32 experts, 4096 rows, H 7168, F 2048: 775 us,
+// 3.4 GB of memory traffic at 4.4 TB/s. A step takes 0.97 to 1.2 us, a tile's
+// stores 2.4. In fp32: 945, 3280 and 1217 us. Added to what C holds: in bf16
+// 1054, 3569 and 1700, in fp32 1406, 4320 and 2513: each 16-row block waits for
+// its values of C, and the copy ring for the tile's stores.
 //
 // Work order: experts by falling row count, an expert's tiles in bands of
 // kBand tile rows, column by column; consecutive runs of 32 tiles (one per CU)
