@@ -92,16 +92,23 @@ __device__ __forceinline__ void seq_range(const BalanceArgs &a, int b, int &lo, 
     lo = a.seq ? min(max(a.seq[b], 0), a.T) : 0;
     hi = a.seq ? min(max(a.seq[b + 1], lo), a.T) : a.T;
 }
-// the first sequence that ends after token t (B if none)
-__device__ __forceinline__ int first_seq(const BalanceArgs &a, int t) {
-    if (!a.seq) return 0;
-    int lo = 0, hi = a.B;
+// the first sequence from b on that ends after token t (B if none). The offsets
+// of a padded batch end in many empty sequences: one by one they took 0.17 us
+// each (8192 tokens, the last 191 outside all of 1024 sequences: 207 us of loss
+// and 149 of gradient in place of 43 and 13)
+__device__ __forceinline__ int first_seq(const BalanceArgs &a, int b, int t) {
+    if (!a.seq) return b;
+    int lo = b, hi = a.B;
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (a.seq[mid + 1] > t) hi = mid;
         else lo = mid + 1;
     }
     return lo;
+}
+// the same where b itself is the likely one
+__device__ __forceinline__ int next_seq(const BalanceArgs &a, int b, int t) {
+    return b >= a.B || !a.seq || a.seq[b + 1] > t ? b : first_seq(a, b + 1, t);
 }
 
 template <int V, int NI, int LPT>
@@ -169,13 +176,14 @@ __global__ __launch_bounds__(kThreads) void balance_sums_kernel(BalanceArgs a, f
         for (int e = tid; e < a.E; e += kThreads) counts[e] = 0;
     }
     const int t0 = blockIdx.x * a.chunk, t1 = min(t0 + a.chunk, a.T);
-    for (int b = first_seq(a, t0); b < a.B; ++b) {
+    for (int b = first_seq(a, 0, t0), pos = t0; b < a.B; b = next_seq(a, b + 1, pos)) {
         int lo, hi;
         seq_range(a, b, lo, hi);
         if (lo >= t1) break;
         lo = max(lo, t0);
         hi = min(hi, t1);
-        if (lo >= hi) continue;  // an empty sequence
+        pos = max(pos, hi);
+        if (lo >= hi) continue;  // an empty sequence in front of all
         for (int e = tid; e < a.E; e += kThreads) sC[e] = 0;
         __syncthreads();
         for (long long i = (long long)lo * a.k + tid; i < (long long)hi * a.k; i += kThreads) {
@@ -228,6 +236,7 @@ __global__ __launch_bounds__(kThreads) void balance_sums_kernel(BalanceArgs a, f
             partC[slot * a.E + e] = sC[e];
         }
         if (tid == 0) partZ[slot] = (sZ[0] + sZ[1]) + (sZ[2] + sZ[3]);
+        if (hi == t1) break;
         __syncthreads();
     }
 }
@@ -382,15 +391,15 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(BalanceArgs a,
     }
     const float d0 = g.dloss ? g.dloss[0] : 1.0f, d1 = g.dloss ? g.dloss[1] : 1.0f;
     // [pos, end): a run of tokens of one sequence, or of none
-    int b = aux ? first_seq(a, t0) : a.B;
+    int b = aux ? first_seq(a, 0, t0) : a.B;
     int pos = t0;
     while (pos < t1) {
         int end = t1;
         bool in_seq = false;
         int lo = 0, hi = 0;
-        for (; b < a.B; ++b) {
+        for (; b < a.B; b = next_seq(a, b + 1, pos)) {
             seq_range(a, b, lo, hi);
-            if (hi <= pos) continue;  // empty, or behind
+            if (hi <= pos) continue;  // behind
             in_seq = lo <= pos;
             end = min(t1, in_seq ? hi : lo);
             break;

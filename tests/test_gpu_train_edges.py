@@ -4,6 +4,7 @@ import torch
 
 import mixture_experts_layer_count_amd as moe
 from _gpu import say
+from test_gpu_train import _check_router, _router
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +66,46 @@ def test_scale_byte_of_no_number():
     S = torch.full((8, 1), 255, dtype=torch.uint8, device="cuda")
     for dt in (torch.bfloat16, torch.float32):
         assert torch.isnan(moe.checkpoint_unpack(Q, S, dt)).all()
+
+
+@pytest.mark.parametrize("seq", [
+    [0] * 40 + [7] * 30 + [8] * 3 + [60] * 50 + [97] * 200,     # empty ones first, between and last; 3 tokens behind
+    [5] * 20 + [5, 40] + [40] * 300,                            # tokens in front of all, 60 behind
+    [0, 100] + [100] * 500, [50] * 400, [0] * 100 + [100] * 100,
+])
+def test_router_losses_many_empty_sequences(seq):
+    say(f"[train edges] router losses, {len(seq) - 1} sequences, few of them with tokens")
+    _check_router(*_router(100, 16, 3, len(seq)), seq)
+
+
+def test_router_losses_padded_batch_time():
+    """A batch padded to a fixed number of sequences, with padding tokens behind
+    them, takes about as long as one whose last sequence reaches the end: the
+    empty sequences are not walked one by one (that took 6 and 35 times as
+    long)."""
+    say("[train edges] router losses of a padded batch, time")
+    T, E, k, B = 8192, 128, 8, 4096
+    z, idx, w, dw = (t.cuda() for t in _router(T, E, k, 3))
+
+    def times(last):
+        seq = torch.tensor([last * i // 8 for i in range(9)] + [last] * (B - 8), dtype=torch.int32, device="cuda")
+        per = moe.balance_loss(z, idx, 0.1, 0.1, seq_offsets=seq)[2]
+        out = []
+        for f in (lambda: moe.balance_loss(z, idx, 0.1, 0.1, seq_offsets=seq),
+                  lambda: moe.route_backward(z, idx, w, dw, per, 0.1, 0.1, seq_offsets=seq)):
+            t = []
+            for _ in range(7):
+                a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+                f()
+                a.record()
+                for _ in range(5):
+                    f()
+                b.record()
+                torch.cuda.synchronize()
+                t.append(a.elapsed_time(b))
+            out.append(sorted(t)[3])
+        return out
+
+    times(T)
+    for padded, whole in zip(times(T - 191), times(T)):
+        assert padded < 3 * whole
