@@ -51,7 +51,7 @@
  *    path in registers, the tiled path after staging codes and scales in LDS)
  *    and multiply in bf16; the workspace is the bf16 one. Scale code 0 is
  *    2^-127; code 255 (NaN) makes the outputs that depend on it non-finite.
- *    TILED_A8 is refused.
+ *    TILED_A8 is refused; TILED_A4 multiplies the codes as they are.
  *    H and F must be multiples of 32 and at most 2^20; E <= 1024;
  *    1 <= k <= min(E, 64); moe_route needs T*E < 2^31, moe_permute T*k < 2^31,
  *    moe_forward T <= 65535. Larger sizes return MOE_ERR_UNSUPPORTED (and the
@@ -100,8 +100,20 @@ typedef enum {
  *    with scale amax/448 (page "MOE推理流程解析" §三: activations quantised
  *    before the expert GEMM) and multiplied on the FP8 matrix cores (W8A8);
  *    h is quantised inside the gate/up GEMM, from its bf16 values.
- *    In moe_forward it needs Fs == 0 or Fs == F. */
-typedef enum { MOE_PATH_AUTO = 0, MOE_PATH_GEMV = 1, MOE_PATH_TILED = 2, MOE_PATH_TILED_A8 = 3 } moe_ffn_path;
+ *    In moe_forward it needs Fs == 0 or Fs == F.
+ *  TILED_A4 (MXFP4 weights only): the expert inputs (token rows, then h) are
+ *    quantised to MXFP4 as moe_quantize_mxfp4_rows does and multiplied on the
+ *    4-bit matrix cores (W4A4), for any number of rows; h is quantised inside
+ *    the gate/up GEMM, from its fp32 values. AUTO never picks it: it rounds
+ *    activations to 4 bits. A row with a NaN or infinity gives NaN outputs. In
+ *    moe_forward an MXFP4 shared expert needs Fs == F (a bf16 one does not). */
+typedef enum {
+    MOE_PATH_AUTO = 0,
+    MOE_PATH_GEMV = 1,
+    MOE_PATH_TILED = 2,
+    MOE_PATH_TILED_A8 = 3,
+    MOE_PATH_TILED_A4 = 5 /* 4 is no path */
+} moe_ffn_path;
 
 /* Static string for a status code (host memory, never NULL). */
 const char *moe_status_string(moe_status s);
@@ -190,6 +202,35 @@ moe_status moe_grouped_ffn(const void *Xin, const int32_t *row_src, int k, int M
  * ------------------------------------------------------------------------- */
 moe_status moe_quantize_e4m3_rows(const void *X, moe_dtype x_dt, long long ldx, const int32_t *row_src,
                                   int gk, int R, int C, uint8_t *Q, float *S, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * MXFP4: making and reading back what the MXFP4 experts are kept in, and rows
+ * in the same format (page "MoE-推理部署", expert-quantisation section). For
+ * each group of 32 values (consecutive columns of a row; consecutive K rows of
+ * a weight column), with amax its largest magnitude:
+ *   e = floor(log2 amax) - 2, at least -127 (0 when amax = 0),  S = e + 127,
+ *   Q = E2M1(x * 2^-e): the nearest of 0, .5, 1, 1.5, 2, 3, 4, 6, ties to the
+ *   even code, magnitudes past 6 to 6, the sign kept.
+ * A group that holds a NaN or an infinity gets S = 255 (NaN) and codes 0.
+ * Reading back gives decode(Q) * 2^(S - 127), exact in bf16 and fp32 (values
+ * below 2^-126 may be flushed to zero); S = 255 gives NaN. dtypes: F32, BF16.
+ *  rows: X [R, ldx] (its first C columns), Q [R, C/2] (byte i of a row: columns
+ *    2i in the low nibble, 2i + 1 in the high one), S [R, C/32], Y [R, C]. C a
+ *    multiple of 32 and at most 2^20; ldx >= C, ldx * element size a multiple
+ *    of 16; R * C at most 2^36 - 4096.
+ *  weights: W [G, K, N], Q [G, K/2, N] (byte (i, n): rows 2i and 2i + 1 of
+ *    column n), S [G, K/32, N]: W1, W3 with (K, N) = (H, F), W2 with (F, H). K a
+ *    multiple of 32, N of 8, each at most 2^20; G * K * N at most 2^36 - 4096.
+ * X, W and Y 16-byte aligned, Q (and the weights' S) 8-byte aligned. R == 0 and
+ * G == 0 return MOE_OK. Bit-exact. */
+moe_status moe_quantize_mxfp4_rows(const void *X, moe_dtype x_dt, long long ldx, long long R, int C, uint8_t *Q,
+                                   uint8_t *S, hipStream_t stream);
+moe_status moe_dequantize_mxfp4_rows(const uint8_t *Q, const uint8_t *S, long long R, int C, moe_dtype y_dt, void *Y,
+                                     hipStream_t stream);
+moe_status moe_quantize_mxfp4_weights(const void *W, moe_dtype w_dt, int G, int K, int N, uint8_t *Q, uint8_t *S,
+                                      hipStream_t stream);
+moe_status moe_dequantize_mxfp4_weights(const uint8_t *Q, const uint8_t *S, int G, int K, int N, moe_dtype w_dt,
+                                        void *W, hipStream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Combine / unpermute:
@@ -452,6 +493,27 @@ moe_status moe_ffn_train_backward(const void *dY, const float *topk_w, const int
                                   const moe_ffn_checkpoint *ckpt, const void *dX_add, void *dX, float *dtopk_w,
                                   void *dW1, void *dW3, void *dW2, moe_dtype dw_dt, int accumulate, void *ws,
                                   size_t ws_bytes, hipStream_t stream);
+
+/* Gradients of moe_permute's rows and of moe_combine, for experts of any form
+ * (moe_ffn_train_backward has both within). With r = assign_row[a], a = t*k + j:
+ *   combine: dYp[r] = topk_w[a] dY[t]      dtopk_w[a] = sum_h Yp[r, h] dY[t, h]
+ *            (moe_combine's S, when given, has the gradient dY itself)
+ *   permute: dX[t] = sum_j dXp[r] (+ dX_add[t])
+ * dY, dX, dX_add [T, H] and Yp, dYp, dXp [T*k, H] in dt (F32 or BF16). Every sum
+ * is fp32 in a fixed order (permute: ascending j, then dX_add), rounded once.
+ * n_rows (device, or NULL for T*k): the rows in use, moe_permute's offsets[E].
+ * An assign_row entry outside [0, *n_rows) is a pick that was left out: it has
+ * dtopk_w = 0 and adds nothing to dX. Rows of dYp that no entry names are left
+ * as they were; no two entries may name one row. dYp or dtopk_w may be NULL and
+ * is then not computed (Yp is read for dtopk_w, topk_w for dYp). dX may be
+ * dX_add, dYp may be Yp; other overlaps are not allowed. H a multiple of 4 and at
+ * most 2^20, k <= 64, T < 2^24, T*k < 2^31, T*H at most 2^34 - 1024. Matrices
+ * 16-byte aligned (8-byte, bf16 with H % 8 = 4). T == 0 returns MOE_OK. */
+moe_status moe_combine_backward(const void *dY, const void *Yp, const int32_t *assign_row, const float *topk_w,
+                                const int32_t *n_rows, int T, int k, int H, moe_dtype dt, void *dYp, float *dtopk_w,
+                                hipStream_t stream);
+moe_status moe_permute_backward(const void *dXp, const int32_t *assign_row, const int32_t *n_rows, int T, int k, int H,
+                                moe_dtype dt, const void *dX_add, void *dX, hipStream_t stream);
 
 /* ---------------------------------------------------------------------------
  * moe_forward without a caller workspace, for callers that cannot allocate

@@ -8,12 +8,15 @@ Python binding, with torch providing device memory and streams.
 """
 from ._lib import (
     EP_STAGES, LIB_PATH, MOE_N_EVENTS, STAGES, EPLoopback, FFNCheckpoint, MoEError, MoELayer, StageEvents,
-    balance_loss, checkpoint_pack, checkpoint_unpack, combine, ep_dispatch, ep_exchange, ep_local_experts,
-    ep_recv_offsets, ffn_train_backward, ffn_train_forward, grouped_ffn, lib, permute, quantize_e4m3_rows,
-    rank_tokens, route, route_backward,
+    balance_loss, checkpoint_pack, checkpoint_unpack, combine, combine_backward, dequantize_mxfp4_rows,
+    dequantize_mxfp4_weights, ep_dispatch, ep_exchange, ep_local_experts, ep_recv_offsets, ffn_train_backward,
+    ffn_train_forward, grouped_ffn, lib, permute, permute_backward, quantize_e4m3_rows, quantize_mxfp4_rows,
+    quantize_mxfp4_weights, rank_tokens, route, route_backward,
 )
 
 __all__ = ["EP_STAGES", "LIB_PATH", "MOE_N_EVENTS", "STAGES", "EPLoopback", "FFNCheckpoint", "MoEError", "MoELayer",
-           "StageEvents", "balance_loss", "checkpoint_pack", "checkpoint_unpack", "combine", "ep_dispatch",
-           "ep_exchange", "ep_local_experts", "ep_recv_offsets", "ffn_train_backward", "ffn_train_forward",
-           "grouped_ffn", "lib", "permute", "quantize_e4m3_rows", "rank_tokens", "route", "route_backward"]
+           "StageEvents", "balance_loss", "checkpoint_pack", "checkpoint_unpack", "combine", "combine_backward",
+           "dequantize_mxfp4_rows", "dequantize_mxfp4_weights", "ep_dispatch", "ep_exchange", "ep_local_experts",
+           "ep_recv_offsets", "ffn_train_backward", "ffn_train_forward", "grouped_ffn", "lib", "permute",
+           "permute_backward", "quantize_e4m3_rows", "quantize_mxfp4_rows", "quantize_mxfp4_weights", "rank_tokens",
+           "route", "route_backward"]

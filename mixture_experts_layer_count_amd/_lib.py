@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(PKG, "libmoe.so")
 (MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_HIP,
  MOE_ERR_SCRATCH_LIMIT) = range(6)
 MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_MXFP4 = 0, 1, 2, 3
-PATHS = {"auto": 0, "gemv": 1, "tiled": 2, "tiled_a8": 3}
+PATHS = {"auto": 0, "gemv": 1, "tiled": 2, "tiled_a8": 3, "tiled_a4": 5}
 # bits of moe_debug_bounds() (the bounds-checked build)
 (MOE_BOUNDS_TILE, MOE_BOUNDS_A_ROW, MOE_BOUNDS_SCALE_ROW, MOE_BOUNDS_TAIL_SLOT, MOE_BOUNDS_PERM_ROW,
  MOE_BOUNDS_COMBINE_ROW, MOE_BOUNDS_QUANT_ROW, MOE_BOUNDS_EP_ROW) = (1 << i for i in range(8))
@@ -39,6 +39,10 @@ SIGNATURES = {
                              _P, _SZ, _P]),
     "moe_quantize_e4m3_rows": (_I, [_P, _I, ctypes.c_longlong, _P, _I, _I, _I, _P, _P, _P]),
     "moe_combine": (_I, [_P, _P, _P, _I, _I, _I, _P, _I, _P, _P]),
+    "moe_quantize_mxfp4_rows": (_I, [_P, _I, ctypes.c_longlong, ctypes.c_longlong, _I, _P, _P, _P]),
+    "moe_dequantize_mxfp4_rows": (_I, [_P, _P, ctypes.c_longlong, _I, _I, _P, _P]),
+    "moe_quantize_mxfp4_weights": (_I, [_P, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_dequantize_mxfp4_weights": (_I, [_P, _P, _I, _I, _I, _I, _P, _P]),
     "moe_forward_workspace_bytes": (_SZ, [_P, _I]),
     "moe_forward": (_I, [_P, _P, _I, _P, _P, _SZ, _P, _P, _P, _P, _P, _P]),
     "moe_forward_noalloc_max_bytes": (_SZ, []),
@@ -59,6 +63,8 @@ SIGNATURES = {
     "moe_ffn_train_backward_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
     "moe_ffn_train_backward": (_I, [_P, _P, _P, _P, _I, _I, _P, _I, _I, _I, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P,
                                     _P, _I, _I, _P, _SZ, _P]),
+    "moe_combine_backward": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_permute_backward": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P]),
     "moe_forward_noalloc": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _P, _P]),
     "moe_debug_bounds": (ctypes.c_uint, []),
 }
@@ -245,9 +251,8 @@ def grouped_ffn(Xin, offsets, W1, W3, W2, S1=None, S3=None, S2=None, row_src=Non
     p = PATHS[path]
     nbytes = lib().moe_grouped_ffn_workspace_bytes(M, G, H, F, adt, wdt, p)
     ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=Xin.device)
-    _check("moe_grouped_ffn", lib().moe_grouped_ffn(
-        _ptr(Xin), _ptr(row_src), k, M, _ptr(offsets), G, H, F, _ptr(W1), _ptr(W3), _ptr(W2), wdt,
-        _ptr(S1), _ptr(S3), _ptr(S2), adt, _ptr(Yp), p, _ptr(ws), nbytes, _stream()))
+    _call("moe_grouped_ffn", Xin.device, _ptr(Xin), _ptr(row_src), k, M, _ptr(offsets), G, H, F, _ptr(W1), _ptr(W3),
+          _ptr(W2), wdt, _ptr(S1), _ptr(S3), _ptr(S2), adt, _ptr(Yp), p, _ptr(ws), nbytes)
     return Yp
 
 
@@ -796,6 +801,112 @@ def ffn_train_backward(dY, ckpt, offsets, W1, W3, W2, topk_w=None, row_src=None,
     _call("moe_ffn_train_backward", dev, gp, tp, rp, ap, k, T, op, G, H, F, *w, MOE_BF16, ctypes.byref(ptrs), ep, xp,
           up, *wg, _DW_DTYPES[dw_dtype], int(dW is not None), wp, nbytes)
     return dX, dtopk_w, *grads
+
+
+def combine_backward(dY, Yp, assign_row, topk_w, n_rows=None, need=("dYp", "dtopk_w")):
+    """-> (dYp [T*k,H], dtopk_w [T,k] f32): the gradients of combine's rows and
+    weights from dY [T,H] at its output (its S has the gradient dY). `n_rows`: int32
+    device tensor whose one value is the rows in use (permute's offsets[-1:]; None:
+    all; rows from there on are not written). `need` names what to compute (the
+    other is None). See moe_combine_backward."""
+    T, k = topk_w.shape
+    H = dY.shape[1]
+    dev = dY.device
+    dt = act_dtype(dY)
+    gp = _want(dY, "dY", (T, H), dY.dtype)
+    ap = _want(assign_row, "assign_row", (T * k,), torch.int32, dev)
+    tp = _want(topk_w, "topk_w", (T, k), torch.float32, dev)
+    yp = None if Yp is None else _want(Yp, "Yp", (T * k, H), dY.dtype, dev)
+    np_ = None if n_rows is None else _want(n_rows, "n_rows", (1,), torch.int32, dev)
+    if set(need) - {"dYp", "dtopk_w"}:
+        raise ValueError("need names dYp and dtopk_w")
+    dYp = dtopk_w = dp = up = None
+    if "dYp" in need:
+        dYp, dp = _new((T * k, H), dY.dtype, dev)
+    if "dtopk_w" in need:
+        if Yp is None:
+            raise ValueError("dtopk_w needs Yp")
+        dtopk_w, up = _new((T, k), torch.float32, dev)
+    _call("moe_combine_backward", dev, gp, yp, ap, tp, np_, T, k, H, dt, dp, up)
+    return dYp, dtopk_w
+
+
+def permute_backward(dXp, assign_row, k: int, dX_add=None, n_rows=None):
+    """dX [T,H]: the gradient of permute's input tokens from dXp [T*k,H] at its
+    sorted rows, plus dX_add [T,H] (another path's gradient). `n_rows` as for
+    combine_backward. See moe_permute_backward."""
+    M, H = dXp.shape
+    if k < 1 or M % k:
+        raise ValueError("dXp must hold T*k rows")
+    T = M // k
+    dev = dXp.device
+    dt = act_dtype(dXp)
+    gp = _want(dXp, "dXp", (M, H), dXp.dtype)
+    ap = _want(assign_row, "assign_row", (M,), torch.int32, dev)
+    ep = None if dX_add is None else _want(dX_add, "dX_add", (T, H), dXp.dtype, dev)
+    np_ = None if n_rows is None else _want(n_rows, "n_rows", (1,), torch.int32, dev)
+    dX, xp = _new((T, H), dXp.dtype, dev)
+    _call("moe_permute_backward", dev, gp, ap, np_, T, k, H, dt, ep, xp)
+    return dX
+
+
+# ---------------------------------------------------------------------------
+# MXFP4: quantisation of rows and weights, and reading them back
+# ---------------------------------------------------------------------------
+def quantize_mxfp4_rows(X):
+    """E2M1 codes Q [R,C/2] and E8M0 scale bytes S [R,C/32] (uint8) of the bf16 or
+    f32 rows X [R,C] (rows may be strided). See moe_quantize_mxfp4_rows."""
+    R, C = X.shape
+    dev = X.device
+    if not X.is_cuda or (C > 1 and X.stride(1) != 1):
+        raise ValueError("X must be a device tensor with contiguous rows")
+    ldx = X.stride(0) if R > 1 else C
+    Q, qp = _new((R, C // 2), torch.uint8, dev)
+    S, sp = _new((R, C // 32), torch.uint8, dev)
+    _call("moe_quantize_mxfp4_rows", dev, X.data_ptr(), act_dtype(X), ldx, R, C, qp, sp)
+    return Q, S
+
+
+def dequantize_mxfp4_rows(Q, S, dtype=torch.bfloat16):
+    """The values [R,C] that quantize_mxfp4_rows' codes and scales stand for, in
+    bfloat16 or float32 (exact in both)."""
+    R, C = Q.shape[0], 2 * Q.shape[1]
+    dev = Q.device
+    qp = _want(Q, "Q", (R, C // 2), torch.uint8)
+    sp = _want(S, "S", (R, C // 32), torch.uint8, dev)
+    Y, yp = _new((R, C), dtype, dev)
+    _call("moe_dequantize_mxfp4_rows", dev, qp, sp, R, C, act_dtype(Y), yp)
+    return Y
+
+
+def quantize_mxfp4_weights(W):
+    """MXFP4 codes Q [G,K/2,N] and scales S [G,K/32,N] (uint8) of the bf16 or f32
+    matrices W [G,K,N], as a layer's W1, W3, W2 and S1, S3, S2 take them (W [K,N]:
+    Q [K/2,N], S [K/32,N], as its shared expert does). See
+    moe_quantize_mxfp4_weights."""
+    if W.dim() not in (2, 3):
+        raise ValueError("W must be [G,K,N] or [K,N]")
+    *lead, K, N = W.shape
+    dev = W.device
+    wp = _want(W, "W", W.shape, W.dtype)
+    Q, qp = _new((*lead, K // 2, N), torch.uint8, dev)
+    S, sp = _new((*lead, K // 32, N), torch.uint8, dev)
+    _call("moe_quantize_mxfp4_weights", dev, wp, act_dtype(W), lead[0] if lead else 1, K, N, qp, sp)
+    return Q, S
+
+
+def dequantize_mxfp4_weights(Q, S, dtype=torch.bfloat16):
+    """The matrices [G,K,N] (or [K,N]) that MXFP4 codes and scales stand for, in
+    bfloat16 or float32 (exact in both)."""
+    if Q.dim() not in (2, 3):
+        raise ValueError("Q must be [G,K/2,N] or [K/2,N]")
+    *lead, K2, N = Q.shape
+    dev = Q.device
+    qp = _want(Q, "Q", Q.shape, torch.uint8)
+    sp = _want(S, "S", (*lead, 2 * K2 // 32, N), torch.uint8, dev)
+    W, wp = _new((*lead, 2 * K2, N), dtype, dev)
+    _call("moe_dequantize_mxfp4_weights", dev, qp, sp, lead[0] if lead else 1, 2 * K2, N, act_dtype(W), wp)
+    return W
 
 
 # ---------------------------------------------------------------------------

@@ -5,6 +5,7 @@
 
 #include "abi_util.h"
 #include "common.h"
+#include "mx4.h"
 #include "train.h"
 
 using namespace moe;
@@ -44,6 +45,7 @@ moe_status check_ffn_dims(int H, int F, moe_dtype w_dt) {
 struct FfnPlan {
     bool tiled;
     bool a8;      // tiled with E4M3 activations (W8A8)
+    bool a4;      // tiled with MXFP4 rows (W4A4)
     bool tail;    // tiled with the tail split (bf16 and MXFP4 weights)
     int bm;
     int ksplit1;  // split-K of gate/up (row-streaming path; 1: none)
@@ -53,7 +55,8 @@ struct FfnPlan {
 };
 
 bool path_ok(moe_ffn_path path) {
-    return path == MOE_PATH_AUTO || path == MOE_PATH_GEMV || path == MOE_PATH_TILED || path == MOE_PATH_TILED_A8;
+    return path == MOE_PATH_AUTO || path == MOE_PATH_GEMV || path == MOE_PATH_TILED || path == MOE_PATH_TILED_A8 ||
+           path == MOE_PATH_TILED_A4;
 }
 
 // a8_ok: the caller can run the W8A8 form (AUTO picks it for FP8 weights
@@ -65,6 +68,8 @@ FfnPlan plan_ffn(int M, int G, int H, int F, moe_dtype w_dt, moe_ffn_path path, 
     const bool can_a8 = a8_ok && w_dt == MOE_FP8_E4M3 && tiled_a8_supports(F, H) && tiled_a8_supports(H, F);
     if (path == MOE_PATH_TILED_A8) {
         p.tiled = p.a8 = can_a8;
+    } else if (path == MOE_PATH_TILED_A4) {
+        p.tiled = p.a4 = w_dt == MOE_MXFP4;
     } else if (path == MOE_PATH_TILED) {
         p.tiled = can_tile;
     } else if (path == MOE_PATH_GEMV) {
@@ -78,8 +83,8 @@ FfnPlan plan_ffn(int M, int G, int H, int F, moe_dtype w_dt, moe_ffn_path path, 
         p.tiled = can_tile && (long long)M >= min_rows * G;
         p.a8 = p.tiled && can_a8;
     }
-    p.bm = p.a8 ? tiled_a8_bm(M, G) : p.tiled ? tiled_gemm_bm(wt, M, G) : kGemvBM;
-    p.tail = p.tiled && !p.a8 && (w_dt == MOE_BF16 || w_dt == MOE_MXFP4);
+    p.bm = p.a4 ? tiled_a4_bm(M, G) : p.a8 ? tiled_a8_bm(M, G) : p.tiled ? tiled_gemm_bm(wt, M, G) : kGemvBM;
+    p.tail = p.tiled && !p.a8 && !p.a4 && (w_dt == MOE_BF16 || w_dt == MOE_MXFP4);
     p.ksplit1 = 1;
     p.kchunk1 = H;
     p.ksplit2 = 1;
@@ -120,6 +125,9 @@ struct FfnWs {
     float *part1;  // gate/up split-K partials [ksplit1][rows][2 hw] (g then u), or null
     uint8_t *xq, *hq;  // W8A8: E4M3 codes of the expert inputs [xrows][H] and of h [rows][hw]
     float *xs, *hs;    // and their per-row 128-column scales
+    uint8_t *x4, *h4;  // W4A4: panels of the expert inputs and of h, and their scale words
+    uint32_t *x4s, *h4s;
+    long long ld4;     // rows of a panel
     float *tail_part;  // tail split: partial sums and counters (or null)
     int32_t *tail_cnt;
 };
@@ -132,14 +140,15 @@ struct ExtraGroup {
     const float *S1 = nullptr, *S3 = nullptr, *S2 = nullptr;
 };
 
-// xrows: rows of quantised expert input (W8A8 only).
+// xrows: rows of quantised expert input (W8A8 only). W4A4: the rows of the
+// grouped launches are the first a4_rows; bf16 h is kept for the others only.
 size_t ffn_ws_carve(Carver &c, FfnWs &w, const FfnPlan &p, int rows, int groups, int H, int hw,
-                    moe_dtype act_dt, int xrows) {
+                    moe_dtype act_dt, int xrows, int a4_rows) {
     const long long max_tiles = max_tiles_for(rows, groups, p.bm);
     w.tiles = static_cast<int32_t *>(c.take(sizeof(int32_t) * 4 * max_tiles));
     w.n_tiles = static_cast<int32_t *>(c.take(sizeof(int32_t)));
     w.group_tile_start = static_cast<int32_t *>(c.take(sizeof(int32_t) * (groups + 1)));
-    w.h = c.take(dt_size(act_dt) * (size_t)rows * hw);
+    w.h = c.take(dt_size(act_dt) * (size_t)(p.a4 ? rows - a4_rows : rows) * hw);
     w.part = p.tiled ? c.take(dt_size(act_dt) * (size_t)rows * H)
                      : c.take(sizeof(float) * (size_t)p.ksplit2 * rows * H);
     w.part1 = p.ksplit1 > 1 ? static_cast<float *>(c.take(sizeof(float) * (size_t)p.ksplit1 * rows * 2 * hw))
@@ -150,6 +159,15 @@ size_t ffn_ws_carve(Carver &c, FfnWs &w, const FfnPlan &p, int rows, int groups,
         w.xs = static_cast<float *>(c.take(sizeof(float) * (size_t)rows * (H / 128)));
         w.hq = static_cast<uint8_t *>(c.take((size_t)rows * hw));
         w.hs = static_cast<float *>(c.take(sizeof(float) * (size_t)rows * (hw / 128)));
+    }
+    if (p.a4) {
+        // a tile reads whole, so its last rows may lie past the last panel row in use
+        w.ld4 = a4_rows + 256LL;
+        const size_t px = (size_t)w.ld4 * mx4::panels(H), ph = (size_t)w.ld4 * mx4::panels(hw);
+        w.x4 = static_cast<uint8_t *>(c.take(64 * px));
+        w.x4s = static_cast<uint32_t *>(c.take(4 * px));
+        w.h4 = static_cast<uint8_t *>(c.take(64 * ph));
+        w.h4s = static_cast<uint32_t *>(c.take(4 * ph));
     }
     if (p.tail) {
         w.tail_part = static_cast<float *>(c.take(tiled_tail_bytes(p.bm)));
@@ -249,6 +267,7 @@ void mxfp4_strides(GemmProblem &g) {
 
 hipError_t run_gemm(const FfnPlan &p, GemmProblem g, WType wt, bool swiglu, bool out_bf16, hipStream_t s) {
     if (wt == W_MXFP4) mxfp4_strides(g);
+    if (p.a4) return launch_tiled_a4(g, swiglu, p.bm, s);
     if (p.a8) return out_bf16 ? launch_tiled_a8(g, swiglu, p.bm, s) : hipErrorInvalidValue;
     return p.tiled ? launch_tiled_gemm(g, wt, swiglu, out_bf16, p.bm, s)
                    : launch_stream_gemm(g, wt, swiglu, out_bf16, s);
@@ -281,6 +300,19 @@ void set_a8(GemmProblem &g, const uint8_t *q, const float *sc, int width, int ro
     g.as_ld = rows;
 }
 
+// W4A4 operands: the rows' panels and scale words
+void set_a4(GemmProblem &g, const uint8_t *q, const uint32_t *sc, long long ld) {
+    g.A = q;
+    g.As = reinterpret_cast<const float *>(sc);
+    g.as_ld = ld;
+}
+// and where gate/up leaves h
+void set_h4(GemmProblem &g, const FfnWs &w) {
+    g.Cq = w.h4;
+    g.Cqs = reinterpret_cast<float *>(w.h4s);
+    g.cqs_ld = w.ld4;
+}
+
 }  // namespace
 
 extern "C" {
@@ -290,7 +322,7 @@ unsigned moe_debug_bounds(void) {
     if (hipDeviceSynchronize() != hipSuccess) return ~0u;
     return bounds_take_tiled128() | bounds_take_tiled256() | bounds_take_tiledf32() | bounds_take_a8() |
            bounds_take_stream() | bounds_take_permute() | bounds_take_combine() | bounds_take_quant() |
-           bounds_take_ep() | bounds_take_persist() | bounds_take_train_rows() | bounds_take_train_weights();
+           bounds_take_ep() | bounds_take_persist() | bounds_take_a4() | bounds_take_train_rows() | bounds_take_train_weights();
 #else
     return 0u;
 #endif
@@ -452,11 +484,12 @@ size_t moe_grouped_ffn_workspace_bytes(int M, int G, int H, int F, moe_dtype act
     const FfnPlan p = plan_ffn(M, G, H, F, w_dt, path);
     Carver c(nullptr);
     FfnWs w{};
-    size_t bytes = ffn_ws_carve(c, w, p, M, G, H, F, act_dt, M);
+    size_t bytes = ffn_ws_carve(c, w, p, M, G, H, F, act_dt, M, M);
+    if (p.a4) return bytes;
     FfnPlan q = p;  // the fp32 partials of the row-streaming form can be larger
     q.tiled = q.a8 = false;
     Carver c2(nullptr);
-    const size_t b2 = ffn_ws_carve(c2, w, q, M, G, H, F, act_dt, M);
+    const size_t b2 = ffn_ws_carve(c2, w, q, M, G, H, F, act_dt, M, M);
     return bytes > b2 ? bytes : b2;
 }
 
@@ -471,6 +504,7 @@ moe_status moe_grouped_ffn(const void *Xin, const int32_t *row_src, int k, int M
     if (st != MOE_OK) return st;
     if (!path_ok(path)) return MOE_ERR_INVALID_ARG;
     if (path == MOE_PATH_TILED_A8 && w_dt != MOE_FP8_E4M3) return MOE_ERR_UNSUPPORTED;
+    if (path == MOE_PATH_TILED_A4 && w_dt != MOE_MXFP4) return MOE_ERR_UNSUPPORTED;
     if (M == 0) return MOE_OK;
     if (!Xin || !offsets || !W1 || !W3 || !W2 || !Yp) return MOE_ERR_INVALID_ARG;
     const bool sc = scaled(w_dt);
@@ -482,12 +516,25 @@ moe_status moe_grouped_ffn(const void *Xin, const int32_t *row_src, int k, int M
         return MOE_ERR_WORKSPACE_TOO_SMALL;
     Carver c(ws);
     FfnWs w{};
-    ffn_ws_carve(c, w, p, M, G, H, F, act_dt, M);
+    ffn_ws_carve(c, w, p, M, G, H, F, act_dt, M, M);
     const WType wt = wtype(w_dt);
     const bool bf = act_dt == MOE_BF16;
     const int max_tiles = (int)max_tiles_for(M, G, p.bm);
     const ExtraGroup none{};
 
+    if (p.a4) {
+        // MXFP4 rows (gathered here) and the tile list, gate/up writing MXFP4 h, down
+        const TilesJob tiles{offsets, G, p.bm, w.tiles, w.n_tiles, w.group_tile_start, nullptr, 0};
+        MOE_TRY(launch_mx4_panels({Xin, row_src, k, H, M, 0, offsets + G, w.x4, w.x4s, w.ld4}, &tiles, stream));
+        GemmProblem g1 = gate_up_problem(nullptr, nullptr, 1, &w, G, max_tiles, M, H, F, W1, W3, S1, S3, none, M,
+                                         nullptr);
+        set_a4(g1, w.x4, w.x4s, w.ld4);
+        set_h4(g1, w);
+        MOE_TRY(run_gemm(p, g1, wt, true, true, stream));
+        GemmProblem g2 = down_problem(nullptr, &w, G, max_tiles, M, H, F, W2, S2, none, M, Yp, 0, 1, F);
+        set_a4(g2, w.h4, w.h4s, w.ld4);
+        return hip_status(run_gemm(p, g2, wt, false, true, stream));
+    }
     MOE_TRY(launch_build_tiles(offsets, G, 0, p.bm, w.tiles, w.n_tiles, w.group_tile_start, stream, w.tail_cnt,
                                w.tail_cnt ? tiled_tail_counters : 0));
     if (p.a8) {
@@ -566,6 +613,10 @@ moe_status check_desc(const moe_layer_desc *d) {
     if (d->path == MOE_PATH_TILED_A8 &&
         (d->w_dt != MOE_FP8_E4M3 || (d->Fs > 0 && d->ws_dt == MOE_FP8_E4M3 && d->Fs != d->F)))
         return MOE_ERR_UNSUPPORTED;
+    // and so does W4A4 an MXFP4 one
+    if (d->path == MOE_PATH_TILED_A4 &&
+        (d->w_dt != MOE_MXFP4 || (d->Fs > 0 && d->ws_dt == MOE_MXFP4 && d->Fs != d->F)))
+        return MOE_ERR_UNSUPPORTED;
     if (!d->Wg || !d->W1 || !d->W3 || !d->W2) return MOE_ERR_INVALID_ARG;
     const bool sc = scaled(d->w_dt);
     if (sc != (d->S1 != nullptr) || sc != (d->S3 != nullptr) || sc != (d->S2 != nullptr))
@@ -625,7 +676,7 @@ ForwardWs carve_forward(const moe_layer_desc *d, int T, void *base) {
     FfnPlan carve = f.plan;
     const bool separate = d->Fs > 0 && !f.combined;
     if (separate && !f.plan.tiled && f.plan_s.ksplit2 > carve.ksplit2) carve.ksplit2 = f.plan_s.ksplit2;
-    ffn_ws_carve(c, f.ffn, carve, rows, groups, d->H, hw, d->act_dt, T);
+    ffn_ws_carve(c, f.ffn, carve, rows, groups, d->H, hw, d->act_dt, T, A + (f.combined ? T : 0));
     f.part1_s = nullptr;
     if (separate && !f.plan_s.tiled && f.plan_s.ksplit1 > 1)
         f.part1_s = static_cast<float *>(c.take(sizeof(float) * (size_t)f.plan_s.ksplit1 * T * 2 * d->Fs));
@@ -722,6 +773,9 @@ moe_status moe_forward(const moe_layer_desc *d, const void *X, int T, void *Y, v
         sl.extra0 = ex.rows > 0 ? A : -1;
         MOE_TRY(launch_quant_rows(X, H, nullptr, 1, T, H, f.ffn.xq, f.ffn.xs, stream, &sl));
     }
+    if (p.a4)
+        MOE_TRY(launch_mx4_panels({X, f.row_src, d->k, H, A, ex.rows, f.offsets + E, f.ffn.x4, f.ffn.x4s, f.ffn.ld4},
+                                  nullptr, stream));
     MOE_TRY(mark(MOE_EV_SCHEDULE));
     GemmProblem g1 = gate_up_problem(X, f.row_src, d->k, &f.ffn, E, max_tiles, M, H, F, W1, W3, S1, S3, ex, A,
                                      f.ffn.h);
@@ -732,10 +786,14 @@ moe_status moe_forward(const moe_layer_desc *d, const void *X, int T, void *Y, v
         g1.Cqs = f.ffn.hs;
         g1.cqs_ld = M;
     }
+    if (p.a4) {
+        set_a4(g1, f.ffn.x4, f.ffn.x4s, f.ffn.ld4);
+        set_h4(g1, f.ffn);
+    }
     if (p.tiled) MOE_TRY(run_gemm(p, g1, wt, true, bf, stream));
     else MOE_TRY(run_gate_up_rows(p, g1, f.ffn, M, F, wt, d->act_dt, stream));
     MOE_TRY(mark(MOE_EV_GATE_UP));
-    void *h_s = static_cast<char *>(f.ffn.h) + hb * (size_t)A * hw;
+    void *h_s = static_cast<char *>(f.ffn.h) + (p.a4 ? 0 : hb * (size_t)A * hw);
     const ExtraGroup none{};
     if (d->Fs > 0 && !f.combined) {
         GemmProblem gs = gate_up_problem(X, nullptr, 1, nullptr, 1, 0, T, H, d->Fs, Ws1, Ws3, Ss1, Ss3, none, 0,
@@ -758,6 +816,7 @@ moe_status moe_forward(const moe_layer_desc *d, const void *X, int T, void *Y, v
         GemmProblem g2 = down_problem(f.ffn.h, &f.ffn, E, max_tiles, M, H, F, W2, S2, ex, A, f.ffn.part, 0, 1,
                                       F);
         if (p.a8) set_a8(g2, f.ffn.hq, f.ffn.hs, F, M);
+        if (p.a4) set_a4(g2, f.ffn.h4, f.ffn.h4s, f.ffn.ld4);
         MOE_TRY(run_gemm(p, g2, wt, false, bf, stream));
         MOE_TRY(mark(MOE_EV_DOWN));
         void *Sp = static_cast<char *>(f.ffn.part) + hb * (size_t)A * H;

@@ -1,0 +1,324 @@
+// MXFP4 quantisation of rows and of weight matrices, and reading them back
+// (format: mx4.h).
+//
+// HBM-bound: 2 (fp32: 4) bytes a value in, 17/32 out, and the reverse.
+#include "mx4.h"
+#include "schedule.h"
+#include "train.h"
+
+namespace moe {
+
+MOE_BOUNDS_FILE(mx4)
+namespace {
+
+using namespace mx4;
+
+constexpr long long kMaxThreads = 0xffffffffLL;  // of a launch (beyond, it takes their number mod 2^32)
+constexpr int kPer = 16;                         // values per thread of the row kernels
+
+// ---- rows: a thread owns 16 consecutive values; the two threads of a group
+// exchange their maxima, and one of them stores the scale byte ----
+template <bool F32>
+__global__ __launch_bounds__(256) void mx4_rows_kernel(const void *X, long long ldx, long long n, int C, uint8_t *Q,
+                                                       uint8_t *S) {
+    const long long t = (long long)blockIdx.x * 256 + threadIdx.x, i = t * kPer;
+    // C is a multiple of 32: both threads of a group are in or out together
+    if (i >= n) return;
+    long long o = i;
+    if (ldx != C) {
+        const long long row = i / C;
+        o = row * ldx + (i - row * C);
+    }
+    float v[2][8];
+    load8<F32>(X, o, v[0]);
+    load8<F32>(X, o + 8, v[1]);
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, max(mag_bits(v[0][j]), mag_bits(v[1][j])));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 1));
+    const uint32_t b = scale_byte(m);
+    *reinterpret_cast<u32x2 *>(Q + i / 2) = u32x2{codes8(v[0], b), codes8(v[1], b)};
+    if ((t & 1) == 0) S[i / kGroup] = (uint8_t)b;
+}
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// the eight values of a code word, times the scale
+__device__ __forceinline__ void values8(uint32_t w, float s, float (&v)[8]) {
+    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 0);
+    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 1);
+    const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 2);
+    const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 3);
+    v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1], v[4] = c[0], v[5] = c[1], v[6] = d[0], v[7] = d[1];
+}
+// the NaN scale of a group, applied by the caller (the conversions read
+// exponent 255 as a power of two)
+__device__ __forceinline__ float nan_if(uint32_t byte, float x) {
+    return byte == 255u ? __uint_as_float(0x7fc00000u) : x;
+}
+
+template <bool F32>
+__device__ __forceinline__ void store8(void *Y, long long o, const float (&v)[8]) {
+    if constexpr (F32) {
+        f32x4 *p = reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(Y) + o);
+        p[0] = f32x4{v[0], v[1], v[2], v[3]};
+        p[1] = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+        *reinterpret_cast<u32x4 *>(reinterpret_cast<uint16_t *>(Y) + o) =
+            u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    }
+}
+
+template <bool F32>
+__global__ __launch_bounds__(256) void mx4_rows_back_kernel(const uint8_t *Q, const uint8_t *S, long long n, void *Y) {
+    const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * kPer;
+    if (i >= n) return;
+    const u32x2 q = *reinterpret_cast<const u32x2 *>(Q + i / 2);
+    const uint32_t b = S[i / kGroup];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float v[8];
+        values8(q[h], scale_of(b), v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = nan_if(b, v[j]);
+        store8<F32>(Y, i + 8 * h, v);
+    }
+}
+
+// ---- weights [G][K][N]: a thread owns 8 columns of one group of 32 K rows
+// (a wavefront's rows are contiguous: 1 KB of bf16, 512 bytes of codes), its
+// values kept in registers between the maximum and the codes ----
+template <bool F32>
+__global__ __launch_bounds__(256) void mx4_weights_kernel(const void *W, long long threads, int N, uint8_t *Q,
+                                                          uint8_t *S) {
+    const long long t = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (t >= threads) return;
+    const int per = N / 8;
+    const long long g = t / per;  // group of 32 rows, over all matrices (K is a multiple of 32)
+    const int c = (int)(t - g * per) * 8;
+    float v[32][8];
+#pragma unroll
+    for (int r = 0; r < 32; ++r) load8<F32>(W, (32 * g + r) * N + c, v[r]);
+    uint32_t b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int r = 0; r < 32; ++r) m = max(m, mag_bits(v[r][j]));
+        b[j] = scale_byte(m);
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        uint32_t q[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t w = (uint32_t)__builtin_amdgcn_cvt_scalef32_pk_fp4_f32(
+                0u, v[2 * r][j], v[2 * r + 1][j], scale_of(b[j] == 255u ? 127u : b[j]), 0);
+            q[j] = b[j] == 255u ? 0u : w & 255u;
+        }
+        *reinterpret_cast<u32x2 *>(Q + (16 * g + r) * N + c) =
+            u32x2{q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24, q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24};
+    }
+    *reinterpret_cast<u32x2 *>(S + g * N + c) =
+        u32x2{b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24};
+}
+
+template <bool F32>
+__global__ __launch_bounds__(256) void mx4_weights_back_kernel(const uint8_t *Q, const uint8_t *S, long long threads,
+                                                               int N, void *W) {
+    const long long t = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (t >= threads) return;
+    const int per = N / 8;
+    const long long g = t / per;
+    const int c = (int)(t - g * per) * 8;
+    u32x2 q[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) q[r] = *reinterpret_cast<const u32x2 *>(Q + (16 * g + r) * N + c);
+    const u32x2 sw = *reinterpret_cast<const u32x2 *>(S + g * N + c);
+    uint32_t b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) b[j] = sw[j >> 2] >> (8 * (j & 3)) & 255u;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        float lo[8], hi[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const f32x2 x = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[r][j >> 2] >> (8 * (j & 3)), scale_of(b[j]), 0);
+            lo[j] = nan_if(b[j], x[0]);
+            hi[j] = nan_if(b[j], x[1]);
+        }
+        store8<F32>(W, (32 * g + 2 * r) * N + c, lo);
+        store8<F32>(W, (32 * g + 2 * r + 1) * N + c, hi);
+    }
+}
+
+// ---- rows in the product's layout: 16 lanes a row and panel (8 values each,
+// four lanes a group), 64 rows a workgroup ----
+constexpr int kPanelRows = 64;
+template <int P, bool TILES>
+__global__ __launch_bounds__(1024) void mx4_panels_kernel(Mx4Panels p, TilesJob j) {
+    __shared__ int scan_lds[16];
+    int blk = blockIdx.x;
+    if (TILES) {
+        if (blk == 0) {
+            if (blockIdx.y == 0)
+                build_tiles(j.offsets, j.G, 0, j.bm, j.tiles, j.n_tiles, j.start, j.zero, j.n_zero, scan_lds);
+            return;
+        }
+        --blk;
+    }
+    const int sub = threadIdx.x & 15;
+    const int r = blk * kPanelRows + (threadIdx.x >> 4);
+    const int used = p.n_rows ? min(p.rows, *p.n_rows) : p.rows;
+    if (r >= p.rows + p.extra || (r >= used && r < p.rows)) return;  // a row's 16 lanes together
+    const long long src = r >= p.rows ? r - p.rows : p.row_src ? p.row_src[r] / p.gk : r;
+    const int np = panels(p.C), kb0 = blockIdx.y * P;
+    const uint16_t *x = reinterpret_cast<const uint16_t *>(p.X) + src * p.C;
+    float v[P][8];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const int c = 128 * (kb0 + i) + 8 * sub;
+        if (c < p.C) load8<false>(x, c, v[i]);
+        else
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[i][q] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const int kb = kb0 + i;
+        if (kb >= np) return;
+        uint32_t m = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) m = max(m, mag_bits(v[i][q]));
+        m = max(m, (uint32_t)__shfl_xor((int)m, 1));
+        m = max(m, (uint32_t)__shfl_xor((int)m, 2));
+        const uint32_t b = scale_byte(m);
+        uint32_t w = b << (8 * (sub >> 2));
+        w |= (uint32_t)__shfl_xor((int)w, 4);
+        w |= (uint32_t)__shfl_xor((int)w, 8);
+        const long long o = kb * p.ld + r;
+        *reinterpret_cast<uint32_t *>(p.A + o * 64 + 4 * sub) = codes8(v[i], b);
+        if (sub == 0) p.As[o] = w;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_mx4_panels(const Mx4Panels &p, const TilesJob *tiles, hipStream_t s) {
+    if (p.rows < 0 || p.extra < 0 || p.C < kGroup || p.C % kGroup || p.gk < 1 || !p.A || !p.As ||
+        p.ld < (long long)p.rows + p.extra)
+        return hipErrorInvalidValue;
+    const long long rows = (long long)p.rows + p.extra, groups = (rows + kPanelRows - 1) / kPanelRows;
+    const int np = panels(p.C);
+    const long long bx = groups + (tiles ? 1 : 0);
+    if (bx == 0) return hipSuccess;
+    const bool one = groups * np < 1024;  // few rows: a panel a workgroup
+    const int py = one ? np : (np + 3) / 4;
+    if (bx > kMaxThreads / 1024 || py > 65535) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)bx, (unsigned)py), block(1024);
+    const TilesJob none{};
+    if (tiles) {
+        if (one) hipLaunchKernelGGL((mx4_panels_kernel<1, true>), grid, block, 0, s, p, *tiles);
+        else hipLaunchKernelGGL((mx4_panels_kernel<4, true>), grid, block, 0, s, p, *tiles);
+    } else {
+        if (one) hipLaunchKernelGGL((mx4_panels_kernel<1, false>), grid, block, 0, s, p, none);
+        else hipLaunchKernelGGL((mx4_panels_kernel<4, false>), grid, block, 0, s, p, none);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace moe
+
+// ---------------------------------------------------------------------------
+// public entry points
+// ---------------------------------------------------------------------------
+#include "abi_util.h"
+
+using namespace moe;
+
+namespace {
+
+// values of one call: a launch of 256 threads per 4096 (rows) or 65536 values,
+// and a grid's dimension holds fewer than 2^32 threads
+constexpr long long kMaxValues = (1LL << 36) - 4096;
+
+bool off16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+bool off8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7) != 0; }
+
+moe_status check_rows(long long R, int C, moe_dtype dt) {
+    if (R < 0 || C < 1) return MOE_ERR_INVALID_ARG;
+    if ((dt != MOE_F32 && dt != MOE_BF16) || C % 32 || C > kMaxDim || R > kMaxValues / C) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+moe_status check_weights(int G, int K, int N, moe_dtype dt) {
+    if (G < 0 || K < 1 || N < 1) return MOE_ERR_INVALID_ARG;
+    if ((dt != MOE_F32 && dt != MOE_BF16) || K % 32 || N % 8 || K > kMaxDim || N > kMaxDim ||
+        G > kMaxValues / ((long long)K * N))
+        return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_quantize_mxfp4_rows(const void *X, moe_dtype x_dt, long long ldx, long long R, int C, uint8_t *Q,
+                                   uint8_t *S, hipStream_t stream) {
+    const moe_status st = check_rows(R, C, x_dt);
+    if (st != MOE_OK) return st;
+    if (ldx < C) return MOE_ERR_INVALID_ARG;
+    if (ldx % (x_dt == MOE_F32 ? 4 : 8)) return MOE_ERR_UNSUPPORTED;
+    if (R == 0) return MOE_OK;
+    if (!X || !Q || !S) return MOE_ERR_INVALID_ARG;
+    if (off16(X) || off8(Q)) return MOE_ERR_UNSUPPORTED;
+    const long long n = R * C;
+    const dim3 grid((unsigned)((n / kPer + 255) / 256));
+    if (x_dt == MOE_F32) hipLaunchKernelGGL(mx4_rows_kernel<true>, grid, dim3(256), 0, stream, X, ldx, n, C, Q, S);
+    else hipLaunchKernelGGL(mx4_rows_kernel<false>, grid, dim3(256), 0, stream, X, ldx, n, C, Q, S);
+    return hip_status(hipGetLastError());
+}
+
+moe_status moe_dequantize_mxfp4_rows(const uint8_t *Q, const uint8_t *S, long long R, int C, moe_dtype y_dt, void *Y,
+                                     hipStream_t stream) {
+    const moe_status st = check_rows(R, C, y_dt);
+    if (st != MOE_OK) return st;
+    if (R == 0) return MOE_OK;
+    if (!Q || !S || !Y) return MOE_ERR_INVALID_ARG;
+    if (off8(Q) || off16(Y)) return MOE_ERR_UNSUPPORTED;
+    const long long n = R * C;
+    const dim3 grid((unsigned)((n / kPer + 255) / 256));
+    if (y_dt == MOE_F32) hipLaunchKernelGGL(mx4_rows_back_kernel<true>, grid, dim3(256), 0, stream, Q, S, n, Y);
+    else hipLaunchKernelGGL(mx4_rows_back_kernel<false>, grid, dim3(256), 0, stream, Q, S, n, Y);
+    return hip_status(hipGetLastError());
+}
+
+moe_status moe_quantize_mxfp4_weights(const void *W, moe_dtype w_dt, int G, int K, int N, uint8_t *Q, uint8_t *S,
+                                      hipStream_t stream) {
+    const moe_status st = check_weights(G, K, N, w_dt);
+    if (st != MOE_OK) return st;
+    if (G == 0) return MOE_OK;
+    if (!W || !Q || !S) return MOE_ERR_INVALID_ARG;
+    if (off16(W) || off8(Q) || off8(S)) return MOE_ERR_UNSUPPORTED;
+    const long long threads = (long long)G * (K / 32) * (N / 8);
+    const dim3 grid((unsigned)((threads + 255) / 256));
+    if (w_dt == MOE_F32) hipLaunchKernelGGL(mx4_weights_kernel<true>, grid, dim3(256), 0, stream, W, threads, N, Q, S);
+    else hipLaunchKernelGGL(mx4_weights_kernel<false>, grid, dim3(256), 0, stream, W, threads, N, Q, S);
+    return hip_status(hipGetLastError());
+}
+
+moe_status moe_dequantize_mxfp4_weights(const uint8_t *Q, const uint8_t *S, int G, int K, int N, moe_dtype w_dt,
+                                        void *W, hipStream_t stream) {
+    const moe_status st = check_weights(G, K, N, w_dt);
+    if (st != MOE_OK) return st;
+    if (G == 0) return MOE_OK;
+    if (!Q || !S || !W) return MOE_ERR_INVALID_ARG;
+    if (off8(Q) || off8(S) || off16(W)) return MOE_ERR_UNSUPPORTED;
+    const long long threads = (long long)G * (K / 32) * (N / 8);
+    const dim3 grid((unsigned)((threads + 255) / 256));
+    if (w_dt == MOE_F32)
+        hipLaunchKernelGGL(mx4_weights_back_kernel<true>, grid, dim3(256), 0, stream, Q, S, threads, N, W);
+    else hipLaunchKernelGGL(mx4_weights_back_kernel<false>, grid, dim3(256), 0, stream, Q, S, threads, N, W);
+    return hip_status(hipGetLastError());
+}
+
+}  // extern "C"

@@ -125,4 +125,29 @@ struct GatherProblem {
 };
 hipError_t launch_gather_grads(const GatherProblem &p, hipStream_t s);
 
+// Gradients of the sorted rows and of the weighted sum back (dispatch_grad.hip),
+// for rows of dt (MOE_F32, MOE_BF16). n_rows: device, NULL for T * k.
+struct CombineBack {
+    const void *dY, *Yp;        // [T][H], [M][H]
+    const int32_t *assign_row;  // [T * k]
+    const float *w;             // [T][k]
+    const int32_t *n_rows;
+    int T, k, H;
+    void *dYp;                  // [M][H] or NULL
+    float *dw;                  // [T][k] or NULL
+};
+struct PermuteBack {
+    const void *dXp;            // [M][H]
+    const int32_t *assign_row, *n_rows;
+    const void *add;            // [T][H] or NULL
+    int T, k, H;
+    void *dX;                   // [T][H]
+};
+// fewer than 2^32 threads a launch: a workgroup of up to 256 a token, a thread
+// for 4 values at least
+constexpr int kCombineBackTokens = (1 << 24) - 1;
+constexpr long long kPermuteBackValues = (1LL << 34) - 1024;
+hipError_t launch_combine_back(const CombineBack &p, moe_dtype dt, hipStream_t s);
+hipError_t launch_permute_back(const PermuteBack &p, moe_dtype dt, hipStream_t s);
+
 }  // namespace moe

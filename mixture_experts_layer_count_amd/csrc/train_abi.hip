@@ -392,4 +392,43 @@ moe_status moe_ffn_train_backward(const void *dY, const float *topk_w, const int
     return hip_status(launch_weights_gemm(q, q2, stream));
 }
 
+// ---------------------------------------------------------------------------
+namespace {
+
+moe_status check_dispatch(int T, int k, int H, moe_dtype dt) {
+    if (T < 0 || k < 1 || H < 1) return MOE_ERR_INVALID_ARG;
+    if ((dt != MOE_F32 && dt != MOE_BF16) || H % 4 || H > kMaxDim || k > 64) return MOE_ERR_UNSUPPORTED;
+    if ((long long)T * k > 0x7fffffffLL || T > kCombineBackTokens || (long long)T * H > kPermuteBackValues)
+        return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+// the boundary that rows of H values allow: 16 bytes, or 8 for bf16 of H % 8 = 4
+bool off_rows(const void *p, int H, moe_dtype dt) {
+    return (reinterpret_cast<uintptr_t>(p) & (dt == MOE_BF16 && H % 8 ? 7 : 15)) != 0;
+}
+
+}  // namespace
+
+moe_status moe_combine_backward(const void *dY, const void *Yp, const int32_t *assign_row, const float *topk_w,
+                                const int32_t *n_rows, int T, int k, int H, moe_dtype dt, void *dYp, float *dtopk_w,
+                                hipStream_t stream) {
+    const moe_status st = check_dispatch(T, k, H, dt);
+    if (st != MOE_OK) return st;
+    if (T == 0) return MOE_OK;
+    if (!dYp && !dtopk_w) return MOE_ERR_INVALID_ARG;
+    if (!dY || !assign_row || (dYp && !topk_w) || (dtopk_w && !Yp)) return MOE_ERR_INVALID_ARG;
+    if (off_rows(dY, H, dt) || off_rows(Yp, H, dt) || off_rows(dYp, H, dt)) return MOE_ERR_UNSUPPORTED;
+    return hip_status(launch_combine_back({dY, Yp, assign_row, topk_w, n_rows, T, k, H, dYp, dtopk_w}, dt, stream));
+}
+
+moe_status moe_permute_backward(const void *dXp, const int32_t *assign_row, const int32_t *n_rows, int T, int k, int H,
+                                moe_dtype dt, const void *dX_add, void *dX, hipStream_t stream) {
+    const moe_status st = check_dispatch(T, k, H, dt);
+    if (st != MOE_OK) return st;
+    if (T == 0) return MOE_OK;
+    if (!dXp || !assign_row || !dX) return MOE_ERR_INVALID_ARG;
+    if (off_rows(dXp, H, dt) || off_rows(dX_add, H, dt) || off_rows(dX, H, dt)) return MOE_ERR_UNSUPPORTED;
+    return hip_status(launch_permute_back({dXp, assign_row, n_rows, dX_add, T, k, H, dX}, dt, stream));
+}
+
 }  // extern "C"
