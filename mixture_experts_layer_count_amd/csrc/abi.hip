@@ -46,7 +46,7 @@ struct FfnPlan {
     bool tiled;
     bool a8;      // tiled with E4M3 activations (W8A8)
     bool a4;      // tiled with MXFP4 rows (W4A4)
-    bool tail;    // tiled with the tail split (bf16 and MXFP4 weights)
+    bool tail;    // tiled with the tail split (bf16 and MXFP4 weights; W4A4, gate/up too)
     int bm;
     int ksplit1;  // split-K of gate/up (row-streaming path; 1: none)
     int kchunk1;
@@ -84,7 +84,7 @@ FfnPlan plan_ffn(int M, int G, int H, int F, moe_dtype w_dt, moe_ffn_path path, 
         p.a8 = p.tiled && can_a8;
     }
     p.bm = p.a4 ? tiled_a4_bm(M, G) : p.a8 ? tiled_a8_bm(M, G) : p.tiled ? tiled_gemm_bm(wt, M, G) : kGemvBM;
-    p.tail = p.tiled && !p.a8 && !p.a4 && (w_dt == MOE_BF16 || w_dt == MOE_MXFP4);
+    p.tail = p.tiled && !p.a8 && (w_dt == MOE_BF16 || w_dt == MOE_MXFP4);
     p.ksplit1 = 1;
     p.kchunk1 = H;
     p.ksplit2 = 1;
@@ -311,6 +311,8 @@ void set_h4(GemmProblem &g, const FfnWs &w) {
     g.Cq = w.h4;
     g.Cqs = reinterpret_cast<float *>(w.h4s);
     g.cqs_ld = w.ld4;
+    g.tail_part = w.tail_part;
+    g.tail_cnt = w.tail_cnt;
 }
 
 }  // namespace
@@ -524,7 +526,7 @@ moe_status moe_grouped_ffn(const void *Xin, const int32_t *row_src, int k, int M
 
     if (p.a4) {
         // MXFP4 rows (gathered here) and the tile list, gate/up writing MXFP4 h, down
-        const TilesJob tiles{offsets, G, p.bm, w.tiles, w.n_tiles, w.group_tile_start, nullptr, 0};
+        const TilesJob tiles{offsets, G, p.bm, w.tiles, w.n_tiles, w.group_tile_start, w.tail_cnt, tiled_tail_counters};
         MOE_TRY(launch_mx4_panels({Xin, row_src, k, H, M, 0, offsets + G, w.x4, w.x4s, w.ld4}, &tiles, stream));
         GemmProblem g1 = gate_up_problem(nullptr, nullptr, 1, &w, G, max_tiles, M, H, F, W1, W3, S1, S3, none, M,
                                          nullptr);

@@ -47,12 +47,15 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
+#ifndef A4_WC
+#define A4_WC 4
+#endif
 constexpr int kA4BK = 128;    // K per step
 constexpr int kA4Items = 64;  // work items per workgroup at most (LDS table)
 
-template <int WR, int MI>
+template <int WR, int WC, int MI>
 struct RingA4 {
-    static constexpr int waves = 4 * WR;
+    static constexpr int waves = WC * WR;
     static constexpr int threads = 64 * waves;
     static constexpr int BM = 32 * MI * WR;
     static constexpr int a_bytes = BM * 64;
@@ -61,7 +64,7 @@ struct RingA4 {
     static constexpr int sb_bytes = 4 * 256;
     static constexpr int sb_at = a_bytes + b_bytes + sa_bytes;
     static constexpr int stage = sb_at + sb_bytes;
-    static constexpr int per_cu = WR == 1 ? 2 : 1;  // workgroups a CU
+    static constexpr int per_cu = 1;  // workgroups a CU
     static constexpr int budget = 160 * 1024 / per_cu - kA4Items * 16;
     static constexpr int S = budget / stage < 6 ? budget / stage : 6;
     static constexpr int a_chunks = a_bytes / 1024;  // 1 KB copies, 16 rows each
@@ -75,35 +78,67 @@ struct RingA4 {
     static_assert(S >= 3 && BM % 64 == 0 && (S - 2) * per_step < 64, "ring");
 };
 
+// Parts that each item of an XCD's last round is split into (1: none), when the
+// fullest XCDs, with `per` items, leave at least half of its workgroups idle
+// there; a part has at least kA4PartSteps steps.
+constexpr int kA4Parts = 4, kA4PartSteps = 4;
+__device__ __forceinline__ int tail_parts(int per, int slots, int nk) {
+    const int tail = per % slots;
+    if (tail == 0) return 1;
+    return max(min(min(kA4Parts, kBlocksPerXcd / tail), nk / kA4PartSteps), 1);
+}
+
+// What steers the K loop is kept in scalar registers: a count that went through a
+// vector load or a division leaves a loop of exec masks, 15 % slower
+__device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+template <int OPB, int OPA>
+__device__ __forceinline__ f32x16 mfma4(const i32x4 &b, const i32x4 &a, const f32x16 &c, int sb, int sa) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(i32x8{b[0], b[1], b[2], b[3], 0, 0, 0, 0},
+                                                           i32x8{a[0], a[1], a[2], a[3], 0, 0, 0, 0}, c, 4, 4, OPB, sb,
+                                                           OPA, sa);
+}
 struct ItemA4 {
     int g, row0, row_end, n0;
 };
 
-template <bool SWIGLU, int WR, int MI>
-__global__ __launch_bounds__(256 * WR, WR == 1 ? 2 : 1) void tiled_a4_kernel(GemmProblem p, int nN) {
-    typedef RingA4<WR, MI> R;
-    constexpr int S = R::S, NW = R::waves;
+template <bool SWIGLU, int WR, int WC, int MI>
+__global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p, int nN) {
+    typedef RingA4<WR, WC, MI> R;
+    constexpr int S = R::S, NW = R::waves, NJ = 8 / WC;  // 32-column blocks of a wavefront
     constexpr int W = SWIGLU ? 128 : 256;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[R::lds];
     int *table = reinterpret_cast<int *>(lds + R::table);
 
     const int tid = threadIdx.x;
-    const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wr = w / 4, wc = w % 4;
+    const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wr = w / WC, wc = w % WC;
     const int l32 = lane & 31, hb = lane >> 5;
     const int nk = (p.K + kA4BK - 1) / kA4BK;
 
     // ---- this workgroup's items ----
-    const int n_tiles = *p.n_tiles;
+    const int n_tiles = scalar(*p.n_tiles);
     const int n_work = n_tiles * nN;
     const int per = (n_work + kXcds - 1) / kXcds;
     const int xcd = blockIdx.x % kXcds, slot = blockIdx.x / kXcds, slots = gridDim.x / kXcds;
     const int mine = min(per, n_work - xcd * per);
-    if (slot >= mine) return;
-    const int count = (mine - slot + slots - 1) / slots;
+    if (mine <= 0) return;
+    // full rounds, then (split) one part of an item of the last one
+    const int split = scalar(tail_parts(per, slots, nk));
+    const int tail = split > 1 ? scalar(mine % slots) : 0, full = mine - tail;
+    int count = slot < full ? scalar((full - slot + slots - 1) / slots) : 0;
+    int part = 0, parts = 1;  // of the last item
+    if (slot < tail * split) {
+        parts = split;
+        part = scalar(slot % split);
+        ++count;
+    }
+    if (count == 0) return;
     if (MOE_BOUNDS_FAIL(count <= kA4Items, BOUNDS_TILE)) return;
+    const int last_k0 = scalar(part * nk / parts), last_k1 = scalar((part + 1) * nk / parts);  // its steps
     if (w == 0 && lane < count) {
         int mt, nt;
-        tile_of(p, nN, n_tiles, xcd * per + slot + slots * lane, mt, nt);
+        const bool cut = parts > 1 && lane == count - 1;
+        tile_of(p, nN, n_tiles, xcd * per + (cut ? full + slot / split : slot + slots * lane), mt, nt);
         const bool ok = mt < p.max_tiles;
         int g = ok ? p.tiles[4 * mt] : 0, r0 = ok ? p.tiles[4 * mt + 1] : 0, r1 = ok ? p.tiles[4 * mt + 2] : 0;
         if (MOE_BOUNDS_FAIL(ok && g >= 0 && g < p.n_groups && r0 >= 0 && r0 < r1 && r1 <= p.M, BOUNDS_TILE)) {
@@ -114,6 +149,7 @@ __global__ __launch_bounds__(256 * WR, WR == 1 ? 2 : 1) void tiled_a4_kernel(Gem
         *reinterpret_cast<i32x4 *>(table + 4 * lane) = i32x4{g, r0, r1, nt * W};
     }
     __syncthreads();
+    count = scalar(count);
     auto item_at = [&](int j) {
         const i32x4 t = *reinterpret_cast<const i32x4 *>(table + 4 * j);
         ItemA4 it;
@@ -141,12 +177,13 @@ __global__ __launch_bounds__(256 * WR, WR == 1 ? 2 : 1) void tiled_a4_kernel(Gem
     // byte rows and K groups of the last step that the weights have
     const int k_rows = p.K / 2 - 64 * (nk - 1), k_groups = p.K / 32 - 4 * (nk - 1);
     const bool ragged = p.K % kA4BK != 0;
-    auto set_sources = [&](const ItemA4 &it) {
+    auto set_sources = [&](const ItemA4 &it, int kt) {
         int ln = lane;  // re-read: its multiples need not live through the K loop
         asm volatile("" : "+v"(ln));
         const bool extra = it.g == p.extra_group;
-        a_base = reinterpret_cast<const uint8_t *>(p.A) + (long long)it.row0 * 64;
-        const long long go = extra ? 0 : (long long)it.g * p.b_stride, so = extra ? 0 : (long long)it.g * p.s_stride;
+        a_base = reinterpret_cast<const uint8_t *>(p.A) + (kt * p.as_ld + it.row0) * 64;
+        const long long go = (extra ? 0 : (long long)it.g * p.b_stride) + 64LL * kt * p.N;
+        const long long so = (extra ? 0 : (long long)it.g * p.s_stride) + 4LL * kt * p.N;
         const uint8_t *B0 = reinterpret_cast<const uint8_t *>(extra ? p.Bx0 : p.B0) + go;
         const uint8_t *S0 = reinterpret_cast<const uint8_t *>(extra ? p.Sx0 : p.S0) + so;
         b_base[0] = B0;
@@ -163,7 +200,7 @@ __global__ __launch_bounds__(256 * WR, WR == 1 ? 2 : 1) void tiled_a4_kernel(Gem
         for (int q = 0; q < R::nS; ++q) {
             const int i = s_slot(q);
             if (i < R::BM / 64) {
-                s_base[q] = reinterpret_cast<const uint8_t *>(p.As) + (long long)it.row0 * 4;
+                s_base[q] = reinterpret_cast<const uint8_t *>(p.As) + (kt * p.as_ld + it.row0) * 4;
                 s_off[q] = (64 * i + ln) * 4;
             } else {
                 const int h = (i - R::BM / 64) >> 1, kg = 2 * ((i - R::BM / 64) & 1) + (ln >> 5);
@@ -173,7 +210,39 @@ __global__ __launch_bounds__(256 * WR, WR == 1 ? 2 : 1) void tiled_a4_kernel(Gem
             }
         }
     };
-    int c_item = 0, c_kt = 0;  // what the next copies are of
+    // what the next copies are of: step c_kt of item c_item, c_left steps before the next item
+    int c_item = 0, c_kt, c_left;
+    long long a_step = p.as_ld * 64, b_step = 64LL * p.N, s_step[R::nS];
+#pragma unroll
+    for (int q = 0; q < R::nS; ++q) s_step[q] = s_slot(q) < R::BM / 64 ? p.as_ld * 4 : 4LL * p.N;
+    auto begin_item = [&]() {
+        const bool cut = c_item == count - 1;
+        c_kt = cut ? last_k0 : 0;
+        c_left = (cut ? last_k1 : nk) - c_kt;
+        set_sources(item_at(c_item), c_kt);
+    };
+    auto move = [&](long long by) {
+        a_base += by * a_step;
+        b_base[0] += by * b_step;
+        b_base[1] += by * b_step;
+#pragma unroll
+        for (int q = 0; q < R::nS; ++q) s_base[q] += by * s_step[q];
+        c_kt += (int)by;
+    };
+    // after an item's last step: the next item; past the last one its last step's
+    // copies are repeated (into stages that nobody reads)
+    auto next_item = [&]() {
+        if (c_item + 1 < count) {
+            ++c_item;
+            begin_item();
+        } else {
+            move(-1);
+            a_step = b_step = 0;
+#pragma unroll
+            for (int q = 0; q < R::nS; ++q) s_step[q] = 0;
+            c_left = 0x7fffffff;
+        }
+    };
     auto copy = [&](int q, int stage) {
         uint8_t *st = lds + stage * R::stage;
         const bool last = ragged && c_kt == nk - 1;
@@ -182,105 +251,110 @@ __global__ __launch_bounds__(256 * WR, WR == 1 ? 2 : 1) void tiled_a4_kernel(Gem
         } else if (q < R::nA + R::nB) {
             const int i = w + NW * (q - R::nA);
             uint32_t o = b_off[q - R::nA];
-            if (last) o -= (uint32_t)max(8 * (i & 7) + (lane >> 3) - (k_rows - 1), 0) * (uint32_t)p.N;
+            o -= last ? (uint32_t)max(8 * (i & 7) + (lane >> 3) - (k_rows - 1), 0) * (uint32_t)p.N : 0u;
             copy16(b_base[(NW * (q - R::nA)) >> 3] + o, st + R::a_bytes + i * 1024);
         } else {
             const int i = s_slot(q - R::nA - R::nB);
             uint32_t o = s_off[q - R::nA - R::nB];
-            if (last && i >= R::BM / 64)
-                o -= (uint32_t)max(2 * ((i - R::BM / 64) & 1) + (lane >> 5) - (k_groups - 1), 0) * (uint32_t)p.N;
+            o -= last && i >= R::BM / 64
+                     ? (uint32_t)max(2 * ((i - R::BM / 64) & 1) + (lane >> 5) - (k_groups - 1), 0) * (uint32_t)p.N
+                     : 0u;
             copy4(s_base[q - R::nA - R::nB] + o, st + R::a_bytes + R::b_bytes + i * 256);
         }
     };
-    // on to the next step, or the next item; past the last item its last step's
-    // copies are repeated (into stages that nobody reads)
-    auto advance = [&]() {
-        if (c_kt + 1 < nk) {
-            ++c_kt;
-            a_base += p.as_ld * 64;
-            b_base[0] += 64LL * p.N;
-            b_base[1] += 64LL * p.N;
-#pragma unroll
-            for (int q = 0; q < R::nS; ++q) s_base[q] += s_slot(q) < R::BM / 64 ? p.as_ld * 4 : 4LL * p.N;
-        } else if (c_item + 1 < count) {
-            ++c_item;
-            c_kt = 0;
-            set_sources(item_at(c_item));
-        }
-    };
-
-    // ---- operand reads of half kh (64 deep) of a stage ----
+    // ---- operand reads of half kh (64 deep) of a stage, and of a stage's scales ----
     struct Frag {
-        i32x4 a[MI], b[2];
-        u32x2 raw[2][2];
-        int sa[MI], sb[2];
+        i32x4 a[MI], b[NJ];
+        u32x2 raw[NJ][2];
     };
     const int i16 = lane & 15;
-    uint32_t tr_at[2];  // column block j: byte row 16 hb + i16 / 2 of the first half
+    // column block j of this wavefront: half-tile and column within it
+    auto b_half = [&](int j) { return SWIGLU ? j / (NJ / 2) : (32 * (NJ * wc + j)) >> 7; };
+    auto b_col = [&](int j) { return SWIGLU ? 32 * (NJ / 2 * wc + j % (NJ / 2)) : (32 * (NJ * wc + j)) & 127; };
+    uint32_t tr_at[NJ];  // byte row 16 hb + i16 / 2 of the first half
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int col = SWIGLU ? 32 * wc : 64 * (wc & 1) + 32 * j, half = SWIGLU ? j : wc >> 1;
-        const int c = (col >> 4) + ((lane >> 4) & 1), row = 16 * hb + (i16 >> 1);
-        tr_at[j] = R::a_bytes + half * 8192 + row * 128 + 16 * (c ^ (2 * ((row >> 1) & 3))) + 8 * (i16 & 1);
+    for (int j = 0; j < NJ; ++j) {
+        const int c = (b_col(j) >> 4) + ((lane >> 4) & 1), row = 16 * hb + (i16 >> 1);
+        tr_at[j] = R::a_bytes + b_half(j) * 8192 + row * 128 + 16 * (c ^ (2 * ((row >> 1) & 3))) + 8 * (i16 & 1);
     }
     const int a_row = wr * 32 * MI + l32;
     const int a_at = a_row * 64 + 16 * (hb ^ ((a_row >> 2) & 3));  // first half; the second: ^ 32
-    const int sa_at = R::a_bytes + R::b_bytes + a_row * 4 + hb;
-    const int sb_at = R::sb_at + (SWIGLU ? 32 * wc : (wc >> 1) * 512 + 64 * (wc & 1)) + l32 + 128 * hb;
-    constexpr int NR = 4 + 2 + 2 * MI;
+    const int sa_at = R::a_bytes + R::b_bytes + a_row * 4;
+    // scales of the column blocks by one transposing read: its rows are (half,
+    // block) pairs, so that a lane gets its column's bytes of all of them
+    uint32_t sb_at;
+    {
+        const int r = (i16 >> 1) & (2 * NJ - 1), j = r % NJ, kh = r / NJ;
+        sb_at = R::sb_at + b_half(j) * 512 + (2 * kh + hb) * 128 + b_col(j) + 16 * ((lane >> 4) & 1) + 8 * (i16 & 1);
+    }
+    u32x2 sb_raw, sb;        // read, in use: byte NJ kh + j
+    int sa_raw[MI], sa[MI];  // byte 2 kh of the word in use
+    constexpr int NRF = 2 * NJ + MI, NRS = MI + 1;  // reads of a half, and of a stage's scales
     auto read = [&](Frag &f, int r, int stage, auto kh_) {
         constexpr int kh = decltype(kh_)::value;
         const uint8_t *st = lds + stage * R::stage;
-        if (r < 4) {
+        if (r < 2 * NJ) {
             const int j = r >> 1;
             const uint32_t at = lds_addr(st) + tr_at[j];
             if (r & 1) f.raw[j][1] = ds_tr8_at<4096 * kh + 1024>(at);
             else f.raw[j][0] = ds_tr8_at<4096 * kh>(at);
-        } else if (r < 4 + MI) {
-            f.a[r - 4] = *reinterpret_cast<const i32x4 *>(st + (a_at ^ (32 * kh)) + 2048 * (r - 4));
-        } else if (r < 6 + MI) {
-            const int j = r - 4 - MI;
-            f.sb[j] = st[sb_at + 256 * kh + (SWIGLU ? 512 : 32) * j];
+        } else if (r < NRF) {
+            f.a[r - 2 * NJ] = *reinterpret_cast<const i32x4 *>(st + (a_at ^ (32 * kh)) + 2048 * (r - 2 * NJ));
+        } else if (r == NRF) {
+            sb_raw = ds_tr8(lds_addr(st) + sb_at);
         } else {
-            f.sa[r - 6 - MI] = st[sa_at + 2 * kh + 128 * (r - 6 - MI)];
+            sa_raw[r - NRF - 1] = *reinterpret_cast<const int *>(st + sa_at + 128 * (r - NRF - 1));
         }
     };
-    auto land = [&](Frag &f) {
+    auto land = [&](Frag &f, bool scales) {
         wait_lds();
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < NJ; ++j) {
             fence(f.raw[j][0]);
             fence(f.raw[j][1]);
             f.b[j] = i32x4{(int)f.raw[j][0][0], (int)f.raw[j][0][1], (int)f.raw[j][1][0], (int)f.raw[j][1][1]};
         }
+        if (scales) {
+            fence(sb_raw);
+            sb = sb_raw;
+#pragma unroll
+            for (int m = 0; m < MI; ++m) sa[m] = sa_raw[m] >> (8 * hb);
+        }
     };
 
-    f32x16 acc[MI][2];
+    f32x16 acc[MI][NJ];
     auto clear = [&]() {
 #pragma unroll
         for (int m = 0; m < MI; ++m)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < NJ; ++j)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[m][j][i] = 0.0f;
     };
     clear();
     // the weights are the first operand: a lane's sixteen results are one row
     // (lane % 32 of its block) and columns 8 q + 4 (lane / 32) + 0..3, q < 4
-    auto mma = [&](const Frag &f, int m) {
+    auto mma = [&](const Frag &f, int i, auto kh_) {
+        constexpr int kh = decltype(kh_)::value;
+        const int m = i / NJ, j = i % NJ;
         __builtin_amdgcn_sched_barrier(0);
-        const i32x4 a = f.a[m];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const i32x4 b = f.b[j];
-            acc[m][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                i32x8{b[0], b[1], b[2], b[3], 0, 0, 0, 0}, i32x8{a[0], a[1], a[2], a[3], 0, 0, 0, 0}, acc[m][j], 4, 4,
-                0, f.sb[j], 0, f.sa[m]);
+        const int sbw = (int)(NJ == 4 ? sb[kh] : sb[0]);
+        switch (NJ == 4 ? j : 2 * kh + j) {
+        case 0: acc[m][j] = mfma4<0, 2 * kh>(f.b[j], f.a[m], acc[m][j], sbw, sa[m]); break;
+        case 1: acc[m][j] = mfma4<1, 2 * kh>(f.b[j], f.a[m], acc[m][j], sbw, sa[m]); break;
+        case 2: acc[m][j] = mfma4<2, 2 * kh>(f.b[j], f.a[m], acc[m][j], sbw, sa[m]); break;
+        default: acc[m][j] = mfma4<3, 2 * kh>(f.b[j], f.a[m], acc[m][j], sbw, sa[m]); break;
         }
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    // ---- a finished tile ----
+    // ---- a finished tile. Every store is issued, so that the waits below can
+    // count them: lanes without an output give an offset past the buffer's end,
+    // which the store drops ----
+    constexpr int kNowhere = 0x7ffffff0;
+    auto rsrc = [](void *base, int bytes) {
+        return __builtin_amdgcn_make_buffer_rsrc(base, 0, bytes, 0x00020000);
+    };
     auto swap32 = [](uint32_t &x, uint32_t &y) {  // x's upper 32 lanes and y's lower ones change places
         const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
         x = r[0];
@@ -292,51 +366,57 @@ __global__ __launch_bounds__(256 * WR, WR == 1 ? 2 : 1) void tiled_a4_kernel(Gem
     auto gate_up_out = [&](const ItemA4 &it) {
         int ln = lane;
         asm volatile("" : "+v"(ln));
-        const bool pad = it.n0 + 32 * wc >= p.N;  // columns past the end: zero codes, scale 1
-        uint8_t *Hs = reinterpret_cast<uint8_t *>(p.Cqs);
-        const long long at = (long long)(it.n0 >> 7) * p.cqs_ld;
+        const long long at = (long long)(it.n0 >> 7) * p.cqs_ld + it.row0;
+        const int rows = it.row_end - it.row0;
+        const auto codes = rsrc(p.Cq + at * 64, rows * 64);
+        const auto scales = rsrc(reinterpret_cast<uint8_t *>(p.Cqs) + at * 4, rows * 4);
 #pragma unroll
-        for (int m = 0; m < MI; m += 2) {
-            uint32_t code[2][2], byte[2];
+        for (int j = 0; j < NJ / 2; ++j) {
+            const int grp = NJ / 2 * wc + j;              // group of 32 of the tile's columns
+            const bool pad = it.n0 + 32 * grp >= p.N;  // columns past the end: zero codes, scale 1
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (m + u >= MI) {
-                    code[u][0] = code[0][0];
-                    code[u][1] = code[0][1];
-                    byte[u] = byte[0];
-                    continue;
+            for (int m = 0; m < MI; m += 2) {
+                uint32_t code[2][2], byte[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if (m + u >= MI) {
+                        code[u][0] = code[0][0];
+                        code[u][1] = code[0][1];
+                        byte[u] = byte[0];
+                        continue;
+                    }
+                    const f32x16 &g = acc[m + u][j], &x = acc[m + u][j + NJ / 2];
+                    float v[16];
+                    uint32_t t = 0;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        v[i] = silu_f32(g[i]) * x[i];
+                        t = max(t, mx4::mag_bits(v[i]));
+                    }
+                    uint32_t s = t;
+                    swap32(t, s);
+                    byte[u] = mx4::scale_byte(max(t, s));
+                    code[u][0] = mx4::codes8(v, byte[u]);
+                    code[u][1] = mx4::codes8(v + 8, byte[u]);
+                    if (pad) {
+                        code[u][0] = code[u][1] = 0;
+                        byte[u] = 127;
+                    }
                 }
-                const f32x16 &g = acc[m + u][0], &x = acc[m + u][1];
-                float v[16];
-                uint32_t t = 0;
+                u32x4 out;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    v[i] = silu_f32(g[i]) * x[i];
-                    t = max(t, mx4::mag_bits(v[i]));
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t x = code[0][h], y = code[1][h];
+                    swap32(x, y);
+                    out[2 * h] = (x & 0xffffu) | y << 16;
+                    out[2 * h + 1] = x >> 16 | (y & 0xffff0000u);
                 }
-                uint32_t s = t;
-                swap32(t, s);
-                byte[u] = mx4::scale_byte(max(t, s));
-                code[u][0] = mx4::codes8(v, byte[u]);
-                code[u][1] = mx4::codes8(v + 8, byte[u]);
-                if (pad) {
-                    code[u][0] = code[u][1] = 0;
-                    byte[u] = 127;
-                }
-            }
-            u32x4 out;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t x = code[0][h], y = code[1][h];
-                swap32(x, y);
-                out[2 * h] = (x & 0xffffu) | y << 16;
-                out[2 * h + 1] = x >> 16 | (y & 0xffff0000u);
-            }
-            const bool up = ln >= 32;
-            const int row = it.row0 + wr * 32 * MI + 32 * (up ? m + 1 : m) + (ln & 31);
-            if (row < it.row_end && (!up || m + 1 < MI)) {
-                *reinterpret_cast<u32x4 *>(p.Cq + (at + row) * 64 + 16 * wc) = out;
-                Hs[(at + row) * 4 + wc] = (uint8_t)(up ? byte[1] : byte[0]);
+                const bool up = ln >= 32;
+                const int row = wr * 32 * MI + 32 * (up ? m + 1 : m) + (ln & 31);  // of the tile
+                const bool in = row < rows && (!up || m + 1 < MI);
+                __builtin_amdgcn_raw_buffer_store_b128(out, codes, in ? row * 64 + 16 * grp : kNowhere, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(up ? byte[1] : byte[0]), scales,
+                                                     in ? row * 4 + grp : kNowhere, 0, 0);
             }
         }
     };
@@ -345,12 +425,13 @@ __global__ __launch_bounds__(256 * WR, WR == 1 ? 2 : 1) void tiled_a4_kernel(Gem
     auto down_out = [&](const ItemA4 &it) {
         int ln = lane;
         asm volatile("" : "+v"(ln));
-        uint16_t *C = reinterpret_cast<uint16_t *>(p.C);
+        const int rows = it.row_end - it.row0, ld = p.ldc;
+        const auto C = rsrc(reinterpret_cast<uint16_t *>(p.C) + (long long)it.row0 * ld + it.n0, (rows * ld - it.n0) * 2);
 #pragma unroll
         for (int m = 0; m < MI; ++m) {
-            const int row = it.row0 + wr * 32 * MI + 32 * m + (ln & 31);
+            const int row = wr * 32 * MI + 32 * m + (ln & 31);  // of the tile
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < NJ; ++j)
 #pragma unroll
                 for (int q = 0; q < 4; q += 2) {
                     const f32x16 &x = acc[m][j];
@@ -359,77 +440,161 @@ __global__ __launch_bounds__(256 * WR, WR == 1 ? 2 : 1) void tiled_a4_kernel(Gem
                              b1 = pack_bf16x2(x[4 * q + 6], x[4 * q + 7]);
                     swap32(a0, b0);
                     swap32(a1, b1);
-                    const int col = it.n0 + 64 * wc + 32 * j + 8 * (q + (ln >> 5));
-                    if (row < it.row_end && col < p.N)
-                        *reinterpret_cast<u32x4 *>(C + (long long)row * p.ldc + col) = u32x4{a0, a1, b0, b1};
+                    const int col = 32 * (NJ * wc + j) + 8 * (q + (ln >> 5));
+                    const bool in = row < rows && it.n0 + col < p.N;
+                    __builtin_amdgcn_raw_buffer_store_b128(u32x4{a0, a1, b0, b1}, C,
+                                                               in ? (row * ld + col) * 2 : kNowhere, 0, 0);
                 }
         }
+    };
+
+    constexpr int ST = SWIGLU ? NJ * ((MI + 1) / 2) : 2 * NJ * MI;  // stores of a tile
+    auto tile_out = [&](const ItemA4 &it) {
+        if constexpr (SWIGLU) gate_up_out(it);
+        else down_out(it);
+    };
+    // One part of a split item: its fp32 sums go to its slot; the workgroup that
+    // finds itself the last adds the parts in their order, all read back from
+    // memory, so the sum does not depend on which is last. One thread makes the
+    // stores visible beyond this XCD's L2 and counts the part (the counter is left
+    // at zero); its one acquire serves the workgroup after the barrier.
+    auto join_parts = [&]() -> bool {
+        const int first = xcd * kBlocksPerXcd + (slot - part), cnt = xcd * kBlocksPerXcd + slot / parts;
+        if (MOE_BOUNDS_FAIL(first >= 0 && first + parts <= kTailSlots, BOUNDS_TAIL_SLOT)) return false;
+        constexpr int NV = MI * NJ * 4;
+        f32x4 *buf = reinterpret_cast<f32x4 *>(p.tail_part) + (long long)first * NV * R::threads;
+        f32x4 *mine_at = buf + (long long)part * NV * R::threads;
+#pragma unroll
+        for (int m = 0; m < MI; ++m)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    mine_at[((m * NJ + j) * 4 + q) * R::threads + tid] =
+                        f32x4{acc[m][j][4 * q], acc[m][j][4 * q + 1], acc[m][j][4 * q + 2], acc[m][j][4 * q + 3]};
+        wait_vm<0>();
+        __syncthreads();
+        int *is_last = reinterpret_cast<int *>(lds);  // the ring is idle
+        if (tid == 0) {
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+            const bool last = __hip_atomic_fetch_add(p.tail_cnt + cnt, 1, __ATOMIC_RELAXED,
+                                                     __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
+            if (last) {
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+                __hip_atomic_store(p.tail_cnt + cnt, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+            *is_last = last;
+        }
+        __syncthreads();
+        if (!*is_last) return false;
+        clear();
+        for (int q = 0; q < parts; ++q) {
+            const f32x4 *from = buf + (long long)q * NV * R::threads;
+#pragma unroll
+            for (int m = 0; m < MI; ++m)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const f32x4 v = from[((m * NJ + j) * 4 + i) * R::threads + tid];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) acc[m][j][4 * i + x] += v[x];
+                    }
+        }
+        return true;
     };
 
     // ---- fill the ring, then the steps of every item ----
     typedef std::integral_constant<int, 0> H0;
     typedef std::integral_constant<int, 1> H1;
     constexpr int NC = R::per_step;
-    set_sources(item_at(0));
+    // A half step's products in order, with what is issued before each. Reads come
+    // early, so that they have landed when the last products are issued; the copies
+    // into a stage follow the barrier that frees it. PRE products stand before it
+    constexpr int P = MI * NJ, PRE = P > 4 ? 2 : 1, PB = P - PRE;
+    constexpr int RA = P > 4 ? P - 4 : 1, RB = PB > 4 ? PB - 4 : 1;
+    auto upto = [](int i, int n, int slots) { return i >= slots ? n : i * n / slots; };
+    begin_item();
 #pragma unroll
     for (int t = 0; t < S; ++t) {
 #pragma unroll
         for (int q = 0; q < NC; ++q) copy(q, t);
-        advance();
+        move(1);
+        if (--c_left == 0) next_item();
     }
     wait_vm<(S - 1) * NC>();
     __builtin_amdgcn_s_barrier();
     Frag f0, f1;
 #pragma unroll
-    for (int r = 0; r < NR; ++r) read(f0, r, 0, H0{});
-    land(f0);
-    constexpr int PRE = MI > 1 ? 1 : 0, SL = MI - PRE;  // row blocks multiplied before the barrier
+    for (int r = 0; r < NRF + NRS; ++r) read(f0, r, 0, H0{});
+    land(f0, true);
     int stage = 0;
-    for (int j = 0; j < count; ++j) {
-        for (int kt = 0; kt < nk; ++kt) {
-            const int nstage = stage + 1 == S ? 0 : stage + 1;
+    // One step, without a branch: its products would sink past one, away from the
+    // reads and copies that they hide
+    auto step = [&](auto stores) {
+        const int nstage = stage + 1 == S ? 0 : stage + 1;
 #pragma unroll
-            for (int m = 0; m < MI; ++m) {
+        for (int i = 0; i < P; ++i) {
 #pragma unroll
-                for (int r = m * NR / MI; r < (m + 1) * NR / MI; ++r) read(f1, r, stage, H1{});
-                mma(f0, m);
-            }
-            land(f1);  // the stage is read: its reads are done before anyone refills it
-#pragma unroll
-            for (int m = 0; m < PRE; ++m) mma(f1, m);
-            wait_vm<(S - 2) * NC>();
-            __builtin_amdgcn_s_barrier();
-#pragma unroll
-            for (int c = 0; c < SL; ++c) {
-#pragma unroll
-                for (int r = c * NR / SL; r < (c + 1) * NR / SL; ++r) read(f0, r, nstage, H0{});
-#pragma unroll
-                for (int q = c * NC / SL; q < (c + 1) * NC / SL; ++q) copy(q, stage);
-                mma(f1, c + PRE);
-            }
-            advance();
-            land(f0);
-            stage = nstage;
+            for (int r = upto(i, NRF, RA); r < upto(i + 1, NRF, RA); ++r) read(f1, r, stage, H1{});
+            mma(f0, i, H0{});
         }
-        const ItemA4 it = item_at(j);
-        if constexpr (SWIGLU) gate_up_out(it);
-        else down_out(it);
-        clear();
+        land(f1, false);  // the stage is read: its reads are done before anyone refills it
+#pragma unroll
+        for (int i = 0; i < PRE; ++i) mma(f1, i, H1{});
+        wait_vm<(S - 2) * NC + decltype(stores)::value>();
+        __builtin_amdgcn_s_barrier();
+#pragma unroll
+        for (int i = 0; i < PB; ++i) {
+#pragma unroll
+            for (int r = upto(i, NRF + NRS, RB); r < upto(i + 1, NRF + NRS, RB); ++r) read(f0, r, nstage, H0{});
+#pragma unroll
+            for (int q = upto(i, NC, PB); q < upto(i + 1, NC, PB); ++q) copy(q, stage);
+            mma(f1, PRE + i, H1{});
+        }
+        move(1);
+        land(f0, true);
+        stage = nstage;
+    };
+    // Runs of steps up to the next event: the end of an item's copies, of its
+    // products, or of the first steps after a stored tile, whose waits let its
+    // stores (newer than the copies waited for) be under way
+    int j = 0, left = count == 1 ? last_k1 - last_k0 : nk, after = 0;
+    for (;;) {
+        int n = min(left, c_left);
+        left -= n, c_left -= n;
+        if (after > 0) {
+            const int m = min(n, after);
+            n -= m, after -= m;
+            for (int i = 0; i < m; ++i) step(std::integral_constant<int, ST>{});
+        }
+        for (int i = 0; i < n; ++i) step(H0{});
+        if (c_left == 0) next_item();
+        if (left == 0) {
+            if (j == count - 1) break;
+            tile_out(item_at(j));
+            clear();
+            ++j;
+            left = j == count - 1 ? last_k1 - last_k0 : nk;
+            after = S - 2;
+        }
     }
     wait_vm<0>();  // the repeated copies land before the workgroup ends
+    if (parts > 1 && !join_parts()) return;
+    tile_out(item_at(count - 1));
 }
 
-template <bool SWIGLU, int WR, int MI>
+template <bool SWIGLU, int MI>
 hipError_t launch(const GemmProblem &p, hipStream_t s) {
-    typedef RingA4<WR, MI> R;
+    constexpr int WR = 2, WC = A4_WC;
+    typedef RingA4<WR, WC, MI> R;
     const int nN = (p.N + (SWIGLU ? 127 : 255)) / (SWIGLU ? 128 : 256);
     const long long items = ((long long)p.max_tiles * nN + kXcds - 1) / kXcds;  // of an XCD, at most
     if (items > 0x0fffffffLL) return hipErrorInvalidValue;
     // one round of resident workgroups, or as many as keep to the item table
     long long slots = kBlocksPerXcd * R::per_cu;
     while ((items + slots - 1) / slots > kA4Items) slots += kBlocksPerXcd * R::per_cu;
-    if (slots > items) slots = items;
-    hipLaunchKernelGGL((tiled_a4_kernel<SWIGLU, WR, MI>), dim3((unsigned)(slots * kXcds)), dim3(R::threads), 0, s, p, nN);
+    hipLaunchKernelGGL((tiled_a4_kernel<SWIGLU, WR, WC, MI>), dim3((unsigned)(slots * kXcds)), dim3(R::threads), 0, s, p, nN);
     return hipGetLastError();
 }
 
@@ -443,15 +608,15 @@ int tiled_a4_bm(long long rows, int groups) {
 
 hipError_t launch_tiled_a4(const GemmProblem &p, bool swiglu, int bm, hipStream_t s) {
     if (p.N < 32 || p.N % 32 || p.K < 32 || p.K % 32 || !p.tiles || !p.n_tiles || !p.A || !p.As || p.as_ld < p.M + 256LL ||
-        !p.B0 || !p.S0 || (swiglu && (!p.B1 || !p.S1 || !p.Cq || !p.Cqs || p.cqs_ld < p.M)) || (!swiglu && !p.C))
+        !p.B0 || !p.S0 || !p.tail_part || !p.tail_cnt || (swiglu && (!p.B1 || !p.S1 || !p.Cq || !p.Cqs || p.cqs_ld < p.M)) || (!swiglu && !p.C))
         return hipErrorInvalidValue;
     if (p.extra_group >= 0 && (!p.Bx0 || !p.Sx0 || (swiglu && (!p.Bx1 || !p.Sx1)))) return hipErrorInvalidValue;
     if (p.max_tiles < 1) return hipSuccess;
     switch (bm) {
-    case 256: return swiglu ? tiled::launch<true, 2, 4>(p, s) : tiled::launch<false, 2, 4>(p, s);
-    case 192: return swiglu ? tiled::launch<true, 2, 3>(p, s) : tiled::launch<false, 2, 3>(p, s);
-    case 128: return swiglu ? tiled::launch<true, 2, 2>(p, s) : tiled::launch<false, 2, 2>(p, s);
-    case 64: return swiglu ? tiled::launch<true, 2, 1>(p, s) : tiled::launch<false, 2, 1>(p, s);
+    case 256: return swiglu ? tiled::launch<true, 4>(p, s) : tiled::launch<false, 4>(p, s);
+    case 192: return swiglu ? tiled::launch<true, 3>(p, s) : tiled::launch<false, 3>(p, s);
+    case 128: return swiglu ? tiled::launch<true, 2>(p, s) : tiled::launch<false, 2>(p, s);
+    case 64: return swiglu ? tiled::launch<true, 1>(p, s) : tiled::launch<false, 1>(p, s);
     }
     return hipErrorInvalidValue;
 }
