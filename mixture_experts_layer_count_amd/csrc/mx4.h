@@ -39,6 +39,26 @@ __device__ __forceinline__ uint32_t codes8(const float *v, uint32_t byte) {
     return byte == 255u ? 0u : w;
 }
 
+__device__ __forceinline__ bf16x2 pair_of(uint32_t w) { return __builtin_bit_cast(bf16x2, w); }
+// the same of 8 bf16 values as they lie in memory, and the bits of their largest
+// magnitude (as fp32's: infinity and NaN above the others here too)
+__device__ __forceinline__ uint32_t codes8(const u32x4 &x, uint32_t byte) {
+    const float s = scale_of(byte == 255u ? 127u : byte);
+    uint32_t w = 0;
+    w = (uint32_t)__builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, pair_of(x[0]), s, 0);
+    w = (uint32_t)__builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, pair_of(x[1]), s, 1);
+    w = (uint32_t)__builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, pair_of(x[2]), s, 2);
+    w = (uint32_t)__builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, pair_of(x[3]), s, 3);
+    return byte == 255u ? 0u : w;
+}
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u16x2 mags(uint32_t pair) { return __builtin_bit_cast(u16x2, pair & 0x7fff7fffu); }
+__device__ __forceinline__ uint32_t max_bits(const u16x2 &m) { return (uint32_t)max(m[0], m[1]) << 16; }
+__device__ __forceinline__ uint32_t max_bits(const u32x4 &x) {
+    return max_bits(__builtin_elementwise_max(__builtin_elementwise_max(mags(x[0]), mags(x[1])),
+                                              __builtin_elementwise_max(mags(x[2]), mags(x[3]))));
+}
+
 // 8 consecutive values of X at element offset o (16-byte aligned)
 template <bool F32>
 __device__ __forceinline__ void load8(const void *X, long long o, float (&v)[8]) {
@@ -76,7 +96,7 @@ __host__ __device__ inline int panels(int C) { return (C + 127) / 128; }
 struct Mx4Panels {
     const void *X;
     const int32_t *row_src;
-    int gk, C;
+    int gk, C;  // gk <= 64
     int rows, extra;
     const int32_t *n_rows;
     uint8_t *A;

@@ -16,6 +16,15 @@ using namespace mx4;
 constexpr long long kMaxThreads = 0xffffffffLL;  // of a launch (beyond, it takes their number mod 2^32)
 constexpr int kPer = 16;                         // values per thread of the row kernels
 
+// the largest of a lane and its neighbour, and of the four lanes of a quad
+__device__ __forceinline__ uint32_t pair_max(uint32_t v) {
+    return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xb1, 0xf, 0xf, true));  // lanes 1 0 3 2
+}
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+    v = pair_max(v);
+    return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4e, 0xf, 0xf, true));  // lanes 2 3 0 1
+}
+
 // ---- rows: a thread owns 16 consecutive values; the two threads of a group
 // exchange their maxima, and one of them stores the scale byte ----
 template <bool F32>
@@ -29,15 +38,24 @@ __global__ __launch_bounds__(256) void mx4_rows_kernel(const void *X, long long 
         const long long row = i / C;
         o = row * ldx + (i - row * C);
     }
-    float v[2][8];
-    load8<F32>(X, o, v[0]);
-    load8<F32>(X, o + 8, v[1]);
-    uint32_t m = 0;
+    uint32_t m, b;
+    u32x2 q;
+    if constexpr (F32) {
+        float v[2][8];
+        load8<true>(X, o, v[0]);
+        load8<true>(X, o + 8, v[1]);
+        m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, max(mag_bits(v[0][j]), mag_bits(v[1][j])));
-    m = max(m, (uint32_t)__shfl_xor((int)m, 1));
-    const uint32_t b = scale_byte(m);
-    *reinterpret_cast<u32x2 *>(Q + i / 2) = u32x2{codes8(v[0], b), codes8(v[1], b)};
+        for (int j = 0; j < 8; ++j) m = max(m, max(mag_bits(v[0][j]), mag_bits(v[1][j])));
+        b = scale_byte(pair_max(m));
+        q = u32x2{codes8(v[0], b), codes8(v[1], b)};
+    } else {
+        const u32x4 *x = reinterpret_cast<const u32x4 *>(reinterpret_cast<const uint16_t *>(X) + o);
+        const u32x4 x0 = x[0], x1 = x[1];
+        b = scale_byte(pair_max(max(max_bits(x0), max_bits(x1))));
+        q = u32x2{codes8(x0, b), codes8(x1, b)};
+    }
+    *reinterpret_cast<u32x2 *>(Q + i / 2) = q;
     if ((t & 1) == 0) S[i / kGroup] = (uint8_t)b;
 }
 
@@ -152,53 +170,65 @@ __global__ __launch_bounds__(256) void mx4_weights_back_kernel(const uint8_t *Q,
     }
 }
 
-// ---- rows in the product's layout: 16 lanes a row and panel (8 values each,
-// four lanes a group), 64 rows a workgroup ----
-constexpr int kPanelRows = 64;
-template <int P, bool TILES>
-__global__ __launch_bounds__(1024) void mx4_panels_kernel(Mx4Panels p, TilesJob j) {
+// ---- rows in the product's layout: 16 lanes a row and panel (8 values each, four
+// lanes a group), RPT rows of one panel each, 64 RPT rows of a panel a workgroup.
+// SLICED: panel x, x + 8, ... on XCD x (workgroup number mod 8), one after the
+// other: gathered rows are read once for each of a token's k places, and an XCD's
+// slice of all tokens then stays in its L2 ----
+// a / gk of 0 <= a < 2^31 as a product: (a mul) >> (31 + shift), mul = floor(2^(31 +
+// shift) / gk) + 1, 2^shift >= gk. (mul gk exceeds 2^(31 + shift) by at most gk <=
+// 2^shift, so the product is off by less than 1 / gk.) A division by an argument
+// takes about 35 instructions, for every row of every thread
+struct Divide {
+    uint32_t mul, shift;
+    explicit Divide(int gk) : shift(0) {
+        while ((1LL << shift) < gk) ++shift;
+        mul = (uint32_t)((1ULL << (31 + shift)) / gk + 1);
+    }
+    __device__ __forceinline__ int operator()(int a) const {
+        return (int)(((unsigned long long)(uint32_t)a * mul) >> (31 + shift));
+    }
+};
+template <int RPT, bool SLICED>
+__global__ __launch_bounds__(1024) void mx4_panels_kernel(Mx4Panels p, TilesJob j, int chunks, int np, Divide token) {
     __shared__ int scan_lds[16];
     int blk = blockIdx.x;
-    if (TILES) {
-        if (blk == 0) {
-            if (blockIdx.y == 0)
+    if (j.tiles) {  // the tile list, by a workgroup of its own (eight, to keep the others' XCDs)
+        if (blk < 8) {
+            if (blk == 0)
                 build_tiles(j.offsets, j.G, 0, j.bm, j.tiles, j.n_tiles, j.start, j.zero, j.n_zero, scan_lds);
             return;
         }
-        --blk;
+        blk -= 8;
     }
-    const int sub = threadIdx.x & 15;
-    const int r = blk * kPanelRows + (threadIdx.x >> 4);
+    const int kb = SLICED ? blk % 8 + 8 * (blk / 8 / chunks) : blk / chunks;
+    if (kb >= np) return;
+    const int r0 = (SLICED ? blk / 8 : blk) % chunks * (64 * RPT) + (threadIdx.x >> 4);
+    const int sub = threadIdx.x & 15, c = 128 * kb + 8 * sub;
     const int used = p.n_rows ? min(p.rows, *p.n_rows) : p.rows;
-    if (r >= p.rows + p.extra || (r >= used && r < p.rows)) return;  // a row's 16 lanes together
-    const long long src = r >= p.rows ? r - p.rows : p.row_src ? p.row_src[r] / p.gk : r;
-    const int np = panels(p.C), kb0 = blockIdx.y * P;
-    const uint16_t *x = reinterpret_cast<const uint16_t *>(p.X) + src * p.C;
-    float v[P][8];
+    // a row's 16 lanes are in or out together; those out read row 0 of X
+    bool in[RPT];
+    long long src[RPT];
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        const int c = 128 * (kb0 + i) + 8 * sub;
-        if (c < p.C) load8<false>(x, c, v[i]);
-        else
+    for (int i = 0; i < RPT; ++i) {
+        const int r = r0 + 64 * i;
+        in[i] = r < used || (r >= p.rows && r < p.rows + p.extra);
+        src[i] = !in[i] ? 0 : r >= p.rows ? r - p.rows : p.row_src ? token(p.row_src[r]) : r;
+    }
+    u32x4 x[RPT];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[i][q] = 0.0f;
+    for (int i = 0; i < RPT; ++i) {
+        x[i] = *reinterpret_cast<const u32x4 *>(reinterpret_cast<const uint16_t *>(p.X) + src[i] * p.C +
+                                                (c < p.C ? c : 0));
+        if (c >= p.C) x[i] = u32x4{0, 0, 0, 0};
     }
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        const int kb = kb0 + i;
-        if (kb >= np) return;
-        uint32_t m = 0;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) m = max(m, mag_bits(v[i][q]));
-        m = max(m, (uint32_t)__shfl_xor((int)m, 1));
-        m = max(m, (uint32_t)__shfl_xor((int)m, 2));
-        const uint32_t b = scale_byte(m);
-        uint32_t w = b << (8 * (sub >> 2));
-        w |= (uint32_t)__shfl_xor((int)w, 4);
-        w |= (uint32_t)__shfl_xor((int)w, 8);
-        const long long o = kb * p.ld + r;
-        *reinterpret_cast<uint32_t *>(p.A + o * 64 + 4 * sub) = codes8(v[i], b);
-        if (sub == 0) p.As[o] = w;
+    for (int i = 0; i < RPT; ++i) {
+        const uint32_t b = scale_byte(quad_max(max_bits(x[i])));
+        if (!in[i]) continue;
+        const long long o = kb * p.ld + r0 + 64 * i;
+        *reinterpret_cast<uint32_t *>(p.A + o * 64 + 4 * sub) = codes8(x[i], b);
+        if ((sub & 3) == 0) reinterpret_cast<uint8_t *>(p.As + o)[sub >> 2] = (uint8_t)b;
     }
 }
 
@@ -208,22 +238,22 @@ hipError_t launch_mx4_panels(const Mx4Panels &p, const TilesJob *tiles, hipStrea
     if (p.rows < 0 || p.extra < 0 || p.C < kGroup || p.C % kGroup || p.gk < 1 || !p.A || !p.As ||
         p.ld < (long long)p.rows + p.extra)
         return hipErrorInvalidValue;
-    const long long rows = (long long)p.rows + p.extra, groups = (rows + kPanelRows - 1) / kPanelRows;
+    const long long rows = (long long)p.rows + p.extra;
     const int np = panels(p.C);
-    const long long bx = groups + (tiles ? 1 : 0);
-    if (bx == 0) return hipSuccess;
-    const bool one = groups * np < 1024;  // few rows: a panel a workgroup
-    const int py = one ? np : (np + 3) / 4;
-    if (bx > kMaxThreads / 1024 || py > 65535) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)bx, (unsigned)py), block(1024);
-    const TilesJob none{};
-    if (tiles) {
-        if (one) hipLaunchKernelGGL((mx4_panels_kernel<1, true>), grid, block, 0, s, p, *tiles);
-        else hipLaunchKernelGGL((mx4_panels_kernel<4, true>), grid, block, 0, s, p, *tiles);
-    } else {
-        if (one) hipLaunchKernelGGL((mx4_panels_kernel<1, false>), grid, block, 0, s, p, none);
-        else hipLaunchKernelGGL((mx4_panels_kernel<4, false>), grid, block, 0, s, p, none);
-    }
+    // few rows: one a thread, for more workgroups
+    const bool few = (rows + 63) / 64 * np < 2048;
+    const long long chunks = (rows + (few ? 64 : 256) - 1) / (few ? 64 : 256);
+    // by XCD where gathered rows are read again and the panels fill the XCDs evenly
+    const bool sliced = !few && p.row_src && p.gk > 1 && (np % 8 == 0 || np >= 24);
+    const long long blocks = chunks * (sliced ? (np + 7) / 8 * 8 : np) + (tiles ? 8 : 0);
+    if (blocks == 0) return hipSuccess;
+    if (blocks > kMaxThreads / 1024) return hipErrorInvalidValue;
+    const TilesJob job = tiles ? *tiles : TilesJob{};
+    const dim3 grid((unsigned)blocks), block(1024);
+    const Divide token(p.gk);
+    if (few) hipLaunchKernelGGL((mx4_panels_kernel<1, false>), grid, block, 0, s, p, job, (int)chunks, np, token);
+    else if (sliced) hipLaunchKernelGGL((mx4_panels_kernel<4, true>), grid, block, 0, s, p, job, (int)chunks, np, token);
+    else hipLaunchKernelGGL((mx4_panels_kernel<4, false>), grid, block, 0, s, p, job, (int)chunks, np, token);
     return hipGetLastError();
 }
 

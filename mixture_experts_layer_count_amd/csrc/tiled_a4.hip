@@ -47,9 +47,6 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-#ifndef A4_WC
-#define A4_WC 4
-#endif
 constexpr int kA4BK = 128;    // K per step
 constexpr int kA4Items = 64;  // work items per workgroup at most (LDS table)
 
@@ -64,8 +61,7 @@ struct RingA4 {
     static constexpr int sb_bytes = 4 * 256;
     static constexpr int sb_at = a_bytes + b_bytes + sa_bytes;
     static constexpr int stage = sb_at + sb_bytes;
-    static constexpr int per_cu = 1;  // workgroups a CU
-    static constexpr int budget = 160 * 1024 / per_cu - kA4Items * 16;
+    static constexpr int budget = 160 * 1024 - kA4Items * 32 - 16;
     static constexpr int S = budget / stage < 6 ? budget / stage : 6;
     static constexpr int a_chunks = a_bytes / 1024;  // 1 KB copies, 16 rows each
     static constexpr int nA = (a_chunks + waves - 1) / waves;
@@ -74,18 +70,22 @@ struct RingA4 {
     static constexpr int nS = (slots + waves - 1) / waves;
     static constexpr int per_step = nA + nB + nS;
     static constexpr int table = S * stage;
-    static constexpr int lds = table + kA4Items * 16;
+    static constexpr int flag = table + kA4Items * 32;
+    static constexpr int lds = flag + 16;
     static_assert(S >= 3 && BM % 64 == 0 && (S - 2) * per_step < 64, "ring");
 };
 
-// Parts that each item of an XCD's last round is split into (1: none), when the
-// fullest XCDs, with `per` items, leave at least half of its workgroups idle
-// there; a part has at least kA4PartSteps steps.
+// Equal parts over K that each item of an XCD's last round of workgroups is cut into
+// (1: none), where it leaves half of them idle: one round of parts, of at least
+// kA4PartSteps steps. 8 experts, 8192 rows, K 14336 (2.25 rounds): 321 to 288 us.
+// Cutting the last two rounds' steps into equal ranges instead, with two parts
+// an item, took 312: the card's clock falls with the matrix cores' load, so a
+// round on part of the chip costs less than its length.
 constexpr int kA4Parts = 4, kA4PartSteps = 4;
-__device__ __forceinline__ int tail_parts(int per, int slots, int nk) {
-    const int tail = per % slots;
-    if (tail == 0) return 1;
-    return max(min(min(kA4Parts, kBlocksPerXcd / tail), nk / kA4PartSteps), 1);
+__device__ __forceinline__ int tail_parts(int n, int slots, int nk) {
+    const int tail = n % slots;
+    if (tail == 0 || slots > kBlocksPerXcd) return 1;
+    return max(min(min(kA4Parts, slots / tail), nk / kA4PartSteps), 1);
 }
 
 // What steers the K loop is kept in scalar registers: a count that went through a
@@ -100,6 +100,8 @@ __device__ __forceinline__ f32x16 mfma4(const i32x4 &b, const i32x4 &a, const f3
 }
 struct ItemA4 {
     int g, row0, row_end, n0;
+    int k0, k1;  // steps
+    int cut;     // whether a part of its tile
 };
 
 template <bool SWIGLU, int WR, int WC, int MI>
@@ -122,23 +124,19 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
     const int xcd = blockIdx.x % kXcds, slot = blockIdx.x / kXcds, slots = gridDim.x / kXcds;
     const int mine = min(per, n_work - xcd * per);
     if (mine <= 0) return;
-    // full rounds, then (split) one part of an item of the last one
-    const int split = scalar(tail_parts(per, slots, nk));
-    const int tail = split > 1 ? scalar(mine % slots) : 0, full = mine - tail;
-    int count = slot < full ? scalar((full - slot + slots - 1) / slots) : 0;
-    int part = 0, parts = 1;  // of the last item
-    if (slot < tail * split) {
-        parts = split;
-        part = scalar(slot % split);
-        ++count;
-    }
+    // full rounds of whole items, then one part of an item of the last round
+    const int parts = scalar(tail_parts(mine, slots, nk)), part = scalar(slot % parts);
+    const int tail = parts > 1 ? scalar(mine % slots) : 0, full = mine - tail;
+    const int whole = slot < full ? scalar((full - slot + slots - 1) / slots) : 0;
+    int count = whole + (slot < tail * parts ? 1 : 0);
     if (count == 0) return;
     if (MOE_BOUNDS_FAIL(count <= kA4Items, BOUNDS_TILE)) return;
-    const int last_k0 = scalar(part * nk / parts), last_k1 = scalar((part + 1) * nk / parts);  // its steps
     if (w == 0 && lane < count) {
         int mt, nt;
-        const bool cut = parts > 1 && lane == count - 1;
-        tile_of(p, nN, n_tiles, xcd * per + (cut ? full + slot / split : slot + slots * lane), mt, nt);
+        const int cut = lane >= whole;
+        const int item = cut ? full + slot / parts : slot + slots * lane;
+        const int k0 = cut ? part * nk / parts : 0, k1 = cut ? (part + 1) * nk / parts : nk;
+        tile_of(p, nN, n_tiles, xcd * per + item, mt, nt);
         const bool ok = mt < p.max_tiles;
         int g = ok ? p.tiles[4 * mt] : 0, r0 = ok ? p.tiles[4 * mt + 1] : 0, r1 = ok ? p.tiles[4 * mt + 2] : 0;
         if (MOE_BOUNDS_FAIL(ok && g >= 0 && g < p.n_groups && r0 >= 0 && r0 < r1 && r1 <= p.M, BOUNDS_TILE)) {
@@ -146,18 +144,16 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
             r0 = 0;
             r1 = 1;
         }
-        *reinterpret_cast<i32x4 *>(table + 4 * lane) = i32x4{g, r0, r1, nt * W};
+        i32x4 *rec = reinterpret_cast<i32x4 *>(table + 8 * lane);
+        rec[0] = i32x4{g, r0, r1, nt * W};
+        rec[1] = i32x4{k0, k1, cut, 0};
     }
     __syncthreads();
     count = scalar(count);
     auto item_at = [&](int j) {
-        const i32x4 t = *reinterpret_cast<const i32x4 *>(table + 4 * j);
-        ItemA4 it;
-        it.g = __builtin_amdgcn_readfirstlane(t[0]);
-        it.row0 = __builtin_amdgcn_readfirstlane(t[1]);
-        it.row_end = __builtin_amdgcn_readfirstlane(t[2]);
-        it.n0 = __builtin_amdgcn_readfirstlane(t[3]);
-        return it;
+        const i32x4 *rec = reinterpret_cast<const i32x4 *>(table + 8 * j);
+        const i32x4 t = rec[0], u = rec[1];
+        return ItemA4{scalar(t[0]), scalar(t[1]), scalar(t[2]), scalar(t[3]), scalar(u[0]), scalar(u[1]), scalar(u[2])};
     };
 
     // ---- copies: a uniform base that moves on each step, and a lane's offset.
@@ -177,7 +173,8 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
     // byte rows and K groups of the last step that the weights have
     const int k_rows = p.K / 2 - 64 * (nk - 1), k_groups = p.K / 32 - 4 * (nk - 1);
     const bool ragged = p.K % kA4BK != 0;
-    auto set_sources = [&](const ItemA4 &it, int kt) {
+    auto set_sources = [&](const ItemA4 &it) {
+        const int kt = it.k0;
         int ln = lane;  // re-read: its multiples need not live through the K loop
         asm volatile("" : "+v"(ln));
         const bool extra = it.g == p.extra_group;
@@ -216,10 +213,10 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
 #pragma unroll
     for (int q = 0; q < R::nS; ++q) s_step[q] = s_slot(q) < R::BM / 64 ? p.as_ld * 4 : 4LL * p.N;
     auto begin_item = [&]() {
-        const bool cut = c_item == count - 1;
-        c_kt = cut ? last_k0 : 0;
-        c_left = (cut ? last_k1 : nk) - c_kt;
-        set_sources(item_at(c_item), c_kt);
+        const ItemA4 it = item_at(c_item);
+        c_kt = it.k0;
+        c_left = it.k1 - it.k0;
+        set_sources(it);
     };
     auto move = [&](long long by) {
         a_base += by * a_step;
@@ -363,7 +360,7 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
     // h in MXFP4: a lane holds half of a row's 32 columns, lane ^ 32 the rest.
     // Of two row blocks the lower lanes store the first's rows, the upper ones
     // the second's: 16 bytes of codes and a scale byte a lane
-    auto gate_up_out = [&](const ItemA4 &it) {
+    auto gate_up_out = [&](const ItemA4 &it, auto sums) {
         int ln = lane;
         asm volatile("" : "+v"(ln));
         const long long at = (long long)(it.n0 >> 7) * p.cqs_ld + it.row0;
@@ -385,7 +382,7 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
                         byte[u] = byte[0];
                         continue;
                     }
-                    const f32x16 &g = acc[m + u][j], &x = acc[m + u][j + NJ / 2];
+                    const f32x16 g = sums(m + u, j), x = sums(m + u, j + NJ / 2);
                     float v[16];
                     uint32_t t = 0;
 #pragma unroll
@@ -422,7 +419,7 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
     };
     // bf16 rows: of two 8-column pieces the lower lanes store the first, the
     // upper ones the second
-    auto down_out = [&](const ItemA4 &it) {
+    auto down_out = [&](const ItemA4 &it, auto sums) {
         int ln = lane;
         asm volatile("" : "+v"(ln));
         const int rows = it.row_end - it.row0, ld = p.ldc;
@@ -431,10 +428,10 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
         for (int m = 0; m < MI; ++m) {
             const int row = wr * 32 * MI + 32 * m + (ln & 31);  // of the tile
 #pragma unroll
-            for (int j = 0; j < NJ; ++j)
+            for (int j = 0; j < NJ; ++j) {
+                const f32x16 x = sums(m, j);
 #pragma unroll
                 for (int q = 0; q < 4; q += 2) {
-                    const f32x16 &x = acc[m][j];
                     uint32_t a0 = pack_bf16x2(x[4 * q], x[4 * q + 1]), a1 = pack_bf16x2(x[4 * q + 2], x[4 * q + 3]);
                     uint32_t b0 = pack_bf16x2(x[4 * q + 4], x[4 * q + 5]),
                              b1 = pack_bf16x2(x[4 * q + 6], x[4 * q + 7]);
@@ -445,63 +442,85 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
                     __builtin_amdgcn_raw_buffer_store_b128(u32x4{a0, a1, b0, b1}, C,
                                                                in ? (row * ld + col) * 2 : kNowhere, 0, 0);
                 }
+            }
         }
     };
 
     constexpr int ST = SWIGLU ? NJ * ((MI + 1) / 2) : 2 * NJ * MI;  // stores of a tile
-    auto tile_out = [&](const ItemA4 &it) {
-        if constexpr (SWIGLU) gate_up_out(it);
-        else down_out(it);
+    // sums(m, j): the block's fp32 sums
+    auto tile_out = [&](const ItemA4 &it, auto sums) {
+        if constexpr (SWIGLU) gate_up_out(it, sums);
+        else down_out(it, sums);
     };
-    // One part of a split item: its fp32 sums go to its slot; the workgroup that
-    // finds itself the last adds the parts in their order, all read back from
-    // memory, so the sum does not depend on which is last. One thread makes the
-    // stores visible beyond this XCD's L2 and counts the part (the counter is left
-    // at zero); its one acquire serves the workgroup after the barrier.
-    auto join_parts = [&]() -> bool {
-        const int first = xcd * kBlocksPerXcd + (slot - part), cnt = xcd * kBlocksPerXcd + slot / parts;
-        if (MOE_BOUNDS_FAIL(first >= 0 && first + parts <= kTailSlots, BOUNDS_TAIL_SLOT)) return false;
-        constexpr int NV = MI * NJ * 4;
-        f32x4 *buf = reinterpret_cast<f32x4 *>(p.tail_part) + (long long)first * NV * R::threads;
-        f32x4 *mine_at = buf + (long long)part * NV * R::threads;
+    // ---- an item in parts. Sums pass through memory as [accumulator][thread] vectors;
+    // one thread makes them visible beyond this XCD's L2 (a release), or takes what
+    // was made so (an acquire, which serves the workgroup after the barrier) ----
+    constexpr int NV = MI * NJ * 4;
+    int *flag = reinterpret_cast<int *>(lds + R::flag);
+    constexpr int kSums = NV * R::threads * 16;  // bytes of a tile's sums
+    auto sums_of = [&](int i) { return rsrc(reinterpret_cast<uint8_t *>(p.tail_part) + (long long)i * kSums, kSums); };
+    auto store_sums = [&](int i) {
+        const auto to = sums_of(i);
 #pragma unroll
         for (int m = 0; m < MI; ++m)
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    mine_at[((m * NJ + j) * 4 + q) * R::threads + tid] =
-                        f32x4{acc[m][j][4 * q], acc[m][j][4 * q + 1], acc[m][j][4 * q + 2], acc[m][j][4 * q + 3]};
+                for (int q = 0; q < 4; ++q) {
+                    const f32x16 &x = acc[m][j];
+                    __builtin_amdgcn_raw_buffer_store_b128(
+                        __builtin_bit_cast(u32x4, f32x4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]}), to,
+                        tid * 16, ((m * NJ + j) * 4 + q) * R::threads * 16, 0);
+                }
         wait_vm<0>();
         __syncthreads();
-        int *is_last = reinterpret_cast<int *>(lds);  // the ring is idle
+    };
+    auto stored = [&](const auto &from, int m, int j) {
+        f32x16 x;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const f32x4 v = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                          from, tid * 16, ((m * NJ + j) * 4 + q) * R::threads * 16, 0));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[4 * q + e] = v[e];
+        }
+        return x;
+    };
+    // Each part leaves its sums; the workgroup that finds itself the last
+    // adds them in the parts' order, all read back from memory, so that the sum does
+    // not depend on which is last, and leaves the counter at 0. (The accumulators are
+    // only read here: written on such a path, they spill.)
+    auto join = [&](const ItemA4 &it) {
+        const int first = xcd * kBlocksPerXcd + slot - part, i = xcd * kBlocksPerXcd + slot / parts;
+        if (MOE_BOUNDS_FAIL(first >= 0 && first + parts <= kTailSlots, BOUNDS_TAIL_SLOT)) return;
+        store_sums(first + part);
         if (tid == 0) {
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-            const bool last = __hip_atomic_fetch_add(p.tail_cnt + cnt, 1, __ATOMIC_RELAXED,
+            const bool last = __hip_atomic_fetch_add(p.tail_cnt + i, 1, __ATOMIC_RELAXED,
                                                      __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
             if (last) {
                 __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-                __hip_atomic_store(p.tail_cnt + cnt, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                __hip_atomic_store(p.tail_cnt + i, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             }
-            *is_last = last;
+            *flag = last;
         }
         __syncthreads();
-        if (!*is_last) return false;
-        clear();
-        for (int q = 0; q < parts; ++q) {
-            const f32x4 *from = buf + (long long)q * NV * R::threads;
+        if (!*flag) return;
+        static_assert(kA4Parts == 4, "parts");
+        const auto s0 = sums_of(first), s1 = sums_of(first + 1), s2 = sums_of(first + min(2, parts - 1)),
+                   s3 = sums_of(first + min(3, parts - 1));
+        tile_out(it, [&](int m, int j) {
+            __builtin_amdgcn_sched_barrier(0);  // few loads at a time: registers
+            f32x16 x = stored(s0, m, j) + stored(s1, m, j);
+            __builtin_amdgcn_sched_barrier(0);
+            const f32x16 c = stored(s2, m, j), d = stored(s3, m, j);
 #pragma unroll
-            for (int m = 0; m < MI; ++m)
-#pragma unroll
-                for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const f32x4 v = from[((m * NJ + j) * 4 + i) * R::threads + tid];
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) acc[m][j][4 * i + x] += v[x];
-                    }
-        }
-        return true;
+            for (int e = 0; e < 16; ++e) {
+                x[e] = parts > 2 ? x[e] + c[e] : x[e];
+                x[e] = parts > 3 ? x[e] + d[e] : x[e];
+            }
+            return x;
+        });
     };
 
     // ---- fill the ring, then the steps of every item ----
@@ -559,7 +578,8 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
     // Runs of steps up to the next event: the end of an item's copies, of its
     // products, or of the first steps after a stored tile, whose waits let its
     // stores (newer than the copies waited for) be under way
-    int j = 0, left = count == 1 ? last_k1 - last_k0 : nk, after = 0;
+    ItemA4 it = item_at(0);
+    int j = 0, left = it.k1 - it.k0, after = 0;
     for (;;) {
         int n = min(left, c_left);
         left -= n, c_left -= n;
@@ -571,29 +591,29 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
         for (int i = 0; i < n; ++i) step(H0{});
         if (c_left == 0) next_item();
         if (left == 0) {
-            if (j == count - 1) break;
-            tile_out(item_at(j));
-            clear();
-            ++j;
-            left = j == count - 1 ? last_k1 - last_k0 : nk;
+            const bool last = ++j == count;
+            if (last) wait_vm<0>();  // the repeated copies land before the workgroup ends
+            if (!it.cut) tile_out(it, [&](int m, int j) { return acc[m][j]; });
+            else join(it);
+            if (last) break;
             after = S - 2;
+            clear();
+            it = item_at(j);
+            left = it.k1 - it.k0;
         }
     }
-    wait_vm<0>();  // the repeated copies land before the workgroup ends
-    if (parts > 1 && !join_parts()) return;
-    tile_out(item_at(count - 1));
 }
 
 template <bool SWIGLU, int MI>
 hipError_t launch(const GemmProblem &p, hipStream_t s) {
-    constexpr int WR = 2, WC = A4_WC;
+    constexpr int WR = 2, WC = 4;
     typedef RingA4<WR, WC, MI> R;
     const int nN = (p.N + (SWIGLU ? 127 : 255)) / (SWIGLU ? 128 : 256);
     const long long items = ((long long)p.max_tiles * nN + kXcds - 1) / kXcds;  // of an XCD, at most
     if (items > 0x0fffffffLL) return hipErrorInvalidValue;
     // one round of resident workgroups, or as many as keep to the item table
-    long long slots = kBlocksPerXcd * R::per_cu;
-    while ((items + slots - 1) / slots > kA4Items) slots += kBlocksPerXcd * R::per_cu;
+    long long slots = kBlocksPerXcd;
+    while ((items + slots - 1) / slots > kA4Items) slots += kBlocksPerXcd;
     hipLaunchKernelGGL((tiled_a4_kernel<SWIGLU, WR, WC, MI>), dim3((unsigned)(slots * kXcds)), dim3(R::threads), 0, s, p, nN);
     return hipGetLastError();
 }
