@@ -81,7 +81,7 @@ struct RingA4 {
 // Cutting the last two rounds' steps into equal ranges instead, with two parts
 // an item, took 312: the card's clock falls with the matrix cores' load, so a
 // round on part of the chip costs less than its length.
-constexpr int kA4Parts = 4, kA4PartSteps = 4;
+constexpr int kA4Parts = 4, kA4PartSteps = 12;
 __device__ __forceinline__ int tail_parts(int n, int slots, int nk) {
     const int tail = n % slots;
     if (tail == 0 || slots > kBlocksPerXcd) return 1;
@@ -417,30 +417,41 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
             }
         }
     };
-    // bf16 rows: of two 8-column pieces the lower lanes store the first, the
-    // upper ones the second
+    // bf16 rows: a lane holds 4-column pieces of its row, lane ^ 32 the ones between.
+    // Exchanges between the wavefront's halves and quarters leave 8 columns a lane
+    // and the four lanes l, l + 16, .. with a row's 32: 64 bytes of 16 rows a store
     auto down_out = [&](const ItemA4 &it, auto sums) {
         int ln = lane;
         asm volatile("" : "+v"(ln));
         const int rows = it.row_end - it.row0, ld = p.ldc;
         const auto C = rsrc(reinterpret_cast<uint16_t *>(p.C) + (long long)it.row0 * ld + it.n0, (rows * ld - it.n0) * 2);
+        const int piece = 8 * ((ln >> 5) | ((ln >> 3) & 2));  // column of the lane's piece
 #pragma unroll
         for (int m = 0; m < MI; ++m) {
-            const int row = wr * 32 * MI + 32 * m + (ln & 31);  // of the tile
+            const int row = wr * 32 * MI + 32 * m + (ln & 15);  // of the tile
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
                 const f32x16 x = sums(m, j);
+                uint32_t v[2][4];  // columns 0..7 or 8..15 (upper lanes), and 16 more
 #pragma unroll
-                for (int q = 0; q < 4; q += 2) {
-                    uint32_t a0 = pack_bf16x2(x[4 * q], x[4 * q + 1]), a1 = pack_bf16x2(x[4 * q + 2], x[4 * q + 3]);
-                    uint32_t b0 = pack_bf16x2(x[4 * q + 4], x[4 * q + 5]),
-                             b1 = pack_bf16x2(x[4 * q + 6], x[4 * q + 7]);
-                    swap32(a0, b0);
-                    swap32(a1, b1);
-                    const int col = 32 * (NJ * wc + j) + 8 * (q + (ln >> 5));
-                    const bool in = row < rows && it.n0 + col < p.N;
-                    __builtin_amdgcn_raw_buffer_store_b128(u32x4{a0, a1, b0, b1}, C,
-                                                               in ? (row * ld + col) * 2 : kNowhere, 0, 0);
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[h][e] = pack_bf16x2(x[8 * h + 2 * e], x[8 * h + 2 * e + 1]);
+                    swap32(v[h][0], v[h][2]);
+                    swap32(v[h][1], v[h][3]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {  // rows 16..31's first pieces against rows 0..15's second
+                    const auto r = __builtin_amdgcn_permlane16_swap(v[0][e], v[1][e], false, false);
+                    v[0][e] = r[0];
+                    v[1][e] = r[1];
+                }
+                const int col = 32 * (NJ * wc + j) + piece;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const bool in = row + 16 * h < rows && it.n0 + col < p.N;
+                    __builtin_amdgcn_raw_buffer_store_b128(u32x4{v[h][0], v[h][1], v[h][2], v[h][3]}, C,
+                                                           in ? ((row + 16 * h) * ld + col) * 2 : kNowhere, 0, 0);
                 }
             }
         }
@@ -509,16 +520,21 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
         static_assert(kA4Parts == 4, "parts");
         const auto s0 = sums_of(first), s1 = sums_of(first + 1), s2 = sums_of(first + min(2, parts - 1)),
                    s3 = sums_of(first + min(3, parts - 1));
+        if (parts == 2) {
+            tile_out(it, [&](int m, int j) {
+                __builtin_amdgcn_sched_barrier(0);  // few loads at a time: registers
+                return stored(s0, m, j) + stored(s1, m, j);
+            });
+            return;
+        }
         tile_out(it, [&](int m, int j) {
-            __builtin_amdgcn_sched_barrier(0);  // few loads at a time: registers
+            __builtin_amdgcn_sched_barrier(0);
             f32x16 x = stored(s0, m, j) + stored(s1, m, j);
             __builtin_amdgcn_sched_barrier(0);
             const f32x16 c = stored(s2, m, j), d = stored(s3, m, j);
+            x += c;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                x[e] = parts > 2 ? x[e] + c[e] : x[e];
-                x[e] = parts > 3 ? x[e] + d[e] : x[e];
-            }
+            for (int e = 0; e < 16; ++e) x[e] = parts > 3 ? x[e] + d[e] : x[e];
             return x;
         });
     };
