@@ -249,6 +249,13 @@ def grouped_ffn(Xin, offsets, W1, W3, W2, S1=None, S3=None, S2=None, row_src=Non
     else:
         Yp = out
     p = PATHS[path]
+    if path == "tiled_a4" and wdt == MOE_MXFP4:
+        for t, n, shape in ((W3, "W3", W1.shape), (W2, "W2", (G, F // 2, H)), (S1, "S1", (G, H // 32, F)),
+                            (S3, "S3", (G, H // 32, F)), (S2, "S2", (G, F // 32, H))):
+            _want(t, n, shape, torch.uint8, Xin.device)
+        _want(offsets, "offsets", (G + 1,), torch.int32, Xin.device)
+        if Xin.dim() != 2 or Xin.shape[1] != H or (Xin.shape[0] if row_src is None else row_src.numel()) < M:
+            raise ValueError("Xin must be [T, H], and row_src (without one, Xin) must have M rows")
     nbytes = lib().moe_grouped_ffn_workspace_bytes(M, G, H, F, adt, wdt, p)
     ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=Xin.device)
     _call("moe_grouped_ffn", Xin.device, _ptr(Xin), _ptr(row_src), k, M, _ptr(offsets), G, H, F, _ptr(W1), _ptr(W3),

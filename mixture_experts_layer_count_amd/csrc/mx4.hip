@@ -8,7 +8,6 @@
 
 namespace moe {
 
-MOE_BOUNDS_FILE(mx4)
 namespace {
 
 using namespace mx4;

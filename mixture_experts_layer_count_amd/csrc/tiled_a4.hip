@@ -208,7 +208,7 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
         }
     };
     // what the next copies are of: step c_kt of item c_item, c_left steps before the next item
-    int c_item = 0, c_kt, c_left;
+    int c_item = 0, c_kt, c_left, c_step = 1;
     long long a_step = p.as_ld * 64, b_step = 64LL * p.N, s_step[R::nS];
 #pragma unroll
     for (int q = 0; q < R::nS; ++q) s_step[q] = s_slot(q) < R::BM / 64 ? p.as_ld * 4 : 4LL * p.N;
@@ -224,7 +224,7 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
         b_base[1] += by * b_step;
 #pragma unroll
         for (int q = 0; q < R::nS; ++q) s_base[q] += by * s_step[q];
-        c_kt += (int)by;
+        c_kt += (int)by * c_step;
     };
     // after an item's last step: the next item; past the last one its last step's
     // copies are repeated (into stages that nobody reads)
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
             begin_item();
         } else {
             move(-1);
-            a_step = b_step = 0;
+            a_step = b_step = c_step = 0;
 #pragma unroll
             for (int q = 0; q < R::nS; ++q) s_step[q] = 0;
             c_left = 0x7fffffff;
@@ -242,6 +242,7 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
     };
     auto copy = [&](int q, int stage) {
         uint8_t *st = lds + stage * R::stage;
+        if (MOE_BOUNDS_FAIL(c_kt >= 0 && c_kt < nk, BOUNDS_TILE)) c_kt = nk - 1;
         const bool last = ragged && c_kt == nk - 1;
         if (q < R::nA) {
             copy16(a_base + (a_off + 1024u * (uint32_t)a_chunk(q)), st + a_chunk(q) * 1024);

@@ -16,7 +16,9 @@ on the memory paradox (the gate runs a linear projection and a softmax over all
 experts); the page "MoE-推理部署" (zzmblog.top), section on expert quantisation
 (per-expert FP8 scales; MXFP4 as a single-GPU weight format). oracle.ep follows
 "MOE推理流程解析" §五 (expert-parallel dispatch and combine). oracle.train holds
-the training operators, from their own formulas.
+the training operators, oracle.dispatch the gradients of the sorted rows and of
+the weighted sum, oracle.mx4 the 4-bit format and the FFN in it, from their own
+formulas.
 
 Parity pins: see the functions' docstrings and tests/test_oracle_*.py. The
 whole-layer output at model scale has no printed values on the pages; it is
@@ -30,11 +32,11 @@ from .ref import (
     Layer, forward, forward_tokens,
 )
 from .brute import brute_force_forward
-from . import ep, train
+from . import dispatch, ep, mx4, train
 
 __all__ = [
     "to_f64", "e4m3_decode", "e4m3_encode", "quantize_rows_e4m3", "dequant_rows", "round_bf16", "dequant_blocks", "router_logits", "softmax",
     "select_topk", "route", "routing_weights", "permute", "silu", "swiglu_ffn",
     "grouped_ffn", "combine", "Layer", "forward", "forward_tokens",
-    "brute_force_forward", "ep", "train",
+    "brute_force_forward", "dispatch", "ep", "mx4", "train",
 ]

@@ -1,0 +1,270 @@
+"""GPU: the gradients of the sorted rows and of the weighted sum back, against the
+fp64 oracle (oracle/dispatch.py) and torch's autograd in fp64, and a training step
+around 4-bit experts.
+
+Bounds: u = 2^-24 for each fp32 operation of a sum (its length times the sum of
+magnitudes), half a step for the rounding of an output (bf16 2^-8, fp32 2^-24)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_count_amd as moe
+from mixture_experts_layer_count_amd import _lib
+from oracle import dispatch, mx4
+from _gpu import say
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: U}
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    moe.lib()
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _case(T, E, k, H, dt, seed):
+    g = torch.Generator().manual_seed(seed)
+    w, idx = torch.topk(torch.randn(T, E, generator=g), k, dim=1)
+    _, off, src, back, _ = moe.permute(idx.int().cuda(), E)
+    rows = lambda n: torch.randn(n, H, generator=g).to(dt).cuda()  # noqa: E731
+    return {"dY": rows(T), "Yp": rows(T * k), "w": torch.softmax(w, 1).cuda(), "assign_row": back, "row_src": src,
+            "offsets": off, "k": k, "idx": idx}
+
+
+def _check(d, got, dX, add, n=None):
+    dYp, dw = got
+    k, dt = d["k"], d["dY"].dtype
+    ref, rdw = dispatch.combine_backward(f64(d["dY"]), f64(d["Yp"]), d["assign_row"].cpu().numpy(), f64(d["w"]), n)
+    live = ~np.isnan(ref).any(axis=1)
+    out = f64(dYp)[live]
+    assert (np.abs(out - ref[live]) <= (HALF[dt] + U) * np.abs(ref[live]) + 1e-40).all()
+    _, mag = dispatch.combine_backward(np.abs(f64(d["dY"])), np.abs(f64(d["Yp"])), d["assign_row"].cpu().numpy(), f64(d["w"]), n)
+    assert (np.abs(f64(dw) - rdw) <= (d["dY"].shape[1] + 8) * U * mag).all()
+    r = dispatch.permute_backward(f64(d["Yp"]), d["assign_row"].cpu().numpy(), k, None if add is None else f64(add), n)
+    m = dispatch.permute_backward(np.abs(f64(d["Yp"])), d["assign_row"].cpu().numpy(), k, None if add is None else np.abs(f64(add)), n)
+    tol = (k + 1) * U * m
+    assert (np.abs(f64(dX) - r) <= tol + HALF[dt] * (np.abs(r) + tol) + 1e-40).all()
+
+
+@pytest.mark.parametrize("T,E,k,H,dt", [(1, 1, 1, 4, BF), (1, 8, 2, 4096, BF), (7, 4, 3, 12, BF), (7, 4, 3, 12, F32),
+                                        (33, 8, 2, 520, BF), (64, 8, 8, 516, BF), (100, 16, 5, 1028, F32), (300, 12, 4, 2048, BF),
+                                        (129, 64, 8, 7168, BF), (65, 128, 64, 64, BF), (40, 60, 7, 9000, F32), (9, 4, 2, 20480, BF),
+                                        (5, 4, 2, 16, BF), (2000, 256, 8, 72, F32)])
+def test_gradients(T, E, k, H, dt):
+    say(f"[dispatch] T={T} E={E} k={k} H={H} {dt}")
+    d = _case(T, E, k, H, dt, T + H)
+    got = moe.combine_backward(d["dY"], d["Yp"], d["assign_row"], d["w"])
+    for add in (None, d["dY"]):
+        dX = moe.permute_backward(d["Yp"], d["assign_row"], k, dX_add=add)
+        _check(d, got, dX, add)
+    # one of the two alone
+    a, none = moe.combine_backward(d["dY"], None, d["assign_row"], d["w"], need=("dYp",))
+    assert none is None and torch.equal(a, got[0])
+    none, b = moe.combine_backward(d["dY"], d["Yp"], d["assign_row"], d["w"], need=("dtopk_w",))
+    assert none is None and torch.equal(b, got[1])
+
+
+def test_against_autograd():
+    say("[dispatch] against autograd of the gather and the weighted sum")
+    T, E, k, H = 50, 6, 3, 64
+    d = _case(T, E, k, H, F32, 3)
+    X = torch.randn(T, H, dtype=torch.float64, requires_grad=True)
+    w = d["w"].double().cpu().requires_grad_()
+    src, back = d["row_src"].long().cpu(), d["assign_row"].long().cpu()
+    Xp = X[src // k]
+    Xp.retain_grad()
+    Yp = torch.tanh(Xp)                                # an expert of another form
+    Yp.retain_grad()
+    Y = (w.reshape(-1, 1) * Yp[back]).reshape(T, k, H).sum(1)
+    (Y * d["dY"].double().cpu()).sum().backward()
+    Xd = X.detach().float().cuda()
+    _, _, _, _, Xpd = moe.permute(d["idx"].int().cuda(), E, Xd)
+    Ypd = torch.tanh(Xpd)
+    dYp, dw = moe.combine_backward(d["dY"], Ypd, d["assign_row"], d["w"])
+    dX = moe.permute_backward(dYp * (1 - Ypd * Ypd), d["assign_row"], k)
+    for got, ref in ((dYp, Yp.grad), (dw, w.grad), (dX, X.grad)):
+        assert (got.double().cpu() - ref).abs().max() <= 1e-5 * ref.abs().max()
+
+
+def test_left_out_picks():
+    say("[dispatch] picks that were left out, and rows that nothing names")
+    T, k, H = 37, 3, 136
+    d = _case(T, 8, k, H, BF, 5)
+    n = int(d["offsets"][5])
+    M = T * k
+    n_rows = d["offsets"][5:6].clone()
+    back = d["assign_row"].clone()
+    back[back == 4] = -1                               # row 4 is named by nothing
+    back[back == 9] = 0x7fffffff
+    d["assign_row"] = back
+    for rows, count in ((n_rows, n), (None, None)):
+        got = moe.combine_backward(d["dY"], d["Yp"], back, d["w"], n_rows=rows)
+        dX = moe.permute_backward(d["Yp"], back, k, dX_add=d["dY"], n_rows=rows)
+        _check(d, got, dX, d["dY"], count)
+    # rows that are not named stay as they were
+    lib, ptr = moe.lib(), lambda t: ctypes.c_void_p(t.data_ptr())
+    out = torch.full((M, H), 7.0, dtype=BF, device="cuda")
+    dw = torch.empty(T, k, device="cuda")
+    assert lib.moe_combine_backward(ptr(d["dY"]), ptr(d["Yp"]), ptr(back), ptr(d["w"]), ptr(n_rows), T, k, H, 1, ptr(out),
+                                    ptr(dw), _lib._stream()) == 0
+    named = torch.zeros(M, dtype=torch.bool, device="cuda")
+    live = back[(back >= 0) & (back < n)].long()
+    named[live] = True
+    assert (out[~named] == 7).all() and not (out[named] == 7).all(1).any()
+    # every pick left out
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert not moe.combine_backward(d["dY"], d["Yp"], back, d["w"], n_rows=zero)[1].any()
+    assert torch.equal(moe.permute_backward(d["Yp"], back, k, dX_add=d["dY"], n_rows=zero), d["dY"])
+    assert not moe.permute_backward(d["Yp"], back, k, n_rows=zero).any()
+
+
+def test_in_place_and_empty():
+    say("[dispatch] dX over dX_add, dYp over Yp; no tokens")
+    T, k, H = 70, 2, 1040
+    d = _case(T, 4, k, H, BF, 8)
+    lib, ptr = moe.lib(), lambda t: ctypes.c_void_p(t.data_ptr())
+    dYp, dw = moe.combine_backward(d["dY"], d["Yp"], d["assign_row"], d["w"])
+    dX = moe.permute_backward(d["Yp"], d["assign_row"], k, dX_add=d["dY"])
+    buf, dw2, x = d["Yp"].clone(), torch.empty_like(dw), d["dY"].clone()
+    assert lib.moe_combine_backward(ptr(d["dY"]), ptr(buf), ptr(d["assign_row"]), ptr(d["w"]), None, T, k, H, 1, ptr(buf),
+                                    ptr(dw2), _lib._stream()) == 0
+    assert lib.moe_permute_backward(ptr(d["Yp"]), ptr(d["assign_row"]), None, T, k, H, 1, ptr(x), ptr(x), _lib._stream()) == 0
+    assert torch.equal(buf, dYp) and torch.equal(dw2, dw) and torch.equal(x, dX)
+    none = [t[:0] for t in (d["dY"], d["Yp"], d["assign_row"], d["w"])]
+    a, b = moe.combine_backward(*none)
+    assert a.shape == (0, H) and b.shape == (0, k) and moe.permute_backward(none[1], none[2], k).shape == (0, H)
+
+
+def test_nan_stays_in_its_token():
+    say("[dispatch] NaN and infinity reach their token and rows only")
+    d = _case(60, 8, 2, 200, F32, 9)
+    clean = moe.combine_backward(d["dY"], d["Yp"], d["assign_row"], d["w"])
+    cleanX = moe.permute_backward(d["Yp"], d["assign_row"], 2)
+    dY, Yp = d["dY"].clone(), d["Yp"].clone()
+    dY[7, 3] = float("nan")
+    Yp[11, 0] = float("inf")
+    dYp, dw = moe.combine_backward(dY, Yp, d["assign_row"], d["w"])
+    rows = d["assign_row"].long().view(60, 2)
+    assert torch.isnan(dw[7]).all() and torch.isnan(dYp[rows[7], 3]).all()
+    t = int((rows == 11).any(1).nonzero())
+    other = torch.tensor([i for i in range(60) if i not in (7, t)])
+    assert torch.equal(dw[other], clean[1][other]) and torch.equal(dYp[rows[other].view(-1)], clean[0][rows[other].view(-1)])
+    dX = moe.permute_backward(Yp, d["assign_row"], 2)
+    assert torch.isinf(dX[t, 0]) and torch.equal(dX[other], cleanX[other])
+
+
+def test_past_32_bits():
+    say("[dispatch] rows past 2^32 values")
+    T, k, H, E = 70000, 8, 8192, 16
+    g = torch.Generator(device="cuda").manual_seed(1)
+    idx = torch.topk(torch.rand(T, E, generator=g, device="cuda"), k, dim=1)[1].int()
+    _, _, src, back, _ = moe.permute(idx, E)
+    dY = torch.empty(T, H, dtype=BF, device="cuda").normal_(generator=g)
+    Yp = torch.empty(T * k, H, dtype=BF, device="cuda").normal_(generator=g)
+    w = torch.rand(T, k, generator=g, device="cuda")
+    dYp, dw = moe.combine_backward(dY, Yp, back, w)
+    dX = moe.permute_backward(Yp, back, k)
+    t = torch.tensor([0, T // 2, T - 1], device="cuda")
+    r = back.long().view(T, k)[t]
+    assert int(back.view(-1).max()) * H > 1 << 32
+    assert torch.equal(dYp[r.view(-1)].view(3, k, H), (w[t].unsqueeze(2) * dY[t].float().unsqueeze(1)).bfloat16())
+    ref = (Yp[r.view(-1)].double().view(3, k, H) * dY[t].double().unsqueeze(1))
+    assert ((dw[t] - ref.sum(2)).abs() <= H * U * ref.abs().sum(2)).all()
+    s = Yp[r.view(-1)].double().view(3, k, H)
+    assert ((dX[t].double() - s.sum(1)).abs() <= 2.0 ** -8 * s.sum(1).abs() + 2 * k * U * s.abs().sum(1)).all()
+
+
+def test_captured_and_two_streams():
+    say("[dispatch] captured and replayed; two streams")
+    d = _case(333, 16, 4, 776, BF, 12)
+    run = lambda: [*moe.combine_backward(d["dY"], d["Yp"], d["assign_row"], d["w"]),  # noqa: E731
+                   moe.permute_backward(d["Yp"], d["assign_row"], 4, dX_add=d["dY"])]
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = run()
+    for seed in range(3):
+        d["dY"].copy_(torch.randn(333, 776, generator=torch.Generator().manual_seed(seed)))
+        want = run()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+        torch.randn(1 << 20, device="cuda").sum().item()
+    want = run()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(run())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for o in got for a, b in zip(o, want))
+
+
+def test_training_step_around_frozen_4_bit_experts():
+    """Experts quantised from bf16 masters; forward in 4 bits; backward through the
+    values that the codes stand for (the roundings passed straight through), with the
+    dispatch's own gradients. Against the same in fp64."""
+    say("[dispatch] a step around frozen 4-bit experts")
+    T, H, F, E, k = 256, 256, 160, 8, 2
+    g = torch.Generator(device="cuda").manual_seed(6)
+    X = torch.randn(T, H, generator=g, device="cuda", dtype=BF)
+    Wg = (0.05 * torch.randn(H, E, generator=g, device="cuda")).to(BF)
+    packed = [moe.quantize_mxfp4_weights((0.06 * torch.randn(*s, generator=g, device="cuda")).to(BF))
+              for s in ((E, H, F), (E, H, F), (E, F, H))]
+    W1, W3, W2 = (moe.dequantize_mxfp4_weights(q, s) for q, s in packed)
+    dY = torch.randn(T, H, generator=g, device="cuda", dtype=BF)
+    # forward: the layer, and the same by its stages
+    logits, idx, w = moe.route(X, Wg, k)
+    _, off, src, back, Xp = moe.permute(idx, E, X)
+    (q1, s1), (q3, s3), (q2, s2) = packed
+    Yp = moe.grouped_ffn(Xp, off, q1, q3, q2, s1, s3, s2, path="tiled_a4")
+    Y = moe.combine(Yp, back, w)
+    d = {"Wg": Wg, "W1": q1, "W3": q3, "W2": q2, "S1": s1, "S3": s3, "S2": s2}
+    assert torch.equal(Y, moe.MoELayer(d, k, path="tiled_a4").forward(X))
+    # backward: combine's, the experts' on their values, the sorted rows', the router's
+    dYp, dw = moe.combine_backward(dY, Yp, back, w)
+    dXp = torch.empty_like(Xp)
+    offs = off.tolist()
+    for e, (lo, hi) in enumerate(zip(offs, offs[1:])):
+        xe = moe.dequantize_mxfp4_rows(*moe.quantize_mxfp4_rows(Xp[lo:hi])).float()
+        a, b = xe @ W1[e].float(), xe @ W3[e].float()
+        sg = torch.sigmoid(a)
+        dh = dYp[lo:hi].float() @ W2[e].float().T
+        dXp[lo:hi] = ((dh * b * sg * (1 + a * (1 - sg))) @ W1[e].float().T + (dh * a * sg) @ W3[e].float().T).to(BF)
+    dX = moe.permute_backward(dXp, back, k, dX_add=dY)       # and the residual's
+    dlogits = moe.route_backward(logits, idx, w, dw)
+    # the same in fp64, from the oracle's pieces
+    x, wn, dy = f64(X), f64(w), f64(dY)
+    tok = src.long().cpu().numpy() // k
+    xq = mx4.round_rows(x)[tok]
+    ref = {n: np.zeros((T * k, H)) for n in ("y", "dx")}
+    rdYp, _ = dispatch.combine_backward(dy, np.zeros((T * k, H)), back.cpu().numpy(), wn)
+    for e, (lo, hi) in enumerate(zip(offs, offs[1:])):
+        v1, v3, v2 = (mx4.weight_values(q[e].cpu().numpy(), s[e].cpu().numpy()) for q, s in packed)
+        ref["y"][lo:hi], a, b, _, _ = mx4.ffn(xq[lo:hi], v1, v3, v2)
+        sg, dh = 1 / (1 + np.exp(-a)), rdYp[lo:hi] @ v2.T
+        ref["dx"][lo:hi] = (dh * b * sg * (1 + a * (1 - sg))) @ v1.T + (dh * a * sg) @ v3.T
+    _, rdw = dispatch.combine_backward(dy, ref["y"], back.cpu().numpy(), wn)
+    rdX = dispatch.permute_backward(ref["dx"], back.cpu().numpy(), k, dy)
+    rdz = np.zeros((T, E))
+    np.put_along_axis(rdz, idx.long().cpu().numpy(), wn * (rdw - (wn * rdw).sum(1, keepdims=True)), axis=1)
+    for n, got, r in (("Y", Y, (wn[:, :, None] * ref["y"][back.long().cpu().numpy()].reshape(T, k, H)).sum(1)),
+                      ("dw", dw, rdw), ("dX", dX, rdX), ("dlogits", dlogits, rdz)):
+        err = np.linalg.norm(f64(got) - r) / np.linalg.norm(r)
+        say(f"    {n}: {err:.2e}")
+        # a few bf16 roundings one after the other (2^-8 each), in the 2-norm
+        assert err <= 4 * 2.0 ** -8, n
