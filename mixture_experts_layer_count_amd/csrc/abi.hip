@@ -128,6 +128,7 @@ struct FfnWs {
     uint8_t *x4, *h4;  // W4A4: panels of the expert inputs and of h, and their scale words
     uint32_t *x4s, *h4s;
     long long ld4;     // rows of a panel
+    int32_t *row_of4;  // the rows' places (moe_grouped_ffn)
     float *tail_part;  // tail split: partial sums and counters (or null)
     int32_t *tail_cnt;
 };
@@ -141,16 +142,19 @@ struct ExtraGroup {
 };
 
 // xrows: rows of quantised expert input (W8A8 only). W4A4: the rows of the
-// grouped launches are the first a4_rows; bf16 h is kept for the others only.
+// grouped launches are the first a4_rows; bf16 h is kept for the others only,
+// and the last product's rows and the map to a token's rows lie elsewhere for
+// one of moe_grouped_ffn and moe_forward each (layer: the latter).
 size_t ffn_ws_carve(Carver &c, FfnWs &w, const FfnPlan &p, int rows, int groups, int H, int hw,
-                    moe_dtype act_dt, int xrows, int a4_rows) {
+                    moe_dtype act_dt, int xrows, int a4_rows, bool layer) {
     const long long max_tiles = max_tiles_for(rows, groups, p.bm);
     w.tiles = static_cast<int32_t *>(c.take(sizeof(int32_t) * 4 * max_tiles));
     w.n_tiles = static_cast<int32_t *>(c.take(sizeof(int32_t)));
     w.group_tile_start = static_cast<int32_t *>(c.take(sizeof(int32_t) * (groups + 1)));
     w.h = c.take(dt_size(act_dt) * (size_t)(p.a4 ? rows - a4_rows : rows) * hw);
-    w.part = p.tiled ? c.take(dt_size(act_dt) * (size_t)rows * H)
-                     : c.take(sizeof(float) * (size_t)p.ksplit2 * rows * H);
+    w.part = p.a4 && !layer ? nullptr
+             : p.tiled      ? c.take(dt_size(act_dt) * (size_t)rows * H)
+                            : c.take(sizeof(float) * (size_t)p.ksplit2 * rows * H);
     w.part1 = p.ksplit1 > 1 ? static_cast<float *>(c.take(sizeof(float) * (size_t)p.ksplit1 * rows * 2 * hw))
                             : nullptr;
     if (p.a8) {
@@ -168,6 +172,7 @@ size_t ffn_ws_carve(Carver &c, FfnWs &w, const FfnPlan &p, int rows, int groups,
         w.x4s = static_cast<uint32_t *>(c.take(4 * px));
         w.h4 = static_cast<uint8_t *>(c.take(64 * ph));
         w.h4s = static_cast<uint32_t *>(c.take(4 * ph));
+        if (!layer) w.row_of4 = static_cast<int32_t *>(c.take(4 * (size_t)a4_rows));
     }
     if (p.tail) {
         w.tail_part = static_cast<float *>(c.take(tiled_tail_bytes(p.bm)));
@@ -486,12 +491,12 @@ size_t moe_grouped_ffn_workspace_bytes(int M, int G, int H, int F, moe_dtype act
     const FfnPlan p = plan_ffn(M, G, H, F, w_dt, path);
     Carver c(nullptr);
     FfnWs w{};
-    size_t bytes = ffn_ws_carve(c, w, p, M, G, H, F, act_dt, M, M);
+    size_t bytes = ffn_ws_carve(c, w, p, M, G, H, F, act_dt, M, M, false);
     if (p.a4) return bytes;
     FfnPlan q = p;  // the fp32 partials of the row-streaming form can be larger
     q.tiled = q.a8 = false;
     Carver c2(nullptr);
-    const size_t b2 = ffn_ws_carve(c2, w, q, M, G, H, F, act_dt, M, M);
+    const size_t b2 = ffn_ws_carve(c2, w, q, M, G, H, F, act_dt, M, M, false);
     return bytes > b2 ? bytes : b2;
 }
 
@@ -518,7 +523,7 @@ moe_status moe_grouped_ffn(const void *Xin, const int32_t *row_src, int k, int M
         return MOE_ERR_WORKSPACE_TOO_SMALL;
     Carver c(ws);
     FfnWs w{};
-    ffn_ws_carve(c, w, p, M, G, H, F, act_dt, M, M);
+    ffn_ws_carve(c, w, p, M, G, H, F, act_dt, M, M, false);
     const WType wt = wtype(w_dt);
     const bool bf = act_dt == MOE_BF16;
     const int max_tiles = (int)max_tiles_for(M, G, p.bm);
@@ -527,7 +532,8 @@ moe_status moe_grouped_ffn(const void *Xin, const int32_t *row_src, int k, int M
     if (p.a4) {
         // MXFP4 rows (gathered here) and the tile list, gate/up writing MXFP4 h, down
         const TilesJob tiles{offsets, G, p.bm, w.tiles, w.n_tiles, w.group_tile_start, w.tail_cnt, tiled_tail_counters};
-        MOE_TRY(launch_mx4_panels({Xin, row_src, k, H, M, 0, offsets + G, w.x4, w.x4s, w.ld4}, &tiles, stream));
+        MOE_TRY(launch_mx4_panels({Xin, row_src, k, H, M, 0, offsets + G, w.x4, w.x4s, w.ld4, nullptr, w.row_of4},
+                                  &tiles, stream));
         GemmProblem g1 = gate_up_problem(nullptr, nullptr, 1, &w, G, max_tiles, M, H, F, W1, W3, S1, S3, none, M,
                                          nullptr);
         set_a4(g1, w.x4, w.x4s, w.ld4);
@@ -678,7 +684,8 @@ ForwardWs carve_forward(const moe_layer_desc *d, int T, void *base) {
     FfnPlan carve = f.plan;
     const bool separate = d->Fs > 0 && !f.combined;
     if (separate && !f.plan.tiled && f.plan_s.ksplit2 > carve.ksplit2) carve.ksplit2 = f.plan_s.ksplit2;
-    ffn_ws_carve(c, f.ffn, carve, rows, groups, d->H, hw, d->act_dt, T, A + (f.combined ? T : 0));
+    ffn_ws_carve(c, f.ffn, carve, rows, groups, d->H, hw, d->act_dt, T, A + (f.combined ? T : 0),
+                 true);
     f.part1_s = nullptr;
     if (separate && !f.plan_s.tiled && f.plan_s.ksplit1 > 1)
         f.part1_s = static_cast<float *>(c.take(sizeof(float) * (size_t)f.plan_s.ksplit1 * T * 2 * d->Fs));
@@ -776,7 +783,8 @@ moe_status moe_forward(const moe_layer_desc *d, const void *X, int T, void *Y, v
         MOE_TRY(launch_quant_rows(X, H, nullptr, 1, T, H, f.ffn.xq, f.ffn.xs, stream, &sl));
     }
     if (p.a4)
-        MOE_TRY(launch_mx4_panels({X, f.row_src, d->k, H, A, ex.rows, f.offsets + E, f.ffn.x4, f.ffn.x4s, f.ffn.ld4},
+        MOE_TRY(launch_mx4_panels({X, f.row_src, d->k, H, A, ex.rows, f.offsets + E, f.ffn.x4, f.ffn.x4s, f.ffn.ld4,
+                                   f.assign_row, nullptr},
                                   nullptr, stream));
     MOE_TRY(mark(MOE_EV_SCHEDULE));
     GemmProblem g1 = gate_up_problem(X, f.row_src, d->k, &f.ffn, E, max_tiles, M, H, F, W1, W3, S1, S3, ex, A,

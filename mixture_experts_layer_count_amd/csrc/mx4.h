@@ -92,16 +92,23 @@ __host__ __device__ inline int panels(int C) { return (C + 127) / 128; }
 // (X[r] if row_src is NULL), rows [rows, rows + extra) are X[0 .. extra).
 // n_rows: rows in use among the first `rows` (device, NULL: all); the others
 // are left as they are. A [panels(C)][ld][64], As [panels(C)][ld]. X bf16 [*][C].
-// With `tiles`, the tile list of the products in the same launch.
+// row_of: row_of[a] = the row that holds assignment a < rows, as a hint (an entry
+// that does not name a row of a is passed over, and rows that no entry names are
+// found all the same); a token is then read once for its gk rows. NULL: not known;
+// then room for it may be given in `scratch` (int32 [rows]), and where it pays it is
+// made there, in a launch before.
+// With `tiles`, the tile list of the products too.
 struct Mx4Panels {
     const void *X;
     const int32_t *row_src;
-    int gk, C;  // gk <= 64
+    int gk, C;
     int rows, extra;
     const int32_t *n_rows;
     uint8_t *A;
     uint32_t *As;
     long long ld;
+    const int32_t *row_of;
+    int32_t *scratch;
 };
 struct TilesJob;
 hipError_t launch_mx4_panels(const Mx4Panels &p, const TilesJob *tiles, hipStream_t s);

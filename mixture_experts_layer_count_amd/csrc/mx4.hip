@@ -169,11 +169,6 @@ __global__ __launch_bounds__(256) void mx4_weights_back_kernel(const uint8_t *Q,
     }
 }
 
-// ---- rows in the product's layout: 16 lanes a row and panel (8 values each, four
-// lanes a group), RPT rows of one panel each, 64 RPT rows of a panel a workgroup.
-// SLICED: panel x, x + 8, ... on XCD x (workgroup number mod 8), one after the
-// other: gathered rows are read once for each of a token's k places, and an XCD's
-// slice of all tokens then stays in its L2 ----
 // a / gk of 0 <= a < 2^31 as a product: (a mul) >> (31 + shift), mul = floor(2^(31 +
 // shift) / gk) + 1, 2^shift >= gk. (mul gk exceeds 2^(31 + shift) by at most gk <=
 // 2^shift, so the product is off by less than 1 / gk.) A division by an argument
@@ -188,25 +183,50 @@ struct Divide {
         return (int)(((unsigned long long)(uint32_t)a * mul) >> (31 + shift));
     }
 };
-template <int RPT, bool SLICED>
-__global__ __launch_bounds__(1024) void mx4_panels_kernel(Mx4Panels p, TilesJob j, int chunks, int np, Divide token) {
+
+// ---- rows in the product's layout: 16 lanes a row and panel (8 values each, four
+// lanes a group), RPT rows of one panel each, 64 RPT rows of a panel a workgroup ----
+
+// what the first launch of two, or the first workgroups of one, do beside the rows
+__device__ __forceinline__ void first_jobs(const Mx4Panels &p, const TilesJob &j, int blk, int *scan_lds) {
+    if (blk == 0 && j.tiles)
+        build_tiles(j.offsets, j.G, 0, j.bm, j.tiles, j.n_tiles, j.start, j.zero, j.n_zero, scan_lds);
+}
+// the tile list, and which row holds an assignment
+__global__ __launch_bounds__(1024) void mx4_row_of_kernel(Mx4Panels p, TilesJob j) {
+    __shared__ int scan_lds[16];
+    first_jobs(p, j, blockIdx.x, scan_lds);
+    const int used = p.n_rows ? min(p.rows, *p.n_rows) : p.rows;
+    for (int r = blockIdx.x * 1024 + threadIdx.x; r < used; r += gridDim.x * 1024) {
+        const int a = p.row_src[r];
+        if (a >= 0 && a < p.rows) p.scratch[a] = r;
+    }
+}
+
+__device__ __forceinline__ u32x4 load_panel(const Mx4Panels &p, long long row, int c) {
+    const u32x4 x = *reinterpret_cast<const u32x4 *>(reinterpret_cast<const uint16_t *>(p.X) + row * p.C +
+                                                     (c < p.C ? c : 0));
+    return c < p.C ? x : u32x4{0, 0, 0, 0};
+}
+__device__ __forceinline__ void store_panel(const Mx4Panels &p, int kb, int row, int sub, uint32_t codes, uint32_t b) {
+    const long long o = kb * p.ld + row;
+    *reinterpret_cast<uint32_t *>(p.A + o * 64 + 4 * sub) = codes;
+    if ((sub & 3) == 0) reinterpret_cast<uint8_t *>(p.As + o)[sub >> 2] = (uint8_t)b;
+}
+
+// row by row
+template <int RPT>
+__global__ __launch_bounds__(1024) void mx4_panels_kernel(Mx4Panels p, TilesJob j, int chunks, Divide token) {
     __shared__ int scan_lds[16];
     int blk = blockIdx.x;
-    if (j.tiles) {  // the tile list, by a workgroup of its own (eight, to keep the others' XCDs)
-        if (blk < 8) {
-            if (blk == 0)
-                build_tiles(j.offsets, j.G, 0, j.bm, j.tiles, j.n_tiles, j.start, j.zero, j.n_zero, scan_lds);
-            return;
-        }
-        blk -= 8;
+    if (j.tiles && blk-- == 0) {
+        first_jobs(p, j, 0, scan_lds);
+        return;
     }
-    const int kb = SLICED ? blk % 8 + 8 * (blk / 8 / chunks) : blk / chunks;
-    if (kb >= np) return;
-    const int r0 = (SLICED ? blk / 8 : blk) % chunks * (64 * RPT) + (threadIdx.x >> 4);
+    const int kb = blk / chunks, r0 = blk % chunks * (64 * RPT) + (threadIdx.x >> 4);
     const int sub = threadIdx.x & 15, c = 128 * kb + 8 * sub;
     const int used = p.n_rows ? min(p.rows, *p.n_rows) : p.rows;
-    // a row's 16 lanes are in or out together; those out read row 0 of X
-    bool in[RPT];
+    bool in[RPT];  // a row's 16 lanes together
     long long src[RPT];
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
@@ -216,18 +236,62 @@ __global__ __launch_bounds__(1024) void mx4_panels_kernel(Mx4Panels p, TilesJob 
     }
     u32x4 x[RPT];
 #pragma unroll
-    for (int i = 0; i < RPT; ++i) {
-        x[i] = *reinterpret_cast<const u32x4 *>(reinterpret_cast<const uint16_t *>(p.X) + src[i] * p.C +
-                                                (c < p.C ? c : 0));
-        if (c >= p.C) x[i] = u32x4{0, 0, 0, 0};
-    }
+    for (int i = 0; i < RPT; ++i) x[i] = in[i] ? load_panel(p, src[i], c) : u32x4{0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
         const uint32_t b = scale_byte(quad_max(max_bits(x[i])));
-        if (!in[i]) continue;
-        const long long o = kb * p.ld + r0 + 64 * i;
-        *reinterpret_cast<uint32_t *>(p.A + o * 64 + 4 * sub) = codes8(x[i], b);
-        if ((sub & 3) == 0) reinterpret_cast<uint8_t *>(p.As + o)[sub >> 2] = (uint8_t)b;
+        if (in[i]) store_panel(p, kb, r0 + 64 * i, sub, codes8(x[i], b), b);
+    }
+}
+
+// token by token: its row is read and coded once and stored at the rows of its gk
+// assignments. Lane i of a token's 16 looks up assignments i, i + 16, ..
+template <int RPT>
+__global__ __launch_bounds__(1024) void mx4_panels_token_kernel(Mx4Panels p, int chunks, int tokens, Divide token) {
+    const int kb = blockIdx.x / chunks, chunk = blockIdx.x % chunks, t0 = chunk * (64 * RPT) + (threadIdx.x >> 4);
+    const int sub = threadIdx.x & 15, c = 128 * kb + 8 * sub;
+    const int used = p.n_rows ? min(p.rows, *p.n_rows) : p.rows;
+    for (int j0 = 0; j0 < p.gk; j0 += 16) {
+        int row[RPT];
+        u32x4 x[RPT];
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+            const int t = t0 + 64 * i;
+            const long long a = (long long)t * p.gk + j0 + sub;
+            row[i] = t < tokens && j0 + sub < p.gk && a < p.rows ? p.row_of[a] : -1;
+            if (row[i] < 0 || row[i] >= used || p.row_src[row[i]] != (int)a) row[i] = -1;
+        }
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+            // a token that no row names is not read (X may end before it)
+            const int t = t0 + 64 * i;
+            const bool some = (__ballot(row[i] >= 0) >> (threadIdx.x & 48) & 0xffffu) != 0 || t < p.extra;
+            x[i] = some ? load_panel(p, t, c) : u32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+            const uint32_t b = scale_byte(quad_max(max_bits(x[i]))), codes = codes8(x[i], b);
+            for (int j = 0; j < 16 && j0 + j < p.gk; ++j) {
+                const int r = __shfl(row[i], j, 16);
+                if (r >= 0) store_panel(p, kb, r, sub, codes, b);
+            }
+            if (j0 == 0 && t0 + 64 * i < p.extra) store_panel(p, kb, p.rows + t0 + 64 * i, sub, codes, b);
+        }
+    }
+    // rows that no entry of row_of names (an assignment that two rows hold, or one past
+    // the rows' number): a lane looks at one, and its 16 lanes code what they find
+    for (int base = chunk * 1024; base < used; base += chunks * 1024) {
+        const int r = base + threadIdx.x;
+        const int a = r < used ? p.row_src[r] : 0;
+        const bool own = r < used && ((uint32_t)a >= (uint32_t)p.rows || p.row_of[a] != r);
+        uint32_t left = (uint32_t)(__ballot(own) >> (threadIdx.x & 48)) & 0xffffu;
+        while (__any(left != 0)) {
+            const int i = left ? __ffs((int)left) - 1 : 0, t = token(__shfl(a, i, 16));
+            const u32x4 x = left ? load_panel(p, t, c) : u32x4{0, 0, 0, 0};
+            const uint32_t b = scale_byte(quad_max(max_bits(x)));
+            if (left) store_panel(p, kb, r - sub + i, sub, codes8(x, b), b);
+            left &= left - 1;
+        }
     }
 }
 
@@ -238,21 +302,40 @@ hipError_t launch_mx4_panels(const Mx4Panels &p, const TilesJob *tiles, hipStrea
         p.ld < (long long)p.rows + p.extra)
         return hipErrorInvalidValue;
     const long long rows = (long long)p.rows + p.extra;
+    if (rows == 0 && !tiles) return hipSuccess;
     const int np = panels(p.C);
     // few rows: one a thread, for more workgroups
     const bool few = (rows + 63) / 64 * np < 2048;
-    const long long chunks = (rows + (few ? 64 : 256) - 1) / (few ? 64 : 256);
-    // by XCD where gathered rows are read again and the panels fill the XCDs evenly
-    const bool sliced = !few && p.row_src && p.gk > 1 && (np % 8 == 0 || np >= 24);
-    const long long blocks = chunks * (sliced ? (np + 7) / 8 * 8 : np) + (tiles ? 8 : 0);
-    if (blocks == 0) return hipSuccess;
-    if (blocks > kMaxThreads / 1024) return hipErrorInvalidValue;
     const TilesJob job = tiles ? *tiles : TilesJob{};
-    const dim3 grid((unsigned)blocks), block(1024);
     const Divide token(p.gk);
-    if (few) hipLaunchKernelGGL((mx4_panels_kernel<1, false>), grid, block, 0, s, p, job, (int)chunks, np, token);
-    else if (sliced) hipLaunchKernelGGL((mx4_panels_kernel<4, true>), grid, block, 0, s, p, job, (int)chunks, np, token);
-    else hipLaunchKernelGGL((mx4_panels_kernel<4, false>), grid, block, 0, s, p, job, (int)chunks, np, token);
+    const dim3 block(1024);
+    // 65536 rows of 8192 tokens, C 2048: 53 us by row (268 MB of tokens read from beyond
+    // the L2s, at 5 TB/s), 37 + 6 for row_of by token. 8192 rows of 4096 tokens, C 4096: 21
+    // by row, 20 + 5 by token
+    if (!few && p.row_src && p.gk >= 4 && (p.row_of || p.scratch)) {
+        Mx4Panels q = p;
+        if (!q.row_of) {
+            const long long n = (rows + 1023) / 1024;
+            hipLaunchKernelGGL(mx4_row_of_kernel, dim3((unsigned)(n < 512 ? n : 512)), block, 0, s, p, job);
+            q.row_of = p.scratch;
+        } else if (tiles) {
+            return hipErrorInvalidValue;
+        }
+        long long tokens = (p.rows + (long long)p.gk - 1) / p.gk;
+        if (tokens < p.extra) tokens = p.extra;
+        const long long chunks = (tokens + 255) / 256;
+        if (chunks * np > kMaxThreads / 1024) return hipErrorInvalidValue;
+        hipLaunchKernelGGL(mx4_panels_token_kernel<4>, dim3((unsigned)(chunks * np)), block, 0, s, q, (int)chunks,
+                           (int)tokens, token);
+        return hipGetLastError();
+    }
+    const long long chunks = (rows + (few ? 64 : 256) - 1) / (few ? 64 : 256);
+    const long long blocks = chunks * np + (tiles ? 1 : 0);
+    if (blocks > kMaxThreads / 1024) return hipErrorInvalidValue;
+    if (few)
+        hipLaunchKernelGGL(mx4_panels_kernel<1>, dim3((unsigned)blocks), block, 0, s, p, job, (int)chunks, token);
+    else
+        hipLaunchKernelGGL(mx4_panels_kernel<4>, dim3((unsigned)blocks), block, 0, s, p, job, (int)chunks, token);
     return hipGetLastError();
 }
 

@@ -270,6 +270,30 @@ def test_ffn_rows_behind_the_last_group():
     assert (out == 3).all()
 
 
+def test_ffn_rows_of_any_assignments():
+    """Many rows whose assignments are no permutation: one twice, some missing, some past
+    the number of rows (other ranks' tokens)."""
+    say("[mx4] ffn of many rows, some of the same assignment, some past the rows' number")
+    T, H, F, E, k = 4500, 1056, 64, 6, 4
+    d = _case(T, H, F, E, k, 15)
+    src = d["row_src"].clone()
+    g = torch.Generator().manual_seed(4)
+    at = torch.randperm(T * k, generator=g)[:700].cuda()
+    src[at[:300]] = src[at[300:600]]                        # twice
+    M = 16001                                               # fewer rows than assignments
+    off = d["offsets"].clamp(max=M)
+    src = src[:M].clone()
+    assert int((src >= M).sum()) > 500 and src.unique().numel() < M
+    Y = _ffn(d | {"row_src": src, "offsets": off})
+    Xp = d["X"][src.long() // k].contiguous()
+    assert torch.equal(Y, _ffn(d | {"X": Xp, "k": 1, "offsets": off}, row_src=None))
+    _check(d | {"row_src": src, "offsets": off}, Y, rows=range(0, M, 197))
+    # no rows in use, nothing read
+    out = torch.full((M, H), 7.0, dtype=torch.bfloat16, device="cuda")
+    _ffn(d | {"row_src": torch.full_like(src, 0x7ffffff0), "offsets": torch.zeros_like(off)}, out=out)
+    assert (out == 7).all()
+
+
 def test_ffn_nan_and_infinity_stay_in_their_rows():
     say("[mx4] ffn with NaN, infinity and the NaN scale")
     d = _case(150, 256, 160, 3, 1, 11)
@@ -353,7 +377,8 @@ def _layer(T, H, F, E, k, Fs, shared, seed):
 
 
 @pytest.mark.parametrize("T,H,F,E,k,Fs,shared", [(1, 256, 128, 8, 2, 0, None), (130, 384, 160, 8, 3, 160, "mxfp4"),
-                                                 (700, 256, 416, 16, 4, 96, "bf16"), (2500, 512, 256, 4, 1, 256, "mxfp4")])
+                                                 (700, 256, 416, 16, 4, 96, "bf16"), (2500, 512, 256, 4, 1, 256, "mxfp4"),
+                                                 (3300, 1088, 64, 12, 5, 64, "mxfp4")])
 def test_layer_is_its_stages(T, H, F, E, k, Fs, shared):
     say(f"[mx4] layer T={T} H={H} F={F} E={E} k={k} shared {shared}")
     d = _layer(T, H, F, E, k, Fs, shared, T)
