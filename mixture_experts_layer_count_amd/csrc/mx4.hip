@@ -13,7 +13,9 @@ namespace {
 using namespace mx4;
 
 constexpr long long kMaxThreads = 0xffffffffLL;  // of a launch (beyond, it takes their number mod 2^32)
-constexpr int kPer = 16;                         // values per thread of the row kernels
+// fewer threads of two words take one: 16384: 4.0 against 4.5 us, 32768: 6.6 against 5.2
+constexpr long long kFewThreads = 1 << 15;
+constexpr int kPer = 16;  // values per thread of the row kernels
 
 // the largest of a lane and its neighbour, and of the four lanes of a quad
 __device__ __forceinline__ uint32_t pair_max(uint32_t v) {
@@ -102,42 +104,92 @@ __global__ __launch_bounds__(256) void mx4_rows_back_kernel(const uint8_t *Q, co
     }
 }
 
-// ---- weights [G][K][N]: a thread owns 8 columns of one group of 32 K rows
-// (a wavefront's rows are contiguous: 1 KB of bf16, 512 bytes of codes), its
-// values kept in registers between the maximum and the codes ----
-template <bool F32>
+// byte J of a code word, from the values of two rows: fp32 bits, or the bf16 of
+// columns J & 1 in two words of two columns
+template <int J>
+__device__ __forceinline__ uint32_t codes_f32(uint32_t w, uint32_t lo, uint32_t hi, float s) {
+    return (uint32_t)__builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, __uint_as_float(lo), __uint_as_float(hi), s, J);
+}
+template <int J>
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w, uint32_t lo, uint32_t hi, float s) {
+    const uint32_t pair = __builtin_amdgcn_perm(hi, lo, J & 1 ? 0x07060302u : 0x05040100u);
+    return (uint32_t)__builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, pair_of(pair), s, J);
+}
+
+// ---- weights [G][K][N]: a thread owns 4 WORDS columns of one group of 32 K rows
+// (bf16 with 2 WORDS: a wavefront's rows are 1 KB of values, 512 bytes of codes), its
+// values kept in registers between the maximum and the codes. fp32 takes one word:
+// two would be 256 registers of values ----
+template <bool F32, int WORDS>
 __global__ __launch_bounds__(256) void mx4_weights_kernel(const void *W, long long threads, int N, uint8_t *Q,
                                                           uint8_t *S) {
+    typedef uint32_t Words __attribute__((ext_vector_type(WORDS)));
+    constexpr int kCols = 4 * WORDS, kRegs = F32 ? kCols : kCols / 2;  // registers a row
+    typedef uint32_t Row __attribute__((ext_vector_type(kRegs)));
     const long long t = (long long)blockIdx.x * 256 + threadIdx.x;
     if (t >= threads) return;
-    const int per = N / 8;
+    const int per = N / kCols;
     const long long g = t / per;  // group of 32 rows, over all matrices (K is a multiple of 32)
-    const int c = (int)(t - g * per) * 8;
-    float v[32][8];
+    const int c = (int)(t - g * per) * kCols;
+    Row v[32];
 #pragma unroll
-    for (int r = 0; r < 32; ++r) load8<F32>(W, (32 * g + r) * N + c, v[r]);
-    uint32_t b[8];
+    for (int r = 0; r < 32; ++r) {
+        const long long o = (32 * g + r) * N + c;
+        v[r] = *reinterpret_cast<const Row *>(static_cast<const char *>(W) + (F32 ? 4 : 2) * o);
+    }
+    uint32_t m[kCols];  // bits of the largest magnitudes
+    if constexpr (F32) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        uint32_t m = 0;
+        for (int j = 0; j < kCols; ++j) {
+            m[j] = 0;
 #pragma unroll
-        for (int r = 0; r < 32; ++r) m = max(m, mag_bits(v[r][j]));
-        b[j] = scale_byte(m);
+            for (int r = 0; r < 32; ++r) m[j] = max(m[j], v[r][j] & 0x7fffffffu);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kRegs; ++j) {
+            u16x2 most = mags(v[0][j]);
+#pragma unroll
+            for (int r = 1; r < 32; ++r) most = __builtin_elementwise_max(most, mags(v[r][j]));
+            m[2 * j] = (uint32_t)most[0] << 16;
+            m[2 * j + 1] = (uint32_t)most[1] << 16;
+        }
+    }
+    Words b, keep;  // scale bytes; a mask of the columns without the NaN scale
+    float s[kCols];
+#pragma unroll
+    for (int w = 0; w < WORDS; ++w) b[w] = keep[w] = 0;
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+        const uint32_t byte = scale_byte(m[j]);
+        s[j] = scale_of(byte == 255u ? 127u : byte);
+        b[j / 4] |= byte << (8 * (j & 3));
+        keep[j / 4] |= (byte == 255u ? 0u : 255u) << (8 * (j & 3));
     }
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-        uint32_t q[8];
+        const Row lo = v[2 * r], hi = v[2 * r + 1];
+        Words q;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t w = (uint32_t)__builtin_amdgcn_cvt_scalef32_pk_fp4_f32(
-                0u, v[2 * r][j], v[2 * r + 1][j], scale_of(b[j] == 255u ? 127u : b[j]), 0);
-            q[j] = b[j] == 255u ? 0u : w & 255u;
+        for (int w = 0; w < WORDS; ++w) {
+            uint32_t x = 0;
+            // byte j: the codes of rows 2 r (low) and 2 r + 1 of column 4 w + j
+            if constexpr (F32) {
+                x = codes_f32<0>(x, lo[4 * w], hi[4 * w], s[4 * w]);
+                x = codes_f32<1>(x, lo[4 * w + 1], hi[4 * w + 1], s[4 * w + 1]);
+                x = codes_f32<2>(x, lo[4 * w + 2], hi[4 * w + 2], s[4 * w + 2]);
+                x = codes_f32<3>(x, lo[4 * w + 3], hi[4 * w + 3], s[4 * w + 3]);
+            } else {
+                x = codes_bf16<0>(x, lo[2 * w], hi[2 * w], s[4 * w]);
+                x = codes_bf16<1>(x, lo[2 * w], hi[2 * w], s[4 * w + 1]);
+                x = codes_bf16<2>(x, lo[2 * w + 1], hi[2 * w + 1], s[4 * w + 2]);
+                x = codes_bf16<3>(x, lo[2 * w + 1], hi[2 * w + 1], s[4 * w + 3]);
+            }
+            q[w] = x & keep[w];
         }
-        *reinterpret_cast<u32x2 *>(Q + (16 * g + r) * N + c) =
-            u32x2{q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24, q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24};
+        *reinterpret_cast<Words *>(Q + (16 * g + r) * N + c) = q;
     }
-    *reinterpret_cast<u32x2 *>(S + g * N + c) =
-        u32x2{b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24};
+    *reinterpret_cast<Words *>(S + g * N + c) = b;
 }
 
 template <bool F32>
@@ -411,10 +463,14 @@ moe_status moe_quantize_mxfp4_weights(const void *W, moe_dtype w_dt, int G, int 
     if (G == 0) return MOE_OK;
     if (!W || !Q || !S) return MOE_ERR_INVALID_ARG;
     if (off16(W) || off8(Q) || off8(S)) return MOE_ERR_UNSUPPORTED;
-    const long long threads = (long long)G * (K / 32) * (N / 8);
+    const long long words = (long long)G * (K / 32) * (N / 4);
+    const bool one = w_dt == MOE_F32 || words / 2 < kFewThreads;
+    const long long threads = one ? words : words / 2;
     const dim3 grid((unsigned)((threads + 255) / 256));
-    if (w_dt == MOE_F32) hipLaunchKernelGGL(mx4_weights_kernel<true>, grid, dim3(256), 0, stream, W, threads, N, Q, S);
-    else hipLaunchKernelGGL(mx4_weights_kernel<false>, grid, dim3(256), 0, stream, W, threads, N, Q, S);
+    if (w_dt == MOE_F32)
+        hipLaunchKernelGGL((mx4_weights_kernel<true, 1>), grid, dim3(256), 0, stream, W, threads, N, Q, S);
+    else if (one) hipLaunchKernelGGL((mx4_weights_kernel<false, 1>), grid, dim3(256), 0, stream, W, threads, N, Q, S);
+    else hipLaunchKernelGGL((mx4_weights_kernel<false, 2>), grid, dim3(256), 0, stream, W, threads, N, Q, S);
     return hip_status(hipGetLastError());
 }
 
