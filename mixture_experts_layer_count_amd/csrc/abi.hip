@@ -143,8 +143,8 @@ struct ExtraGroup {
 
 // xrows: rows of quantised expert input (W8A8 only). W4A4: the rows of the
 // grouped launches are the first a4_rows; bf16 h is kept for the others only,
-// and the last product's rows and the map to a token's rows lie elsewhere for
-// one of moe_grouped_ffn and moe_forward each (layer: the latter).
+// and the last product's rows and the tail split's sums are moe_forward's only
+// (layer; the latter for its shared expert), the map to a token's rows the other's.
 size_t ffn_ws_carve(Carver &c, FfnWs &w, const FfnPlan &p, int rows, int groups, int H, int hw,
                     moe_dtype act_dt, int xrows, int a4_rows, bool layer) {
     const long long max_tiles = max_tiles_for(rows, groups, p.bm);
@@ -174,7 +174,7 @@ size_t ffn_ws_carve(Carver &c, FfnWs &w, const FfnPlan &p, int rows, int groups,
         w.h4s = static_cast<uint32_t *>(c.take(4 * ph));
         if (!layer) w.row_of4 = static_cast<int32_t *>(c.take(4 * (size_t)a4_rows));
     }
-    if (p.tail) {
+    if (p.tail && (!p.a4 || layer)) {
         w.tail_part = static_cast<float *>(c.take(tiled_tail_bytes(p.bm)));
         w.tail_cnt = static_cast<int32_t *>(c.take(sizeof(int32_t) * tiled_tail_counters));
     }
@@ -531,7 +531,7 @@ moe_status moe_grouped_ffn(const void *Xin, const int32_t *row_src, int k, int M
 
     if (p.a4) {
         // MXFP4 rows (gathered here) and the tile list, gate/up writing MXFP4 h, down
-        const TilesJob tiles{offsets, G, p.bm, w.tiles, w.n_tiles, w.group_tile_start, w.tail_cnt, tiled_tail_counters};
+        const TilesJob tiles{offsets, G, p.bm, w.tiles, w.n_tiles, w.group_tile_start, nullptr, 0};
         MOE_TRY(launch_mx4_panels({Xin, row_src, k, H, M, 0, offsets + G, w.x4, w.x4s, w.ld4, nullptr, w.row_of4},
                                   &tiles, stream));
         GemmProblem g1 = gate_up_problem(nullptr, nullptr, 1, &w, G, max_tiles, M, H, F, W1, W3, S1, S3, none, M,

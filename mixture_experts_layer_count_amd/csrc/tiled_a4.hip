@@ -49,11 +49,10 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kA4BK = 128;    // K per step
 constexpr int kA4Items = 64;  // work items per workgroup at most (LDS table)
+constexpr int WR = 2, WC = 4, NW = WR * WC, NJ = 8 / WC;  // wavefronts; 32-column blocks of one
 
-template <int WR, int WC, int MI>
+template <int MI>
 struct RingA4 {
-    static constexpr int waves = WC * WR;
-    static constexpr int threads = 64 * waves;
     static constexpr int BM = 32 * MI * WR;
     static constexpr int a_bytes = BM * 64;
     static constexpr int b_bytes = 64 * 256;
@@ -61,36 +60,28 @@ struct RingA4 {
     static constexpr int sb_bytes = 4 * 256;
     static constexpr int sb_at = a_bytes + b_bytes + sa_bytes;
     static constexpr int stage = sb_at + sb_bytes;
-    static constexpr int budget = 160 * 1024 - kA4Items * 32 - 16;
-    static constexpr int S = budget / stage < 6 ? budget / stage : 6;
+    static constexpr int at = 16 * kA4Items;  // the table of items comes first
+    static constexpr int S = (160 * 1024 - at) / stage < 6 ? (160 * 1024 - at) / stage : 6;
     static constexpr int a_chunks = a_bytes / 1024;  // 1 KB copies, 16 rows each
-    static constexpr int nA = (a_chunks + waves - 1) / waves;
-    static constexpr int nB = 16 / waves;            // 1 KB copies, 8 byte rows of a half each
+    static constexpr int nA = (a_chunks + NW - 1) / NW;
+    static constexpr int nB = 16 / NW;               // 1 KB copies, 8 byte rows of a half each
     static constexpr int slots = BM / 64 + 4;        // 256-byte scale copies
-    static constexpr int nS = (slots + waves - 1) / waves;
+    static constexpr int nS = (slots + NW - 1) / NW;
     static constexpr int per_step = nA + nB + nS;
-    static constexpr int table = S * stage;
-    static constexpr int flag = table + kA4Items * 32;
-    static constexpr int lds = flag + 16;
+    static constexpr int lds = at + S * stage;
     static_assert(S >= 3 && BM % 64 == 0 && (S - 2) * per_step < 64, "ring");
 };
-
-// Equal parts over K that each item of an XCD's last round of workgroups is cut into
-// (1: none), where it leaves half of them idle: one round of parts, of at least
-// kA4PartSteps steps. 8 experts, 8192 rows, K 14336 (2.25 rounds): 321 to 288 us.
-// Cutting the last two rounds' steps into equal ranges instead, with two parts
-// an item, took 312: the card's clock falls with the matrix cores' load, so a
-// round on part of the chip costs less than its length.
-constexpr int kA4Parts = 4, kA4PartSteps = 12;
-__device__ __forceinline__ int tail_parts(int n, int slots, int nk) {
-    const int tail = n % slots;
-    if (tail == 0 || slots > kBlocksPerXcd) return 1;
-    return max(min(min(kA4Parts, slots / tail), nk / kA4PartSteps), 1);
-}
 
 // What steers the K loop is kept in scalar registers: a count that went through a
 // vector load or a division leaves a loop of exec masks, 15 % slower
 __device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// Whether an XCD's last round of items, if it leaves half of its workgroups idle, is cut
+// into pieces of 64 rows
+__device__ __forceinline__ bool cut_tail(int n, int slots, int nk) {
+    const int tail = n % slots;
+    return tail > 0 && 2 * tail <= slots && nk >= 16 && slots == kBlocksPerXcd;
+}
 
 template <int OPB, int OPA>
 __device__ __forceinline__ f32x16 mfma4(const i32x4 &b, const i32x4 &a, const f32x16 &c, int sb, int sa) {
@@ -100,60 +91,57 @@ __device__ __forceinline__ f32x16 mfma4(const i32x4 &b, const i32x4 &a, const f3
 }
 struct ItemA4 {
     int g, row0, row_end, n0;
-    int k0, k1;  // steps
-    int cut;     // whether a part of its tile
+};
+// A workgroup's items: number slot + i slots of `n` for i < .., each 64 MI rows of tile
+// first + number / cut (cut > 1: piece number % cut of it; a piece without rows is dropped)
+struct Share {
+    int first, n, cut;
 };
 
-template <bool SWIGLU, int WR, int WC, int MI>
-__global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p, int nN) {
-    typedef RingA4<WR, WC, MI> R;
-    constexpr int S = R::S, NW = R::waves, NJ = 8 / WC;  // 32-column blocks of a wavefront
+template <bool SWIGLU, int MI>
+__device__ __forceinline__ void run_items(const GemmProblem &p, int nN, int n_tiles, const Share &share, uint8_t *lds) {
+    typedef RingA4<MI> R;
+    constexpr int S = R::S;
     constexpr int W = SWIGLU ? 128 : 256;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[R::lds];
-    int *table = reinterpret_cast<int *>(lds + R::table);
+    int *table = reinterpret_cast<int *>(lds);
+    uint8_t *ring = lds + R::at;
 
     const int tid = threadIdx.x;
-    const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wr = w / WC, wc = w % WC;
+    const int lane = tid & 63, w = scalar(tid >> 6), wr = w / WC, wc = w % WC;
     const int l32 = lane & 31, hb = lane >> 5;
     const int nk = (p.K + kA4BK - 1) / kA4BK;
+    const int slot = blockIdx.x / kXcds, slots = gridDim.x / kXcds;
 
     // ---- this workgroup's items ----
-    const int n_tiles = scalar(*p.n_tiles);
-    const int n_work = n_tiles * nN;
-    const int per = (n_work + kXcds - 1) / kXcds;
-    const int xcd = blockIdx.x % kXcds, slot = blockIdx.x / kXcds, slots = gridDim.x / kXcds;
-    const int mine = min(per, n_work - xcd * per);
-    if (mine <= 0) return;
-    // full rounds of whole items, then one part of an item of the last round
-    const int parts = scalar(tail_parts(mine, slots, nk)), part = scalar(slot % parts);
-    const int tail = parts > 1 ? scalar(mine % slots) : 0, full = mine - tail;
-    const int whole = slot < full ? scalar((full - slot + slots - 1) / slots) : 0;
-    int count = whole + (slot < tail * parts ? 1 : 0);
-    if (count == 0) return;
+    int count = slot < share.n ? scalar((share.n - slot + slots - 1) / slots) : 0;
     if (MOE_BOUNDS_FAIL(count <= kA4Items, BOUNDS_TILE)) return;
-    if (w == 0 && lane < count) {
-        int mt, nt;
-        const int cut = lane >= whole;
-        const int item = cut ? full + slot / parts : slot + slots * lane;
-        const int k0 = cut ? part * nk / parts : 0, k1 = cut ? (part + 1) * nk / parts : nk;
-        tile_of(p, nN, n_tiles, xcd * per + item, mt, nt);
-        const bool ok = mt < p.max_tiles;
-        int g = ok ? p.tiles[4 * mt] : 0, r0 = ok ? p.tiles[4 * mt + 1] : 0, r1 = ok ? p.tiles[4 * mt + 2] : 0;
-        if (MOE_BOUNDS_FAIL(ok && g >= 0 && g < p.n_groups && r0 >= 0 && r0 < r1 && r1 <= p.M, BOUNDS_TILE)) {
-            g = 0;
-            r0 = 0;
-            r1 = 1;
+    {
+        int g = 0, r0 = 0, r1 = 0, mt, nt = 0;
+        if (lane < count) {
+            const int item = slot + slots * lane, piece = item % share.cut;
+            tile_of(p, nN, n_tiles, share.first + item / share.cut, mt, nt);
+            const bool ok = mt < p.max_tiles;
+            if (ok) g = p.tiles[4 * mt], r0 = p.tiles[4 * mt + 1], r1 = p.tiles[4 * mt + 2];
+            if (MOE_BOUNDS_FAIL(ok && g >= 0 && g < p.n_groups && r0 >= 0 && r0 < r1 && r1 <= p.M, BOUNDS_TILE)) {
+                g = 0;
+                r0 = 0;
+                r1 = 1;
+            }
+            if (share.cut > 1) {
+                r0 += R::BM * piece;
+                r1 = min(r1, r0 + R::BM);
+            }
         }
-        i32x4 *rec = reinterpret_cast<i32x4 *>(table + 8 * lane);
-        rec[0] = i32x4{g, r0, r1, nt * W};
-        rec[1] = i32x4{k0, k1, cut, 0};
+        const unsigned long long some = __ballot(r0 < r1);
+        if (w == 0 && r0 < r1)
+            *reinterpret_cast<i32x4 *>(table + 4 * __popcll(some & ((1ULL << lane) - 1))) = i32x4{g, r0, r1, nt * W};
+        count = scalar(__popcll(some));
     }
     __syncthreads();
-    count = scalar(count);
+    if (count == 0) return;
     auto item_at = [&](int j) {
-        const i32x4 *rec = reinterpret_cast<const i32x4 *>(table + 8 * j);
-        const i32x4 t = rec[0], u = rec[1];
-        return ItemA4{scalar(t[0]), scalar(t[1]), scalar(t[2]), scalar(t[3]), scalar(u[0]), scalar(u[1]), scalar(u[2])};
+        const i32x4 t = *reinterpret_cast<const i32x4 *>(table + 4 * j);
+        return ItemA4{scalar(t[0]), scalar(t[1]), scalar(t[2]), scalar(t[3])};
     };
 
     // ---- copies: a uniform base that moves on each step, and a lane's offset.
@@ -173,19 +161,19 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
     // byte rows and K groups of the last step that the weights have
     const int k_rows = p.K / 2 - 64 * (nk - 1), k_groups = p.K / 32 - 4 * (nk - 1);
     const bool ragged = p.K % kA4BK != 0;
+    auto bytes = [](const void *x) { return static_cast<const uint8_t *>(x); };
+    const uint8_t *wb0 = bytes(p.B0), *wb1 = bytes(p.B1), *ws0 = bytes(p.S0), *ws1 = bytes(p.S1);
+    const uint8_t *xb0 = bytes(p.Bx0), *xb1 = bytes(p.Bx1), *xs0 = bytes(p.Sx0), *xs1 = bytes(p.Sx1);
     auto set_sources = [&](const ItemA4 &it) {
-        const int kt = it.k0;
         int ln = lane;  // re-read: its multiples need not live through the K loop
         asm volatile("" : "+v"(ln));
         const bool extra = it.g == p.extra_group;
-        a_base = reinterpret_cast<const uint8_t *>(p.A) + (kt * p.as_ld + it.row0) * 64;
-        const long long go = (extra ? 0 : (long long)it.g * p.b_stride) + 64LL * kt * p.N;
-        const long long so = (extra ? 0 : (long long)it.g * p.s_stride) + 4LL * kt * p.N;
-        const uint8_t *B0 = reinterpret_cast<const uint8_t *>(extra ? p.Bx0 : p.B0) + go;
-        const uint8_t *S0 = reinterpret_cast<const uint8_t *>(extra ? p.Sx0 : p.S0) + so;
-        b_base[0] = B0;
-        b_base[1] = SWIGLU ? reinterpret_cast<const uint8_t *>(extra ? p.Bx1 : p.B1) + go : B0;
-        const uint8_t *S1 = SWIGLU ? reinterpret_cast<const uint8_t *>(extra ? p.Sx1 : p.S1) + so : S0;
+        a_base = reinterpret_cast<const uint8_t *>(p.A) + (long long)it.row0 * 64;
+        const long long go = (extra ? 0 : (long long)it.g * p.b_stride);
+        const long long so = (extra ? 0 : (long long)it.g * p.s_stride);
+        const uint8_t *S0 = (extra ? xs0 : ws0) + so, *S1 = SWIGLU ? (extra ? xs1 : ws1) + so : S0;
+        b_base[0] = (extra ? xb0 : wb0) + go;
+        b_base[1] = SWIGLU ? (extra ? xb1 : wb1) + go : b_base[0];
 #pragma unroll
         for (int q = 0; q < R::nB; ++q) {
             const int i = w + NW * q, row = 8 * (i & 7) + (ln >> 3);
@@ -197,7 +185,7 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
         for (int q = 0; q < R::nS; ++q) {
             const int i = s_slot(q);
             if (i < R::BM / 64) {
-                s_base[q] = reinterpret_cast<const uint8_t *>(p.As) + (kt * p.as_ld + it.row0) * 4;
+                s_base[q] = reinterpret_cast<const uint8_t *>(p.As) + (long long)it.row0 * 4;
                 s_off[q] = (64 * i + ln) * 4;
             } else {
                 const int h = (i - R::BM / 64) >> 1, kg = 2 * ((i - R::BM / 64) & 1) + (ln >> 5);
@@ -214,8 +202,8 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
     for (int q = 0; q < R::nS; ++q) s_step[q] = s_slot(q) < R::BM / 64 ? p.as_ld * 4 : 4LL * p.N;
     auto begin_item = [&]() {
         const ItemA4 it = item_at(c_item);
-        c_kt = it.k0;
-        c_left = it.k1 - it.k0;
+        c_kt = 0;
+        c_left = nk;
         set_sources(it);
     };
     auto move = [&](long long by) {
@@ -241,7 +229,7 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
         }
     };
     auto copy = [&](int q, int stage) {
-        uint8_t *st = lds + stage * R::stage;
+        uint8_t *st = ring + stage * R::stage;
         if (MOE_BOUNDS_FAIL(c_kt >= 0 && c_kt < nk, BOUNDS_TILE)) c_kt = nk - 1;
         const bool last = ragged && c_kt == nk - 1;
         if (q < R::nA) {
@@ -290,7 +278,7 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
     constexpr int NRF = 2 * NJ + MI, NRS = MI + 1;  // reads of a half, and of a stage's scales
     auto read = [&](Frag &f, int r, int stage, auto kh_) {
         constexpr int kh = decltype(kh_)::value;
-        const uint8_t *st = lds + stage * R::stage;
+        const uint8_t *st = ring + stage * R::stage;
         if (r < 2 * NJ) {
             const int j = r >> 1;
             const uint32_t at = lds_addr(st) + tr_at[j];
@@ -336,12 +324,11 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
         constexpr int kh = decltype(kh_)::value;
         const int m = i / NJ, j = i % NJ;
         __builtin_amdgcn_sched_barrier(0);
-        const int sbw = (int)(NJ == 4 ? sb[kh] : sb[0]);
-        switch (NJ == 4 ? j : 2 * kh + j) {
-        case 0: acc[m][j] = mfma4<0, 2 * kh>(f.b[j], f.a[m], acc[m][j], sbw, sa[m]); break;
-        case 1: acc[m][j] = mfma4<1, 2 * kh>(f.b[j], f.a[m], acc[m][j], sbw, sa[m]); break;
-        case 2: acc[m][j] = mfma4<2, 2 * kh>(f.b[j], f.a[m], acc[m][j], sbw, sa[m]); break;
-        default: acc[m][j] = mfma4<3, 2 * kh>(f.b[j], f.a[m], acc[m][j], sbw, sa[m]); break;
+        switch (2 * kh + j) {
+        case 0: acc[m][j] = mfma4<0, 2 * kh>(f.b[j], f.a[m], acc[m][j], (int)sb[0], sa[m]); break;
+        case 1: acc[m][j] = mfma4<1, 2 * kh>(f.b[j], f.a[m], acc[m][j], (int)sb[0], sa[m]); break;
+        case 2: acc[m][j] = mfma4<2, 2 * kh>(f.b[j], f.a[m], acc[m][j], (int)sb[0], sa[m]); break;
+        default: acc[m][j] = mfma4<3, 2 * kh>(f.b[j], f.a[m], acc[m][j], (int)sb[0], sa[m]); break;
         }
         __builtin_amdgcn_sched_barrier(0);
     };
@@ -361,7 +348,7 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
     // h in MXFP4: a lane holds half of a row's 32 columns, lane ^ 32 the rest.
     // Of two row blocks the lower lanes store the first's rows, the upper ones
     // the second's: 16 bytes of codes and a scale byte a lane
-    auto gate_up_out = [&](const ItemA4 &it, auto sums) {
+    auto gate_up_out = [&](const ItemA4 &it) {
         int ln = lane;
         asm volatile("" : "+v"(ln));
         const long long at = (long long)(it.n0 >> 7) * p.cqs_ld + it.row0;
@@ -383,7 +370,7 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
                         byte[u] = byte[0];
                         continue;
                     }
-                    const f32x16 g = sums(m + u, j), x = sums(m + u, j + NJ / 2);
+                    const f32x16 &g = acc[m + u][j], &x = acc[m + u][j + NJ / 2];
                     float v[16];
                     uint32_t t = 0;
 #pragma unroll
@@ -421,7 +408,7 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
     // bf16 rows: a lane holds 4-column pieces of its row, lane ^ 32 the ones between.
     // Exchanges between the wavefront's halves and quarters leave 8 columns a lane
     // and the four lanes l, l + 16, .. with a row's 32: 64 bytes of 16 rows a store
-    auto down_out = [&](const ItemA4 &it, auto sums) {
+    auto down_out = [&](const ItemA4 &it) {
         int ln = lane;
         asm volatile("" : "+v"(ln));
         const int rows = it.row_end - it.row0, ld = p.ldc;
@@ -432,7 +419,7 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
             const int row = wr * 32 * MI + 32 * m + (ln & 15);  // of the tile
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
-                const f32x16 x = sums(m, j);
+                const f32x16 &x = acc[m][j];
                 uint32_t v[2][4];  // columns 0..7 or 8..15 (upper lanes), and 16 more
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -459,85 +446,9 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
     };
 
     constexpr int ST = SWIGLU ? NJ * ((MI + 1) / 2) : 2 * NJ * MI;  // stores of a tile
-    // sums(m, j): the block's fp32 sums
-    auto tile_out = [&](const ItemA4 &it, auto sums) {
-        if constexpr (SWIGLU) gate_up_out(it, sums);
-        else down_out(it, sums);
-    };
-    // ---- an item in parts. Sums pass through memory as [accumulator][thread] vectors;
-    // one thread makes them visible beyond this XCD's L2 (a release), or takes what
-    // was made so (an acquire, which serves the workgroup after the barrier) ----
-    constexpr int NV = MI * NJ * 4;
-    int *flag = reinterpret_cast<int *>(lds + R::flag);
-    constexpr int kSums = NV * R::threads * 16;  // bytes of a tile's sums
-    auto sums_of = [&](int i) { return rsrc(reinterpret_cast<uint8_t *>(p.tail_part) + (long long)i * kSums, kSums); };
-    auto store_sums = [&](int i) {
-        const auto to = sums_of(i);
-#pragma unroll
-        for (int m = 0; m < MI; ++m)
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const f32x16 &x = acc[m][j];
-                    __builtin_amdgcn_raw_buffer_store_b128(
-                        __builtin_bit_cast(u32x4, f32x4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]}), to,
-                        tid * 16, ((m * NJ + j) * 4 + q) * R::threads * 16, 0);
-                }
-        wait_vm<0>();
-        __syncthreads();
-    };
-    auto stored = [&](const auto &from, int m, int j) {
-        f32x16 x;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const f32x4 v = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                          from, tid * 16, ((m * NJ + j) * 4 + q) * R::threads * 16, 0));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[4 * q + e] = v[e];
-        }
-        return x;
-    };
-    // Each part leaves its sums; the workgroup that finds itself the last
-    // adds them in the parts' order, all read back from memory, so that the sum does
-    // not depend on which is last, and leaves the counter at 0. (The accumulators are
-    // only read here: written on such a path, they spill.)
-    auto join = [&](const ItemA4 &it) {
-        const int first = xcd * kBlocksPerXcd + slot - part, i = xcd * kBlocksPerXcd + slot / parts;
-        if (MOE_BOUNDS_FAIL(first >= 0 && first + parts <= kTailSlots, BOUNDS_TAIL_SLOT)) return;
-        store_sums(first + part);
-        if (tid == 0) {
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-            const bool last = __hip_atomic_fetch_add(p.tail_cnt + i, 1, __ATOMIC_RELAXED,
-                                                     __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
-            if (last) {
-                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-                __hip_atomic_store(p.tail_cnt + i, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            }
-            *flag = last;
-        }
-        __syncthreads();
-        if (!*flag) return;
-        static_assert(kA4Parts == 4, "parts");
-        const auto s0 = sums_of(first), s1 = sums_of(first + 1), s2 = sums_of(first + min(2, parts - 1)),
-                   s3 = sums_of(first + min(3, parts - 1));
-        if (parts == 2) {
-            tile_out(it, [&](int m, int j) {
-                __builtin_amdgcn_sched_barrier(0);  // few loads at a time: registers
-                return stored(s0, m, j) + stored(s1, m, j);
-            });
-            return;
-        }
-        tile_out(it, [&](int m, int j) {
-            __builtin_amdgcn_sched_barrier(0);
-            f32x16 x = stored(s0, m, j) + stored(s1, m, j);
-            __builtin_amdgcn_sched_barrier(0);
-            const f32x16 c = stored(s2, m, j), d = stored(s3, m, j);
-            x += c;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = parts > 3 ? x[e] + d[e] : x[e];
-            return x;
-        });
+    auto tile_out = [&](const ItemA4 &it) {
+        if constexpr (SWIGLU) gate_up_out(it);
+        else down_out(it);
     };
 
     // ---- fill the ring, then the steps of every item ----
@@ -596,7 +507,7 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
     // products, or of the first steps after a stored tile, whose waits let its
     // stores (newer than the copies waited for) be under way
     ItemA4 it = item_at(0);
-    int j = 0, left = it.k1 - it.k0, after = 0;
+    int j = 0, left = nk, after = 0;
     for (;;) {
         int n = min(left, c_left);
         left -= n, c_left -= n;
@@ -610,28 +521,41 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void tiled_a4_kernel(GemmProblem p
         if (left == 0) {
             const bool last = ++j == count;
             if (last) wait_vm<0>();  // the repeated copies land before the workgroup ends
-            if (!it.cut) tile_out(it, [&](int m, int j) { return acc[m][j]; });
-            else join(it);
+            tile_out(it);
             if (last) break;
             after = S - 2;
             clear();
             it = item_at(j);
-            left = it.k1 - it.k0;
+            left = nk;
         }
     }
 }
 
 template <bool SWIGLU, int MI>
+__global__ __launch_bounds__(64 * NW, 1) void tiled_a4_kernel(GemmProblem p, int nN) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[RingA4<MI>::lds > RingA4<1>::lds ? RingA4<MI>::lds : RingA4<1>::lds];
+    const int n_tiles = scalar(*p.n_tiles);
+    const int n_work = n_tiles * nN;
+    const int per = (n_work + kXcds - 1) / kXcds;
+    const int xcd = blockIdx.x % kXcds, slots = gridDim.x / kXcds;
+    const int mine = min(per, n_work - xcd * per);
+    if (mine <= 0) return;
+    const int tail = MI > 1 && cut_tail(mine, slots, (p.K + kA4BK - 1) / kA4BK) ? scalar(mine % slots) : 0;
+    run_items<SWIGLU, MI>(p, nN, n_tiles, Share{xcd * per, mine - tail, 1}, lds);
+    if (tail == 0) return;
+    __syncthreads();
+    run_items<SWIGLU, 1>(p, nN, n_tiles, Share{xcd * per + mine - tail, tail * MI, MI}, lds);
+}
+
+template <bool SWIGLU, int MI>
 hipError_t launch(const GemmProblem &p, hipStream_t s) {
-    constexpr int WR = 2, WC = 4;
-    typedef RingA4<WR, WC, MI> R;
     const int nN = (p.N + (SWIGLU ? 127 : 255)) / (SWIGLU ? 128 : 256);
     const long long items = ((long long)p.max_tiles * nN + kXcds - 1) / kXcds;  // of an XCD, at most
     if (items > 0x0fffffffLL) return hipErrorInvalidValue;
     // one round of resident workgroups, or as many as keep to the item table
     long long slots = kBlocksPerXcd;
     while ((items + slots - 1) / slots > kA4Items) slots += kBlocksPerXcd;
-    hipLaunchKernelGGL((tiled_a4_kernel<SWIGLU, WR, WC, MI>), dim3((unsigned)(slots * kXcds)), dim3(R::threads), 0, s, p, nN);
+    hipLaunchKernelGGL((tiled_a4_kernel<SWIGLU, MI>), dim3((unsigned)(slots * kXcds)), dim3(64 * NW), 0, s, p, nN);
     return hipGetLastError();
 }
 
@@ -645,7 +569,7 @@ int tiled_a4_bm(long long rows, int groups) {
 
 hipError_t launch_tiled_a4(const GemmProblem &p, bool swiglu, int bm, hipStream_t s) {
     if (p.N < 32 || p.N % 32 || p.K < 32 || p.K % 32 || !p.tiles || !p.n_tiles || !p.A || !p.As || p.as_ld < p.M + 256LL ||
-        !p.B0 || !p.S0 || !p.tail_part || !p.tail_cnt || (swiglu && (!p.B1 || !p.S1 || !p.Cq || !p.Cqs || p.cqs_ld < p.M)) || (!swiglu && !p.C))
+        !p.B0 || !p.S0 || (swiglu && (!p.B1 || !p.S1 || !p.Cq || !p.Cqs || p.cqs_ld < p.M)) || (!swiglu && !p.C))
         return hipErrorInvalidValue;
     if (p.extra_group >= 0 && (!p.Bx0 || !p.Sx0 || (swiglu && (!p.Bx1 || !p.Sx1)))) return hipErrorInvalidValue;
     if (p.max_tiles < 1) return hipSuccess;
