@@ -10,7 +10,7 @@
 // PFLOP/s from registers with random codes, this one 6.1 to 6.4; its issue
 // rate allows 9.0, reached with zeros: the clock falls under load.)
 //
-// Tile: BM rows x 256 B-columns x 128 deep; WR x 4 wavefronts, each BM / WR
+// Tile: BM = 64 MI rows x 256 B-columns x 128 deep; 2 x 4 wavefronts, each 32 MI
 // rows x 64 B-columns (MI x 2 blocks).
 //  * gate/up (SWIGLU): B-columns 0..127 are W1[:, n0:n0+128], the rest
 //    W3[:, n0:n0+128]. Wavefront column wc holds both accumulators of output
@@ -33,6 +33,19 @@
 //    each; the 8 rows x 32 bytes of 32 lanes fall into distinct banks.
 //  * K not a multiple of 128: the rows' panels are filled up with zero codes;
 //    the weights' rows past the end are the last one again (times zero).
+//
+// What bounds it. Few rows an expert: the weights' bytes (32 experts of 7168 x 2048,
+// 128 rows each: gate/up 472 MB in 165 us, down 236 + 59 MB in 86). Many: the matrix
+// cores, at the clock that the card holds under them. 8 experts, 8192 rows, H 4096,
+// F 14336: gate/up 525 us, 3.7 PFLOP/s, down 272 us, 3.5; tiles are 12 % larger than
+// the rows, and the matrix cores are busy for 60 % of the cycles at 1.5 to 1.8 GHz. A
+// loop of the same products, LDS reads and a barrier a step reaches 4.8 PFLOP/s cold
+// and 6.0 in the long run, at 1.3 to 1.7 GHz, against 8.7 at 2.4 GHz with zeros. Fewer
+// cycles hence gain little: reads spread over the whole step with a wait for each row
+// block took 5 % of the cycles and nothing of the median time away. 4 wavefronts of
+// 128 x 128, two workgroups a CU of 128 x 256, ranges of equal steps in place of whole
+// items, staggered starts: as fast or slower. Passing over the products of row blocks
+// without rows costs a branch a half step: 610 to 640 us.
 #include "mx4.h"
 #include "tiled_gemm_kernel.h"
 
@@ -76,11 +89,15 @@ struct RingA4 {
 // vector load or a division leaves a loop of exec masks, 15 % slower
 __device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-// Whether an XCD's last round of items, if it leaves half of its workgroups idle, is cut
-// into pieces of 64 rows
-__device__ __forceinline__ bool cut_tail(int n, int slots, int nk) {
+// The items of an XCD's last round, of n, that are cut into `cut` pieces of 64 rows: all of
+// them where the pieces are one round of its workgroups. 8 experts, 8192 rows (4.5 tiles
+// an expert), whole and cut: H 8192, F 2048 330 and 319 us, H 2048, F 8192 288 and 271,
+// H 1024, F 1024 48 and 46; with two rounds of pieces (H 1024, F 4096) 96.5 and 98.
+// (Equal parts over K, their sums joined through memory: as fast as the pieces at K 14336,
+// and nothing below 12 steps a part.)
+__device__ __forceinline__ int cut_tail(int n, int slots, int cut) {
     const int tail = n % slots;
-    return tail > 0 && 2 * tail <= slots && nk >= 16 && slots == kBlocksPerXcd;
+    return cut > 1 && tail * cut <= slots && slots == kBlocksPerXcd ? tail : 0;
 }
 
 template <int OPB, int OPA>
@@ -540,7 +557,7 @@ __global__ __launch_bounds__(64 * NW, 1) void tiled_a4_kernel(GemmProblem p, int
     const int xcd = blockIdx.x % kXcds, slots = gridDim.x / kXcds;
     const int mine = min(per, n_work - xcd * per);
     if (mine <= 0) return;
-    const int tail = MI > 1 && cut_tail(mine, slots, (p.K + kA4BK - 1) / kA4BK) ? scalar(mine % slots) : 0;
+    const int tail = scalar(cut_tail(mine, slots, MI));
     run_items<SWIGLU, MI>(p, nN, n_tiles, Share{xcd * per, mine - tail, 1}, lds);
     if (tail == 0) return;
     __syncthreads();
@@ -562,6 +579,13 @@ hipError_t launch(const GemmProblem &p, hipStream_t s) {
 }  // namespace
 }  // namespace tiled
 
+// Tall tiles read the weights less often from LDS and L2, short ones multiply fewer
+// rows that are not there. 32 experts of 7168 x 2048, the whole FFN in us, tiles of 64 /
+// 128 / 192 / 256 rows: 24 rows an expert 180 / 189 / 218 / 231, 64: 254 / 201 / 232 / 232,
+// 128: 313 / 265 / 241 / 254, 256: 481 / 375 / 369 / 336, 384: 579 / 488 / 458 / 442. Narrow
+// experts (2048 x 1024) lean to shorter tiles, 64 rows an expert 42 / 41 / 44 / 48, 160:
+// 57 / 56 / 51 / 55, 512: 144 / 123 / 106 / 116; with the rows unevenly spread 256 there
+// again (116 against 123 for 192).
 int tiled_a4_bm(long long rows, int groups) {
     const long long avg = rows / groups;
     return avg > 160 ? 256 : avg > 96 ? 192 : avg > 40 ? 128 : 64;
