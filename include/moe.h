@@ -103,7 +103,7 @@ typedef enum {
  *    In moe_forward it needs Fs == 0 or Fs == F.
  *  TILED_A4 (MXFP4 weights only): the expert inputs (token rows, then h) are
  *    quantised to MXFP4 as moe_quantize_mxfp4_rows does and multiplied on the
- *    4-bit matrix cores (W4A4), for any number of rows; h is quantised inside
+ *    4-bit matrix cores (W4A4), for any number of rows (up to 2^30); h is quantised in
  *    the gate/up GEMM, from its fp32 values. AUTO never picks it: it rounds
  *    activations to 4 bits. A row with a NaN or infinity gives NaN outputs. In
  *    moe_forward an MXFP4 shared expert needs Fs == F (a bf16 one does not). */

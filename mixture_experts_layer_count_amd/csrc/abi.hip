@@ -46,7 +46,7 @@ struct FfnPlan {
     bool tiled;
     bool a8;      // tiled with E4M3 activations (W8A8)
     bool a4;      // tiled with MXFP4 rows (W4A4)
-    bool tail;    // tiled with the tail split (bf16 and MXFP4 weights; W4A4, gate/up too)
+    bool tail;    // tiled with the tail split (bf16 and MXFP4 weights)
     int bm;
     int ksplit1;  // split-K of gate/up (row-streaming path; 1: none)
     int kchunk1;
@@ -84,7 +84,7 @@ FfnPlan plan_ffn(int M, int G, int H, int F, moe_dtype w_dt, moe_ffn_path path, 
         p.a8 = p.tiled && can_a8;
     }
     p.bm = p.a4 ? tiled_a4_bm(M, G) : p.a8 ? tiled_a8_bm(M, G) : p.tiled ? tiled_gemm_bm(wt, M, G) : kGemvBM;
-    p.tail = p.tiled && !p.a8 && (w_dt == MOE_BF16 || w_dt == MOE_MXFP4);
+    p.tail = p.tiled && !p.a8 && !p.a4 && (w_dt == MOE_BF16 || w_dt == MOE_MXFP4);
     p.ksplit1 = 1;
     p.kchunk1 = H;
     p.ksplit2 = 1;
@@ -143,8 +143,9 @@ struct ExtraGroup {
 
 // xrows: rows of quantised expert input (W8A8 only). W4A4: the rows of the
 // grouped launches are the first a4_rows; bf16 h is kept for the others only,
-// and the last product's rows and the tail split's sums are moe_forward's only
-// (layer; the latter for its shared expert), the map to a token's rows the other's.
+// room for the last product's rows is moe_forward's (layer), the map from
+// assignments to rows moe_grouped_ffn's.
+constexpr int kMaxA4Rows = 1 << 30;  // rows are counted past the last one in ints
 size_t ffn_ws_carve(Carver &c, FfnWs &w, const FfnPlan &p, int rows, int groups, int H, int hw,
                     moe_dtype act_dt, int xrows, int a4_rows, bool layer) {
     const long long max_tiles = max_tiles_for(rows, groups, p.bm);
@@ -174,7 +175,7 @@ size_t ffn_ws_carve(Carver &c, FfnWs &w, const FfnPlan &p, int rows, int groups,
         w.h4s = static_cast<uint32_t *>(c.take(4 * ph));
         if (!layer) w.row_of4 = static_cast<int32_t *>(c.take(4 * (size_t)a4_rows));
     }
-    if (p.tail && (!p.a4 || layer)) {
+    if (p.tail) {
         w.tail_part = static_cast<float *>(c.take(tiled_tail_bytes(p.bm)));
         w.tail_cnt = static_cast<int32_t *>(c.take(sizeof(int32_t) * tiled_tail_counters));
     }
@@ -316,8 +317,6 @@ void set_h4(GemmProblem &g, const FfnWs &w) {
     g.Cq = w.h4;
     g.Cqs = reinterpret_cast<float *>(w.h4s);
     g.cqs_ld = w.ld4;
-    g.tail_part = w.tail_part;
-    g.tail_cnt = w.tail_cnt;
 }
 
 }  // namespace
@@ -329,7 +328,8 @@ unsigned moe_debug_bounds(void) {
     if (hipDeviceSynchronize() != hipSuccess) return ~0u;
     return bounds_take_tiled128() | bounds_take_tiled256() | bounds_take_tiledf32() | bounds_take_a8() |
            bounds_take_stream() | bounds_take_permute() | bounds_take_combine() | bounds_take_quant() |
-           bounds_take_ep() | bounds_take_persist() | bounds_take_a4() | bounds_take_train_rows() | bounds_take_train_weights();
+           bounds_take_ep() | bounds_take_persist() | bounds_take_a4() |
+           bounds_take_train_rows() | bounds_take_train_weights();
 #else
     return 0u;
 #endif
@@ -511,7 +511,7 @@ moe_status moe_grouped_ffn(const void *Xin, const int32_t *row_src, int k, int M
     if (st != MOE_OK) return st;
     if (!path_ok(path)) return MOE_ERR_INVALID_ARG;
     if (path == MOE_PATH_TILED_A8 && w_dt != MOE_FP8_E4M3) return MOE_ERR_UNSUPPORTED;
-    if (path == MOE_PATH_TILED_A4 && w_dt != MOE_MXFP4) return MOE_ERR_UNSUPPORTED;
+    if (path == MOE_PATH_TILED_A4 && (w_dt != MOE_MXFP4 || M > kMaxA4Rows)) return MOE_ERR_UNSUPPORTED;
     if (M == 0) return MOE_OK;
     if (!Xin || !offsets || !W1 || !W3 || !W2 || !Yp) return MOE_ERR_INVALID_ARG;
     const bool sc = scaled(w_dt);
@@ -684,8 +684,7 @@ ForwardWs carve_forward(const moe_layer_desc *d, int T, void *base) {
     FfnPlan carve = f.plan;
     const bool separate = d->Fs > 0 && !f.combined;
     if (separate && !f.plan.tiled && f.plan_s.ksplit2 > carve.ksplit2) carve.ksplit2 = f.plan_s.ksplit2;
-    ffn_ws_carve(c, f.ffn, carve, rows, groups, d->H, hw, d->act_dt, T, A + (f.combined ? T : 0),
-                 true);
+    ffn_ws_carve(c, f.ffn, carve, rows, groups, d->H, hw, d->act_dt, T, A + (f.combined ? T : 0), true);
     f.part1_s = nullptr;
     if (separate && !f.plan_s.tiled && f.plan_s.ksplit1 > 1)
         f.part1_s = static_cast<float *>(c.take(sizeof(float) * (size_t)f.plan_s.ksplit1 * T * 2 * d->Fs));

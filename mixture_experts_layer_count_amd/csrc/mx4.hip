@@ -1,7 +1,11 @@
 // MXFP4 quantisation of rows and of weight matrices, and reading them back
 // (format: mx4.h).
 //
-// HBM-bound: 2 (fp32: 4) bytes a value in, 17/32 out, and the reverse.
+// HBM-bound: 2 (fp32: 4) bytes a value in, 17/32 out, and the reverse. A value's
+// arithmetic is about one instruction (a conversion takes two values and the packed
+// maximum two), so bf16 stays in pairs as it lies in memory. bf16, at the copy's rate of
+// 4.5 TB/s or above: rows 32768 x 4096 62-78 us and back 58 (339 MB), weights 8 x 4096 x
+// 14336 254 us (4.7 TB/s) and back 193 (6.2, most of it written).
 #include "mx4.h"
 #include "schedule.h"
 #include "train.h"
@@ -356,15 +360,17 @@ hipError_t launch_mx4_panels(const Mx4Panels &p, const TilesJob *tiles, hipStrea
     const long long rows = (long long)p.rows + p.extra;
     if (rows == 0 && !tiles) return hipSuccess;
     const int np = panels(p.C);
-    // few rows: one a thread, for more workgroups
-    const bool few = (rows + 63) / 64 * np < 2048;
+    // few blocks of 64 rows and a panel: a row a thread, for more workgroups (H 2048, 256
+    // blocks: 3.4 against 5.1 us with four, 1024: 7.6 and 8.1, 4096: 17.5 and 16.5)
+    const long long work = (rows + 63) / 64 * np;
+    const bool few = work <= 1024;
     const TilesJob job = tiles ? *tiles : TilesJob{};
     const Divide token(p.gk);
     const dim3 block(1024);
     // 65536 rows of 8192 tokens, C 2048: 53 us by row (268 MB of tokens read from beyond
     // the L2s, at 5 TB/s), 37 + 6 for row_of by token. 8192 rows of 4096 tokens, C 4096: 21
-    // by row, 20 + 5 by token
-    if (!few && p.row_src && p.gk >= 4 && (p.row_of || p.scratch)) {
+    // by row, 20 + 5 by token. The launch for row_of takes 5 us or more
+    if (p.row_src && p.gk >= 4 && (p.row_of ? !few : p.scratch && work >= 8192)) {
         Mx4Panels q = p;
         if (!q.row_of) {
             const long long n = (rows + 1023) / 1024;
