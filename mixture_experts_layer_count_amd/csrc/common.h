@@ -57,7 +57,6 @@ unsigned bounds_take_combine();
 unsigned bounds_take_quant();
 unsigned bounds_take_ep();
 unsigned bounds_take_persist();
-unsigned bounds_take_a4();
 
 // ---------------------------------------------------------------------------
 // Vector types for MFMA operands and wide loads
@@ -232,13 +231,6 @@ constexpr int tiled_tail_counters = 256;
 hipError_t launch_tiled_a8(const GemmProblem &p, bool swiglu, int bm, hipStream_t s);
 int tiled_a8_bm(long long rows, int groups);  // rows per W8A8 tile (160)
 bool tiled_a8_supports(int N, int K);
-
-// W4A4 variant (MXFP4 weights and MXFP4 rows): A holds the rows' panels and As
-// their scale words, as_ld = cqs_ld their rows a panel (at least M + 256: whole
-// tiles are read); output bf16, or h as panels of Cq and Cqs words (gate/up).
-// Tiles of bm = tiled_a4_bm(rows, groups) rows.
-hipError_t launch_tiled_a4(const GemmProblem &p, bool swiglu, int bm, hipStream_t s);
-int tiled_a4_bm(long long rows, int groups);
 
 // E4M3 quantisation of bf16 rows: for each row and 128-column group,
 // s = amax / 448 (1 when amax is 0), q = E4M3(x / s) rounded to nearest even

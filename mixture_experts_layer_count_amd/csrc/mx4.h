@@ -113,4 +113,12 @@ struct Mx4Panels {
 struct TilesJob;
 hipError_t launch_mx4_panels(const Mx4Panels &p, const TilesJob *tiles, hipStream_t s);
 
+// The grouped product of MXFP4 weights and MXFP4 rows (tiled_a4.hip): A holds the rows'
+// panels and As their scale words, as_ld = cqs_ld their rows a panel (at least M + 256:
+// whole tiles are read); output bf16, or h as panels of Cq and Cqs words (gate/up).
+// Tiles of bm = tiled_a4_bm(rows, groups) rows.
+hipError_t launch_tiled_a4(const GemmProblem &p, bool swiglu, int bm, hipStream_t s);
+int tiled_a4_bm(long long rows, int groups);
+unsigned bounds_take_a4();  // bounds-checked build
+
 }  // namespace moe
