@@ -103,9 +103,10 @@ typedef enum {
  *    In moe_forward it needs Fs == 0 or Fs == F.
  *  TILED_A4 (MXFP4 weights only): the expert inputs (token rows, then h) are
  *    quantised to MXFP4 as moe_quantize_mxfp4_rows does and multiplied on the
- *    4-bit matrix cores (W4A4), for any number of rows (up to 2^30); h is quantised in
- *    the gate/up GEMM, from its fp32 values. AUTO never picks it: it rounds
- *    activations to 4 bits. A row with a NaN or infinity gives NaN outputs. In
+ *    4-bit matrix cores (W4A4), for any number of rows (up to 2^30); h is
+ *    quantised inside the gate/up GEMM, from its fp32 values. AUTO never picks
+ *    it: it rounds activations to 4 bits. A row with a NaN or infinity gives
+ *    NaN outputs. Rows, outputs and codes 16-byte aligned, scales 4-byte. In
  *    moe_forward an MXFP4 shared expert needs Fs == F (a bf16 one does not). */
 typedef enum {
     MOE_PATH_AUTO = 0,
@@ -283,7 +284,7 @@ enum {
     MOE_EV_START = 0,
     MOE_EV_ROUTE,          /* router GEMM + top-k done */
     MOE_EV_PERMUTE,        /* counts / offsets / permutation done */
-    MOE_EV_SCHEDULE,       /* tile list built (and, on TILED_A8, X quantised) */
+    MOE_EV_SCHEDULE,       /* tile list built (on TILED_A8, TILED_A4: X quantised) */
     MOE_EV_GATE_UP,        /* routed gate/up GEMM + SwiGLU done (TILED_A8: h written as E4M3) */
     MOE_EV_SHARED_GATE_UP, /* shared expert gate/up done (no-op without one) */
     MOE_EV_DOWN,           /* routed down projection done */

@@ -250,6 +250,8 @@ def grouped_ffn(Xin, offsets, W1, W3, W2, S1=None, S3=None, S2=None, row_src=Non
         Yp = out
     p = PATHS[path]
     if path == "tiled_a4" and wdt == MOE_MXFP4:
+        if S1 is None or S3 is None or S2 is None:
+            raise ValueError("MXFP4 weights need S1, S3 and S2")
         for t, n, shape in ((W3, "W3", W1.shape), (W2, "W2", (G, F // 2, H)), (S1, "S1", (G, H // 32, F)),
                             (S3, "S3", (G, H // 32, F)), (S2, "S2", (G, F // 32, H))):
             _want(t, n, shape, torch.uint8, Xin.device)

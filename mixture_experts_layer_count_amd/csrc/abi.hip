@@ -3,6 +3,8 @@
 // here synchronises with the device or allocates device memory.
 #include <string.h>
 
+#include <initializer_list>
+
 #include "abi_util.h"
 #include "common.h"
 #include "mx4.h"
@@ -306,7 +308,16 @@ void set_a8(GemmProblem &g, const uint8_t *q, const float *sc, int width, int ro
     g.as_ld = rows;
 }
 
-// W4A4 operands: the rows' panels and scale words
+// W4A4: what its copies and stores need: rows and codes on 16 bytes, scales on 4 (a NULL
+// passes)
+bool a4_aligned(std::initializer_list<const void *> wide, std::initializer_list<const void *> words) {
+    for (const void *p : wide)
+        if (reinterpret_cast<uintptr_t>(p) & 15) return false;
+    for (const void *p : words)
+        if (reinterpret_cast<uintptr_t>(p) & 3) return false;
+    return true;
+}
+// its operands: the rows' panels and scale words
 void set_a4(GemmProblem &g, const uint8_t *q, const uint32_t *sc, long long ld) {
     g.A = q;
     g.As = reinterpret_cast<const float *>(sc);
@@ -518,6 +529,7 @@ moe_status moe_grouped_ffn(const void *Xin, const int32_t *row_src, int k, int M
     if (sc != (S1 != nullptr) || sc != (S3 != nullptr) || sc != (S2 != nullptr))
         return MOE_ERR_INVALID_ARG;
     const FfnPlan p = plan_ffn(M, G, H, F, w_dt, path);
+    if (p.a4 && !a4_aligned({Xin, W1, W3, W2, Yp}, {S1, S3, S2})) return MOE_ERR_UNSUPPORTED;
     if ((path == MOE_PATH_TILED || path == MOE_PATH_TILED_A8) && !p.tiled) return MOE_ERR_UNSUPPORTED;
     if (!ws || ws_bytes < moe_grouped_ffn_workspace_bytes(M, G, H, F, act_dt, w_dt, path))
         return MOE_ERR_WORKSPACE_TOO_SMALL;
@@ -714,6 +726,9 @@ moe_status moe_forward(const moe_layer_desc *d, const void *X, int T, void *Y, v
     if (T == 0) return MOE_OK;
     if (!X || !Y) return MOE_ERR_INVALID_ARG;
     ForwardWs f = carve_forward(d, T, ws);
+    if (f.plan.a4 && !a4_aligned({X, d->W1, d->W3, d->W2, d->Ws1, d->Ws3, d->Ws2},
+                                 {d->S1, d->S3, d->S2, d->Ss1, d->Ss3, d->Ss2}))
+        return MOE_ERR_UNSUPPORTED;
     if (!ws || ws_bytes < f.bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
     if (logits_out) f.logits = logits_out;
     if (topk_idx_out) f.idx = topk_idx_out;

@@ -67,6 +67,22 @@ def test_a4_path_validation():
     assert ws(m, g, h, f, BF16, MXFP4, 0) == ws(m, g, h, f, BF16, MXFP4, 2)
 
 
+def test_a4_alignment_and_limits():
+    lib = moe.lib()
+    big = dict(ws_bytes=1 << 60, path=A4, **MX)
+    for n in ("Xin", "W1", "W3", "W2", "Yp"):
+        assert _ffn(lib, **big | {n: HALF}) == UNSUPPORTED
+    for n in ("S1", "S3", "S2"):
+        assert _ffn(lib, **big | {n: ctypes.c_void_p(0x1002)}) == UNSUPPORTED
+    assert _ffn(lib, **big | dict(M=(1 << 30) + 1)) == UNSUPPORTED
+    d = dict(H=512, F=1024, w_dt=MXFP4, S1=0x1000, S3=0x1000, S2=0x1000, path=A4)
+    forward = lambda X=FAKE, **kw: lib.moe_forward(  # noqa: E731
+        ctypes.byref(_desc(**d | kw)), X, 100, FAKE, None, 0, None, None, None, None, None, None)
+    assert forward() == WS_SMALL
+    assert forward(HALF) == UNSUPPORTED and forward(W1=0x1008) == UNSUPPORTED and forward(S2=0x1001) == UNSUPPORTED
+    assert lib.moe_quantize_mxfp4_rows(FAKE, BF16, 1 << 62, 1 << 62, 64, FAKE, FAKE, None) == UNSUPPORTED
+
+
 def test_a4_layer_validation():
     ws = moe.lib().moe_forward_workspace_bytes
     mx = dict(H=512, F=1024, w_dt=MXFP4, S1=0x1000, S3=0x1000, S2=0x1000, path=A4)
