@@ -112,6 +112,57 @@ __global__ __launch_bounds__(BS) void combine_back_kernel(CombineBack p) {
     }
 }
 
+// ---- combine of short rows: L lanes a token, a unit each, 256 / L tokens a workgroup;
+// four of a token's rows in flight ----
+template <typename E, int V, int L>
+__global__ __launch_bounds__(256) void combine_back_short_kernel(CombineBack p) {
+    const long long t = (long long)blockIdx.x * (256 / L) + threadIdx.x / L;
+    if (t >= p.T) return;  // a token's lanes together
+    const int lane = threadIdx.x % L, M = p.n_rows ? min(p.T * p.k, *p.n_rows) : p.T * p.k;
+    const bool in = lane * V < p.H;
+    const int c = in ? lane * V : 0;  // others read the row's first unit, which counts for nothing
+    const E *Yp = reinterpret_cast<const E *>(p.Yp) + c;
+    E *dYp = reinterpret_cast<E *>(p.dYp) + c;
+    const Unit<E, V> d = load<E, V>(reinterpret_cast<const E *>(p.dY) + t * p.H + c);
+    for (int j0 = 0; j0 < p.k; j0 += 4) {
+        int r[4];
+        float w[4], dot[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const long long a = t * p.k + j0 + u;
+            r[u] = j0 + u < p.k ? p.assign_row[a] : -1;
+            w[u] = j0 + u < p.k && p.dYp ? p.w[a] : 0.0f;
+            if (r[u] >= M) r[u] = -1;
+        }
+        Unit<E, V> y[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            y[u] = Unit<E, V>{};
+            if (p.dw && r[u] >= 0) y[u] = load<E, V>(Yp + (long long)r[u] * p.H);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            dot[u] = 0.0f;
+            float v[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                dot[u] = fmaf(y[u][i], d[i], dot[u]);
+                v[i] = w[u] * d[i];
+            }
+            if (!in || r[u] < 0) dot[u] = 0.0f;
+            else if (p.dYp) store<E, V>(dYp + (long long)r[u] * p.H, v);
+        }
+        if (!p.dw) continue;
+#pragma unroll
+        for (int x = L / 2; x >= 1; x >>= 1)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) dot[u] += __shfl_xor(dot[u], x);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (lane == 0 && j0 + u < p.k) p.dw[t * p.k + j0 + u] = dot[u];
+    }
+}
+
 // ---- permute: a thread a unit of a token's row; up to 8 rows in flight ----
 template <typename E, int V>
 __global__ __launch_bounds__(256) void permute_back_kernel(PermuteBack p, long long threads) {
@@ -155,14 +206,23 @@ hipError_t combine_back(const CombineBack &p, hipStream_t s) {
     hipLaunchKernelGGL((combine_back_kernel<E, V, BS, U>), dim3((unsigned)p.T), dim3(BS), 0, s, p);
     return hipGetLastError();
 }
+template <typename E, int V, int L>
+hipError_t combine_back_short(const CombineBack &p, hipStream_t s) {
+    hipLaunchKernelGGL((combine_back_short_kernel<E, V, L>), dim3((unsigned)((p.T + 256 / L - 1) / (256 / L))), dim3(256),
+                       0, s, p);
+    return hipGetLastError();
+}
 template <typename E, int V>
 hipError_t combine_back(const CombineBack &p, hipStream_t s) {
-    // One wavefront for short rows, else four, with one unit a thread or more. bf16, 8192
-    // tokens, k 8, us: H 512 24 (four wavefronts 45), H 1024 52 (two units a thread; two
-    // wavefronts 59, four 78), H 2048 118 (two units 126, one wavefront 137), H 4096 half
-    // the tokens 118 (one unit 120, four 130); 64 tokens, k 8, H 7168 15 with four units, 18
-    // with two, 25 with one
-    if (p.H <= 64 * V) return combine_back<E, V, 64, 1>(p, s);
+    // 32768 tokens, k 8, bf16, against a wavefront and workgroup a token: H 32 9.5 and 45 us,
+    // H 128 24 and 47, H 512 113 and 118
+    if (p.H <= 8 * V) return combine_back_short<E, V, 8>(p, s);
+    if (p.H <= 16 * V) return combine_back_short<E, V, 16>(p, s);
+    if (p.H <= 32 * V) return combine_back_short<E, V, 32>(p, s);
+    if (p.H <= 64 * V) return combine_back_short<E, V, 64>(p, s);
+    // bf16, 8192 tokens, k 8, us: H 1024 52 (two wavefronts 59, four 78), H 2048 118 (two
+    // units a thread 126, one wavefront 137), H 4096 half the tokens 118 (one unit 120,
+    // four 130); 64 tokens, k 8, H 7168 15 with four units, 18 with two, 25 with one
     if (p.H <= 128 * V) return combine_back<E, V, 64, 2>(p, s);
     if (p.H <= 256 * V) return combine_back<E, V, 256, 1>(p, s);
     if (p.H <= 512 * V) return combine_back<E, V, 256, 2>(p, s);

@@ -35,7 +35,7 @@
 //    the weights' rows past the end are the last one again (times zero).
 //
 // What bounds it. Few rows an expert: the weights' bytes (32 experts of 7168 x 2048,
-// 128 rows each: gate/up 472 MB in 165 us, down 236 + 59 MB in 86). Many: the matrix
+// 128 rows each: gate/up 499 MB in 165 us, down 250 + 59 MB in 86). Many: the matrix
 // cores, at the clock that the card holds under them. 8 experts, 8192 rows, H 4096,
 // F 14336: gate/up 525 us, 3.7 PFLOP/s, down 272 us, 3.5; tiles are 12 % larger than
 // the rows, and the matrix cores are busy for 60 % of the cycles at 1.5 to 1.8 GHz. A

@@ -60,7 +60,8 @@ def _check(d, got, dX, add, n=None):
 @pytest.mark.parametrize("T,E,k,H,dt", [(1, 1, 1, 4, BF), (1, 8, 2, 4096, BF), (7, 4, 3, 12, BF), (7, 4, 3, 12, F32),
                                         (33, 8, 2, 520, BF), (64, 8, 8, 516, BF), (100, 16, 5, 1028, F32), (300, 12, 4, 2048, BF),
                                         (129, 64, 8, 7168, BF), (65, 128, 64, 64, BF), (40, 60, 7, 9000, F32), (9, 4, 2, 20480, BF),
-                                        (5, 4, 2, 16, BF), (2000, 256, 8, 72, F32)])
+                                        (5, 4, 2, 16, BF), (2000, 256, 8, 72, F32), (77, 16, 6, 104, BF), (51, 8, 5, 504, BF),
+                                        (30, 8, 3, 240, F32), (33, 8, 4, 1000, BF)])
 def test_gradients(T, E, k, H, dt):
     say(f"[dispatch] T={T} E={E} k={k} H={H} {dt}")
     d = _case(T, E, k, H, dt, T + H)
