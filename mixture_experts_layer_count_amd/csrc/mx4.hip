@@ -4,7 +4,7 @@
 // HBM-bound: 2 (fp32: 4) bytes a value in, 17/32 out, and the reverse. A value's
 // arithmetic is about one instruction (a conversion takes two values and the packed
 // maximum two), so bf16 stays in pairs as it lies in memory. bf16, at the copy's rate of
-// 4.5 TB/s or above: rows 32768 x 4096 62-78 us and back 58 (339 MB), weights 8 x 4096 x
+// 4.5 TB/s or above: rows 32768 x 4096 62-78 us and back 56 (339 MB), weights 8 x 4096 x
 // 14336 254 us (4.7 TB/s) and back 193 (6.2, most of it written).
 #include "mx4.h"
 #include "schedule.h"
@@ -66,45 +66,51 @@ __global__ __launch_bounds__(256) void mx4_rows_kernel(const void *X, long long 
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-// the eight values of a code word, times the scale
-__device__ __forceinline__ void values8(uint32_t w, float s, float (&v)[8]) {
-    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 0);
-    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 1);
-    const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 2);
-    const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 3);
-    v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1], v[4] = c[0], v[5] = c[1], v[6] = d[0], v[7] = d[1];
-}
 // the NaN scale of a group, applied by the caller (the conversions read
 // exponent 255 as a power of two)
 __device__ __forceinline__ float nan_if(uint32_t byte, float x) {
     return byte == 255u ? __uint_as_float(0x7fc00000u) : x;
 }
 
+// 16 bytes of values: 8 of bf16, 4 of fp32
 template <bool F32>
-__device__ __forceinline__ void store8(void *Y, long long o, const float (&v)[8]) {
-    if constexpr (F32) {
-        f32x4 *p = reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(Y) + o);
-        p[0] = f32x4{v[0], v[1], v[2], v[3]};
-        p[1] = f32x4{v[4], v[5], v[6], v[7]};
-    } else {
+__device__ __forceinline__ void store16(void *Y, long long o, const float *v) {
+    if constexpr (F32)
+        *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(Y) + o) = f32x4{v[0], v[1], v[2], v[3]};
+    else
         *reinterpret_cast<u32x4 *>(reinterpret_cast<uint16_t *>(Y) + o) =
             u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
-    }
 }
+template <bool F32>
+constexpr int kBack = F32 ? 4 : 8;  // values of a store
 
+// A store of 16 bytes a lane, a wavefront's one after the other, and 16 / kBack of them a
+// thread: 16384 x 7168 fp32 89 us, bf16 52 (16 consecutive values a thread: 148, 55)
 template <bool F32>
 __global__ __launch_bounds__(256) void mx4_rows_back_kernel(const uint8_t *Q, const uint8_t *S, long long n, void *Y) {
-    const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * kPer;
-    if (i >= n) return;
-    const u32x2 q = *reinterpret_cast<const u32x2 *>(Q + i / 2);
-    const uint32_t b = S[i / kGroup];
+    constexpr int U = kBack<F32>;
+    const long long base = (long long)blockIdx.x * 256 * kPer + threadIdx.x * U;
+    uint32_t q[kPer / U], b[kPer / U];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float v[8];
-        values8(q[h], scale_of(b), v);
+    for (int u = 0; u < kPer / U; ++u) {
+        const long long i = base + u * 256 * U;
+        q[u] = b[u] = 0;
+        if (i >= n) continue;
+        if constexpr (F32) q[u] = *reinterpret_cast<const uint16_t *>(Q + i / 2);
+        else q[u] = *reinterpret_cast<const uint32_t *>(Q + i / 2);
+        b[u] = S[i / kGroup];
+    }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = nan_if(b, v[j]);
-        store8<F32>(Y, i + 8 * h, v);
+    for (int u = 0; u < kPer / U; ++u) {
+        const long long i = base + u * 256 * U;
+        const f32x2 x[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], scale_of(b[u]), 0),
+                            __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], scale_of(b[u]), 1),
+                            __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], scale_of(b[u]), 2),
+                            __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], scale_of(b[u]), 3)};
+        float v[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) v[j] = nan_if(b[u], x[j / 2][j & 1]);
+        if (i < n) store16<F32>(Y, i, v);
     }
 }
 
@@ -199,29 +205,31 @@ __global__ __launch_bounds__(256) void mx4_weights_kernel(const void *W, long lo
 template <bool F32>
 __global__ __launch_bounds__(256) void mx4_weights_back_kernel(const uint8_t *Q, const uint8_t *S, long long threads,
                                                                int N, void *W) {
+    constexpr int U = kBack<F32>, kWords = U / 4;  // columns a thread
+    typedef uint32_t Words __attribute__((ext_vector_type(kWords)));
     const long long t = (long long)blockIdx.x * 256 + threadIdx.x;
     if (t >= threads) return;
-    const int per = N / 8;
+    const int per = N / U;
     const long long g = t / per;
-    const int c = (int)(t - g * per) * 8;
-    u32x2 q[16];
+    const int c = (int)(t - g * per) * U;
+    Words q[16];
 #pragma unroll
-    for (int r = 0; r < 16; ++r) q[r] = *reinterpret_cast<const u32x2 *>(Q + (16 * g + r) * N + c);
-    const u32x2 sw = *reinterpret_cast<const u32x2 *>(S + g * N + c);
-    uint32_t b[8];
+    for (int r = 0; r < 16; ++r) q[r] = *reinterpret_cast<const Words *>(Q + (16 * g + r) * N + c);
+    const Words sw = *reinterpret_cast<const Words *>(S + g * N + c);
+    uint32_t b[U];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) b[j] = sw[j >> 2] >> (8 * (j & 3)) & 255u;
+    for (int j = 0; j < U; ++j) b[j] = sw[j >> 2] >> (8 * (j & 3)) & 255u;
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-        float lo[8], hi[8];
+        float lo[U], hi[U];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < U; ++j) {
             const f32x2 x = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[r][j >> 2] >> (8 * (j & 3)), scale_of(b[j]), 0);
             lo[j] = nan_if(b[j], x[0]);
             hi[j] = nan_if(b[j], x[1]);
         }
-        store8<F32>(W, (32 * g + 2 * r) * N + c, lo);
-        store8<F32>(W, (32 * g + 2 * r + 1) * N + c, hi);
+        store16<F32>(W, (32 * g + 2 * r) * N + c, lo);
+        store16<F32>(W, (32 * g + 2 * r + 1) * N + c, hi);
     }
 }
 
@@ -487,7 +495,7 @@ moe_status moe_dequantize_mxfp4_weights(const uint8_t *Q, const uint8_t *S, int 
     if (G == 0) return MOE_OK;
     if (!Q || !S || !W) return MOE_ERR_INVALID_ARG;
     if (off8(Q) || off8(S) || off16(W)) return MOE_ERR_UNSUPPORTED;
-    const long long threads = (long long)G * (K / 32) * (N / 8);
+    const long long threads = (long long)G * (K / 32) * (N / (w_dt == MOE_F32 ? kBack<true> : kBack<false>));
     const dim3 grid((unsigned)((threads + 255) / 256));
     if (w_dt == MOE_F32)
         hipLaunchKernelGGL(mx4_weights_back_kernel<true>, grid, dim3(256), 0, stream, Q, S, threads, N, W);
