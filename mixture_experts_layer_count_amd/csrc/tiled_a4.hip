@@ -136,7 +136,15 @@ __device__ __forceinline__ void run_items(const GemmProblem &p, int nN, int n_ti
         int g = 0, r0 = 0, r1 = 0, mt, nt = 0;
         if (lane < count) {
             const int item = slot + slots * lane, piece = item % share.cut;
-            tile_of(p, nN, n_tiles, share.first + item / share.cut, mt, nt);
+            const int id = share.first + item / share.cut;
+            // one round of about a tile an expert: no rows share weights, and the work order's
+            // two dependent loads (0.6 us of 8) are spared
+            if (n_tiles <= p.n_groups && n_tiles * nN <= slots * kXcds) {
+                mt = id / nN;
+                nt = id - mt * nN;
+            } else {
+                tile_of(p, nN, n_tiles, id, mt, nt);
+            }
             const bool ok = mt < p.max_tiles;
             if (ok) g = p.tiles[4 * mt], r0 = p.tiles[4 * mt + 1], r1 = p.tiles[4 * mt + 2];
             if (MOE_BOUNDS_FAIL(ok && g >= 0 && g < p.n_groups && r0 >= 0 && r0 < r1 && r1 <= p.M, BOUNDS_TILE)) {
