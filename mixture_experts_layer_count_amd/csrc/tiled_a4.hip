@@ -34,8 +34,9 @@
 //  * K not a multiple of 128: the rows' panels are filled up with zero codes;
 //    the weights' rows past the end are the last one again (times zero).
 //
-// What bounds it. Few rows an expert: the weights' bytes (32 experts of 7168 x 2048,
-// 128 rows each: gate/up 499 MB in 165 us, down 250 + 59 MB in 86). Many: the matrix
+// What bounds it. Few rows an expert: the weights' bytes (32 experts of 7168 x 2048, 8
+// rows each: gate/up 499 MB in 108 us, down 250 MB in 56; 120 rows: 135 and 83; 128 on
+// average, 6 to 592, 2.5 rounds of tiles: 166 and 90). Many: the matrix
 // cores, at the clock that the card holds under them. 8 experts, 8192 rows, H 4096,
 // F 14336: gate/up 525 us, 3.7 PFLOP/s, down 272 us, 3.5; tiles are 12 % larger than
 // the rows, and the matrix cores are busy for 60 % of the cycles at 1.5 to 1.8 GHz. A
@@ -89,17 +90,6 @@ struct RingA4 {
 // vector load or a division leaves a loop of exec masks, 15 % slower
 __device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-// The items of an XCD's last round, of n, that are cut into `cut` pieces of 64 rows: all of
-// them where the pieces are one round of its workgroups. 8 experts, 8192 rows (4.5 tiles
-// an expert), whole and cut: H 8192, F 2048 330 and 319 us, H 2048, F 8192 288 and 271,
-// H 1024, F 1024 48 and 46; with two rounds of pieces (H 1024, F 4096) 96.5 and 98.
-// (Equal parts over K, their sums joined through memory: as fast as the pieces at K 14336,
-// and nothing below 12 steps a part.)
-__device__ __forceinline__ int cut_tail(int n, int slots, int cut) {
-    const int tail = n % slots;
-    return cut > 1 && tail * cut <= slots && slots == kBlocksPerXcd ? tail : 0;
-}
-
 template <int OPB, int OPA>
 __device__ __forceinline__ f32x16 mfma4(const i32x4 &b, const i32x4 &a, const f32x16 &c, int sb, int sa) {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(i32x8{b[0], b[1], b[2], b[3], 0, 0, 0, 0},
@@ -109,11 +99,32 @@ __device__ __forceinline__ f32x16 mfma4(const i32x4 &b, const i32x4 &a, const f3
 struct ItemA4 {
     int g, row0, row_end, n0;
 };
-// A workgroup's items: number slot + i slots of `n` for i < .., each 64 MI rows of tile
-// first + number / cut (cut > 1: piece number % cut of it; a piece without rows is dropped)
+// A workgroup's items: first + slot + i slots < first + n for i = 0, 1, .., or piece
+// `piece` (64 MI rows) of item `first` alone (n: 1, or 0 for none)
 struct Share {
-    int first, n, cut;
+    int first, n, piece;
 };
+
+// The work order's item `id`: its rows and its column tile
+__device__ __forceinline__ void item_rows(const GemmProblem &p, int nN, int n_tiles, int slots, int id, int &g, int &r0,
+                                          int &r1, int &nt) {
+    int mt;
+    // one round of about a tile an expert: no rows share weights, and the work order's
+    // two dependent loads (0.6 us of 8) are spared
+    if (n_tiles <= p.n_groups && n_tiles * nN <= slots * kXcds) {
+        mt = id / nN;
+        nt = id - mt * nN;
+    } else {
+        tile_of(p, nN, n_tiles, id, mt, nt);
+    }
+    const bool ok = mt < p.max_tiles;
+    g = ok ? p.tiles[4 * mt] : 0, r0 = ok ? p.tiles[4 * mt + 1] : 0, r1 = ok ? p.tiles[4 * mt + 2] : 0;
+    if (MOE_BOUNDS_FAIL(ok && g >= 0 && g < p.n_groups && r0 >= 0 && r0 < r1 && r1 <= p.M, BOUNDS_TILE)) {
+        g = 0;
+        r0 = 0;
+        r1 = 1;
+    }
+}
 
 template <bool SWIGLU, int MI>
 __device__ __forceinline__ void run_items(const GemmProblem &p, int nN, int n_tiles, const Share &share, uint8_t *lds) {
@@ -130,37 +141,20 @@ __device__ __forceinline__ void run_items(const GemmProblem &p, int nN, int n_ti
     const int slot = blockIdx.x / kXcds, slots = gridDim.x / kXcds;
 
     // ---- this workgroup's items ----
-    int count = slot < share.n ? scalar((share.n - slot + slots - 1) / slots) : 0;
+    const bool alone = share.piece >= 0;
+    int count = alone ? share.n : slot < share.n ? scalar((share.n - slot + slots - 1) / slots) : 0;
     if (MOE_BOUNDS_FAIL(count <= kA4Items, BOUNDS_TILE)) return;
     {
-        int g = 0, r0 = 0, r1 = 0, mt, nt = 0;
+        int g, r0 = 0, r1 = 0, nt;
         if (lane < count) {
-            const int item = slot + slots * lane, piece = item % share.cut;
-            const int id = share.first + item / share.cut;
-            // one round of about a tile an expert: no rows share weights, and the work order's
-            // two dependent loads (0.6 us of 8) are spared
-            if (n_tiles <= p.n_groups && n_tiles * nN <= slots * kXcds) {
-                mt = id / nN;
-                nt = id - mt * nN;
-            } else {
-                tile_of(p, nN, n_tiles, id, mt, nt);
-            }
-            const bool ok = mt < p.max_tiles;
-            if (ok) g = p.tiles[4 * mt], r0 = p.tiles[4 * mt + 1], r1 = p.tiles[4 * mt + 2];
-            if (MOE_BOUNDS_FAIL(ok && g >= 0 && g < p.n_groups && r0 >= 0 && r0 < r1 && r1 <= p.M, BOUNDS_TILE)) {
-                g = 0;
-                r0 = 0;
-                r1 = 1;
-            }
-            if (share.cut > 1) {
-                r0 += R::BM * piece;
+            item_rows(p, nN, n_tiles, slots, share.first + (alone ? 0 : slot + slots * lane), g, r0, r1, nt);
+            if (alone) {
+                r0 += R::BM * share.piece;
                 r1 = min(r1, r0 + R::BM);
             }
+            if (w == 0) *reinterpret_cast<i32x4 *>(table + 4 * lane) = i32x4{g, r0, r1, nt * W};
         }
-        const unsigned long long some = __ballot(r0 < r1);
-        if (w == 0 && r0 < r1)
-            *reinterpret_cast<i32x4 *>(table + 4 * __popcll(some & ((1ULL << lane) - 1))) = i32x4{g, r0, r1, nt * W};
-        count = scalar(__popcll(some));
+        count = scalar(__popcll(__ballot(r0 < r1)));  // 0: a piece without rows
     }
     __syncthreads();
     if (count == 0) return;
@@ -565,11 +559,43 @@ __global__ __launch_bounds__(64 * NW, 1) void tiled_a4_kernel(GemmProblem p, int
     const int xcd = blockIdx.x % kXcds, slots = gridDim.x / kXcds;
     const int mine = min(per, n_work - xcd * per);
     if (mine <= 0) return;
-    const int tail = scalar(cut_tail(mine, slots, MI));
-    run_items<SWIGLU, MI>(p, nN, n_tiles, Share{xcd * per, mine - tail, 1}, lds);
+    const int first = xcd * per, slot = blockIdx.x / kXcds;
+    // The items of the last round are cut into pieces of 64 rows where those are one round of
+    // the XCD's workgroups. 8 experts, 8192 rows (4.5 tiles an expert), whole and cut: H 8192,
+    // F 2048 330 and 319 us, H 2048, F 8192 288 and 271, H 1024, F 1024 48 and 46; with two
+    // rounds of pieces (H 1024, F 4096) 96.5 and 98. 32 experts of 7168 x 2048, 6 to 592 rows:
+    // gate/up 172 us with pieces counted as if tiles were full, 166 with those that have rows.
+    // (Equal parts over K, their sums joined through memory: as fast at K 14336, and nothing
+    // below 12 steps a part.)
+    int tail = MI > 1 && slots == kBlocksPerXcd ? scalar(mine % slots) : 0;
+    Share cut{0, 0, 0};
+    if (tail > 0) {
+        const int lane = threadIdx.x & 63;
+        int rows = MI * 64;  // a single round: as if all tiles were full, which needs no lookup
+        if (mine > slots && lane < tail) {
+            int g, r0, r1, nt;
+            item_rows(p, nN, n_tiles, slots, first + mine - tail + lane, g, r0, r1, nt);
+            rows = r1 - r0;
+        }
+        const int n = lane < tail ? (rows + 63) / 64 : 0;
+        int end = n;  // pieces up to this item's last
+#pragma unroll
+        for (int x = 1; x < kBlocksPerXcd; x <<= 1) {
+            const int y = __shfl_up(end, x);
+            if (lane >= x) end += y;
+        }
+        const unsigned long long mine_is = __ballot(slot < end && slot >= end - n);
+        if (scalar(__shfl(end, kBlocksPerXcd - 1)) > slots) {
+            tail = 0;
+        } else if (mine_is) {
+            const int i = scalar(__ffsll((long long)mine_is) - 1);
+            cut = Share{first + mine - tail + i, 1, scalar(slot - __shfl(end - n, i))};
+        }
+    }
+    run_items<SWIGLU, MI>(p, nN, n_tiles, Share{first, mine - tail, -1}, lds);
     if (tail == 0) return;
     __syncthreads();
-    run_items<SWIGLU, 1>(p, nN, n_tiles, Share{xcd * per + mine - tail, tail * MI, MI}, lds);
+    run_items<SWIGLU, 1>(p, nN, n_tiles, cut, lds);
 }
 
 template <bool SWIGLU, int MI>
