@@ -294,6 +294,35 @@ def test_ffn_rows_of_any_assignments():
     assert (out == 7).all()
 
 
+# tiles of 256, 256, 192, 128 rows, more than one round of them and a part of one (in whole
+# tiles or in pieces of 64 rows, some without rows), for gate/up (wide F) or down (wide H)
+@pytest.mark.parametrize("sizes", [[700, 257, 64, 1000, 579], [1, 2598, 1, 0], [6, 300, 64, 65, 128, 193, 0, 192, 1, 250] * 2,
+                                   [7, 64, 65, 130, 0, 1, 127, 128, 129, 10] * 3], ids=["tall", "lone", "mid", "short"])
+@pytest.mark.parametrize("H,F", [(96, 2944), (5888, 64), (96, 1504), (3040, 128)])
+def test_ffn_of_all_experts_is_that_of_each(sizes, H, F):
+    """A row's sums run over K in one order, whatever tile or piece it lies in."""
+    say(f"[mx4] ffn of {len(sizes)} experts, together and one by one, H={H} F={F}")
+    E, M = len(sizes), sum(sizes)
+    d = _experts(E, H, F, M + H)
+    g = torch.Generator(device="cuda").manual_seed(F)
+    x = torch.randn(M, H, generator=g, device="cuda").bfloat16()
+    off = torch.tensor([0] + sizes, device="cuda").cumsum(0).int()
+    names = ("W1", "W3", "W2", "S1", "S3", "S2")
+    run = lambda: moe.grouped_ffn(x, off, *(d[n] for n in names), path="tiled_a4")  # noqa: E731
+    y = run()
+    at = 0
+    for e, n in enumerate(sizes):
+        if n:
+            one = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+            ye = moe.grouped_ffn(x[at:at + n], one, *(d[m][e:e + 1] for m in names), path="tiled_a4")
+            assert torch.equal(y[at:at + n], ye), e
+        at += n
+    h = _lib.load(_lib.DEBUG_LIB_PATH)
+    h.moe_debug_bounds()
+    with _lib.use_library(h):
+        assert torch.equal(run(), y) and h.moe_debug_bounds() == 0
+
+
 def test_ffn_nan_and_infinity_stay_in_their_rows():
     say("[mx4] ffn with NaN, infinity and the NaN scale")
     d = _case(150, 256, 160, 3, 1, 11)
