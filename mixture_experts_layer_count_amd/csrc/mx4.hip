@@ -377,8 +377,9 @@ hipError_t launch_mx4_panels(const Mx4Panels &p, const TilesJob *tiles, hipStrea
     const dim3 block(1024);
     // 65536 rows of 8192 tokens, C 2048: 53 us by row (268 MB of tokens read from beyond
     // the L2s, at 5 TB/s), 37 + 6 for row_of by token. 8192 rows of 4096 tokens, C 4096: 21
-    // by row, 20 + 5 by token. The launch for row_of takes 5 us or more
-    if (p.row_src && p.gk >= 4 && (p.row_of ? !few : p.scratch && work >= 8192)) {
+    // by row, 20 + 5 by token. The launch for row_of takes 5 us or more. (More than a layer's
+    // 64 picks a token: by row, whose time does not grow with them)
+    if (p.row_src && p.gk >= 4 && p.gk <= 64 && (p.row_of ? !few : p.scratch && work >= 8192)) {
         Mx4Panels q = p;
         if (!q.row_of) {
             const long long n = (rows + 1023) / 1024;

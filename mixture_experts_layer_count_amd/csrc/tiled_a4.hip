@@ -145,16 +145,18 @@ __device__ __forceinline__ void run_items(const GemmProblem &p, int nN, int n_ti
     int count = alone ? share.n : slot < share.n ? scalar((share.n - slot + slots - 1) / slots) : 0;
     if (MOE_BOUNDS_FAIL(count <= kA4Items, BOUNDS_TILE)) return;
     {
-        int g, r0 = 0, r1 = 0, nt;
+        int g = 0, r0 = 0, r1 = 0, nt = 0;
         if (lane < count) {
             item_rows(p, nN, n_tiles, slots, share.first + (alone ? 0 : slot + slots * lane), g, r0, r1, nt);
             if (alone) {
                 r0 += R::BM * share.piece;
                 r1 = min(r1, r0 + R::BM);
             }
-            if (w == 0) *reinterpret_cast<i32x4 *>(table + 4 * lane) = i32x4{g, r0, r1, nt * W};
         }
-        count = scalar(__popcll(__ballot(r0 < r1)));  // 0: a piece without rows
+        const unsigned long long some = __ballot(r0 < r1);  // a piece without rows is dropped
+        if (w == 0 && r0 < r1)
+            *reinterpret_cast<i32x4 *>(table + 4 * __popcll(some & ((1ULL << lane) - 1))) = i32x4{g, r0, r1, nt * W};
+        count = scalar(__popcll(some));
     }
     __syncthreads();
     if (count == 0) return;

@@ -294,6 +294,19 @@ def test_ffn_rows_of_any_assignments():
     assert (out == 7).all()
 
 
+@pytest.mark.parametrize("k", [5, 64, 65, 60000, 2**31 - 1])
+def test_ffn_rows_of_any_picks_a_token(k):
+    say(f"[mx4] ffn of many rows, {k} picks a token")
+    M, H = 60000, 1056
+    d = _experts(3, H, 32, 7)
+    g = torch.Generator(device="cuda").manual_seed(k % 1000)
+    src = torch.randint(0, min(2**31 - 1, 20 * k), (M,), generator=g, device="cuda", dtype=torch.int64)
+    x = torch.randn(int(src.max()) // k + 1, H, generator=g, device="cuda").bfloat16()
+    d |= {"X": x, "offsets": torch.tensor([0, 20000, 20001, M], dtype=torch.int32, device="cuda"), "k": k}
+    y = _ffn(d | {"row_src": src.int()})
+    assert torch.equal(y, _ffn(d | {"X": x[src // k].contiguous(), "k": 1, "row_src": None}))
+
+
 # tiles of 256, 256, 192, 128 rows, more than one round of them and a part of one (in whole
 # tiles or in pieces of 64 rows, some without rows), for gate/up (wide F) or down (wide H)
 @pytest.mark.parametrize("sizes", [[700, 257, 64, 1000, 579], [1, 2598, 1, 0], [6, 300, 64, 65, 128, 193, 0, 192, 1, 250] * 2,
