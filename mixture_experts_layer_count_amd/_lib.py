@@ -252,13 +252,20 @@ def grouped_ffn(Xin, offsets, W1, W3, W2, S1=None, S3=None, S2=None, row_src=Non
     if path == "tiled_a4" and wdt == MOE_MXFP4:
         if S1 is None or S3 is None or S2 is None:
             raise ValueError("MXFP4 weights need S1, S3 and S2")
-        for t, n, shape in ((W3, "W3", W1.shape), (W2, "W2", (G, F // 2, H)), (S1, "S1", (G, H // 32, F)),
-                            (S3, "S3", (G, H // 32, F)), (S2, "S2", (G, F // 32, H))):
-            _want(t, n, shape, torch.uint8, Xin.device)
-        _want(offsets, "offsets", (G + 1,), torch.int32, Xin.device)
+        sk, sf, u8 = (G, H // 32, F), (G, F // 32, H), torch.uint8
+        if not (W3.shape == W1.shape and W2.shape == (G, F // 2, H) and S1.shape == sk and S3.shape == sk
+                and S2.shape == sf and offsets.shape == (G + 1,)
+                and W3.dtype is u8 and W2.dtype is u8 and S3.dtype is u8 and S2.dtype is u8
+                and Xin.device == W1.device == W3.device == W2.device == S1.device == S3.device == S2.device
+                == offsets.device):
+            for t, n, shape in ((W3, "W3", W1.shape), (W2, "W2", (G, F // 2, H)), (S1, "S1", sk), (S3, "S3", sk),
+                                (S2, "S2", sf)):
+                _want(t, n, shape, u8, Xin.device)
+            _want(W1, "W1", W1.shape, u8, Xin.device)
+            _want(offsets, "offsets", (G + 1,), torch.int32, Xin.device)
         if Xin.dim() != 2 or Xin.shape[1] != H or (Xin.shape[0] if row_src is None else row_src.numel()) < M:
             raise ValueError("Xin must be [T, H], and row_src (without one, Xin) must have M rows")
-    nbytes = lib().moe_grouped_ffn_workspace_bytes(M, G, H, F, adt, wdt, p)
+    nbytes = _ws_bytes("moe_grouped_ffn", M, G, H, F, adt, wdt, p)
     ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=Xin.device)
     _call("moe_grouped_ffn", Xin.device, _ptr(Xin), _ptr(row_src), k, M, _ptr(offsets), G, H, F, _ptr(W1), _ptr(W3),
           _ptr(W2), wdt, _ptr(S1), _ptr(S3), _ptr(S2), adt, _ptr(Yp), p, _ptr(ws), nbytes)
