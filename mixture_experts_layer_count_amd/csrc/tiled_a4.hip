@@ -38,7 +38,7 @@
 // rows each: gate/up 499 MB in 108 us, down 250 MB in 56; 120 rows: 135 and 83; 128 on
 // average, 6 to 592, 2.5 rounds of tiles: 166 and 90). Many: the matrix
 // cores, at the clock that the card holds under them. 8 experts, 8192 rows, H 4096,
-// F 14336: gate/up 525 us, 3.7 PFLOP/s, down 272 us, 3.5; tiles are 12 % larger than
+// F 14336: gate/up 520 to 570 us, 3.7 to 3.4 PFLOP/s, down 270 to 295; tiles are 12 % larger than
 // the rows, and the matrix cores are busy for 60 % of the cycles at 1.5 to 1.8 GHz. A
 // loop of the same products, LDS reads and a barrier a step reaches 4.8 PFLOP/s cold
 // and 6.0 in the long run, at 1.3 to 1.7 GHz, against 8.7 at 2.4 GHz with zeros. Fewer
