@@ -561,7 +561,7 @@ moe_status moe_forward_noalloc(const moe_layer_desc *desc, const void *X, int T,
 #define MOE_BOUNDS_TAIL_SLOT 8u     /* tail-split partial slot or counter */
 #define MOE_BOUNDS_PERM_ROW 16u     /* permuted row of an assignment */
 #define MOE_BOUNDS_COMBINE_ROW 32u  /* Yp row read by combine */
-#define MOE_BOUNDS_QUANT_ROW 64u    /* scale row written by the quantiser */
+#define MOE_BOUNDS_QUANT_ROW 64u    /* row (W8A8: of scales) written by a row quantiser */
 #define MOE_BOUNDS_EP_ROW 128u      /* row of an expert-parallel exchange */
 unsigned moe_debug_bounds(void);
 

@@ -339,7 +339,7 @@ unsigned moe_debug_bounds(void) {
     if (hipDeviceSynchronize() != hipSuccess) return ~0u;
     return bounds_take_tiled128() | bounds_take_tiled256() | bounds_take_tiledf32() | bounds_take_a8() |
            bounds_take_stream() | bounds_take_permute() | bounds_take_combine() | bounds_take_quant() |
-           bounds_take_ep() | bounds_take_persist() | bounds_take_a4() |
+           bounds_take_ep() | bounds_take_persist() | bounds_take_a4() | bounds_take_mx4() |
            bounds_take_train_rows() | bounds_take_train_weights();
 #else
     return 0u;
@@ -544,7 +544,8 @@ moe_status moe_grouped_ffn(const void *Xin, const int32_t *row_src, int k, int M
     if (p.a4) {
         // MXFP4 rows (gathered here) and the tile list, gate/up writing MXFP4 h, down
         const TilesJob tiles{offsets, G, p.bm, w.tiles, w.n_tiles, w.group_tile_start, nullptr, 0};
-        MOE_TRY(launch_mx4_panels({Xin, row_src, k, H, M, 0, offsets + G, w.x4, w.x4s, w.ld4, nullptr, w.row_of4},
+        MOE_TRY(launch_mx4_panels({Xin, row_src, k, H, M, 0, offsets + G, w.x4, w.x4s, w.ld4, nullptr, w.row_of4,
+                                   row_src ? 0 : M},
                                   &tiles, stream));
         GemmProblem g1 = gate_up_problem(nullptr, nullptr, 1, &w, G, max_tiles, M, H, F, W1, W3, S1, S3, none, M,
                                          nullptr);
@@ -798,7 +799,7 @@ moe_status moe_forward(const moe_layer_desc *d, const void *X, int T, void *Y, v
     }
     if (p.a4)
         MOE_TRY(launch_mx4_panels({X, f.row_src, d->k, H, A, ex.rows, f.offsets + E, f.ffn.x4, f.ffn.x4s, f.ffn.ld4,
-                                   f.assign_row, nullptr},
+                                   f.assign_row, nullptr, T},
                                   nullptr, stream));
     MOE_TRY(mark(MOE_EV_SCHEDULE));
     GemmProblem g1 = gate_up_problem(X, f.row_src, d->k, &f.ffn, E, max_tiles, M, H, F, W1, W3, S1, S3, ex, A,

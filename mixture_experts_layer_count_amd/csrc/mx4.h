@@ -109,6 +109,7 @@ struct Mx4Panels {
     long long ld;
     const int32_t *row_of;
     int32_t *scratch;
+    int a_rows;  // rows of X (the bounds-checked build's checks only; 0: not known)
 };
 struct TilesJob;
 hipError_t launch_mx4_panels(const Mx4Panels &p, const TilesJob *tiles, hipStream_t s);
@@ -120,5 +121,6 @@ hipError_t launch_mx4_panels(const Mx4Panels &p, const TilesJob *tiles, hipStrea
 hipError_t launch_tiled_a4(const GemmProblem &p, bool swiglu, int bm, hipStream_t s);
 int tiled_a4_bm(long long rows, int groups);
 unsigned bounds_take_a4();  // bounds-checked build
+unsigned bounds_take_mx4();
 
 }  // namespace moe

@@ -12,6 +12,8 @@
 
 namespace moe {
 
+MOE_BOUNDS_FILE(mx4)
+
 namespace {
 
 using namespace mx4;
@@ -267,12 +269,19 @@ __global__ __launch_bounds__(1024) void mx4_row_of_kernel(Mx4Panels p, TilesJob 
     }
 }
 
+// the row of X that holds assignment a's token
+__device__ __forceinline__ int source(int a, const Divide &token) {
+    if (MOE_BOUNDS_FAIL(a >= 0, BOUNDS_A_ROW)) a = 0;
+    return token(a);
+}
 __device__ __forceinline__ u32x4 load_panel(const Mx4Panels &p, long long row, int c) {
+    if (MOE_BOUNDS_FAIL(row >= 0 && (p.a_rows <= 0 || row < p.a_rows), BOUNDS_A_ROW)) row = 0;
     const u32x4 x = *reinterpret_cast<const u32x4 *>(reinterpret_cast<const uint16_t *>(p.X) + row * p.C +
                                                      (c < p.C ? c : 0));
     return c < p.C ? x : u32x4{0, 0, 0, 0};
 }
 __device__ __forceinline__ void store_panel(const Mx4Panels &p, int kb, int row, int sub, uint32_t codes, uint32_t b) {
+    if (MOE_BOUNDS_FAIL(row >= 0 && row < p.ld, BOUNDS_QUANT_ROW)) return;
     const long long o = kb * p.ld + row;
     *reinterpret_cast<uint32_t *>(p.A + o * 64 + 4 * sub) = codes;
     if ((sub & 3) == 0) reinterpret_cast<uint8_t *>(p.As + o)[sub >> 2] = (uint8_t)b;
@@ -296,7 +305,7 @@ __global__ __launch_bounds__(1024) void mx4_panels_kernel(Mx4Panels p, TilesJob 
     for (int i = 0; i < RPT; ++i) {
         const int r = r0 + 64 * i;
         in[i] = r < used || (r >= p.rows && r < p.rows + p.extra);
-        src[i] = !in[i] ? 0 : r >= p.rows ? r - p.rows : p.row_src ? token(p.row_src[r]) : r;
+        src[i] = !in[i] ? 0 : r >= p.rows ? r - p.rows : p.row_src ? source(p.row_src[r], token) : r;
     }
     u32x4 x[RPT];
 #pragma unroll
@@ -350,7 +359,7 @@ __global__ __launch_bounds__(1024) void mx4_panels_token_kernel(Mx4Panels p, int
         const bool own = r < used && ((uint32_t)a >= (uint32_t)p.rows || p.row_of[a] != r);
         uint32_t left = (uint32_t)(__ballot(own) >> (threadIdx.x & 48)) & 0xffffu;
         while (__any(left != 0)) {
-            const int i = left ? __ffs((int)left) - 1 : 0, t = token(__shfl(a, i, 16));
+            const int i = left ? __ffs((int)left) - 1 : 0, t = source(__shfl(a, i, 16), token);
             const u32x4 x = left ? load_panel(p, t, c) : u32x4{0, 0, 0, 0};
             const uint32_t b = scale_byte(quad_max(max_bits(x)));
             if (left) store_panel(p, kb, r - sub + i, sub, codes8(x, b), b);
