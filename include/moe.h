@@ -106,8 +106,9 @@ typedef enum {
  *    4-bit matrix cores (W4A4), for any number of rows (up to 2^30); h is
  *    quantised inside the gate/up GEMM, from its fp32 values. AUTO never picks
  *    it: it rounds activations to 4 bits. A row with a NaN or infinity gives
- *    NaN outputs. Rows, outputs and codes 16-byte aligned, scales 4-byte. In
- *    moe_forward an MXFP4 shared expert needs Fs == F (a bf16 one does not). */
+ *    NaN outputs. Rows, outputs, codes and the workspace 16-byte aligned, scales
+ *    4-byte. In moe_forward an MXFP4 shared expert needs Fs == F (a bf16 one does
+ *    not). */
 typedef enum {
     MOE_PATH_AUTO = 0,
     MOE_PATH_GEMV = 1,

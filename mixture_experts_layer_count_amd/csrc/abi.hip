@@ -531,7 +531,8 @@ moe_status moe_grouped_ffn(const void *Xin, const int32_t *row_src, int k, int M
     const FfnPlan p = plan_ffn(M, G, H, F, w_dt, path);
     if (p.a4 && !a4_aligned({Xin, W1, W3, W2, Yp}, {S1, S3, S2})) return MOE_ERR_UNSUPPORTED;
     if ((path == MOE_PATH_TILED || path == MOE_PATH_TILED_A8) && !p.tiled) return MOE_ERR_UNSUPPORTED;
-    if (!ws || ws_bytes < moe_grouped_ffn_workspace_bytes(M, G, H, F, act_dt, w_dt, path))
+    if (!ws || ws_bytes < moe_grouped_ffn_workspace_bytes(M, G, H, F, act_dt, w_dt, path) ||
+        (p.a4 && !a4_aligned({ws}, {})))
         return MOE_ERR_WORKSPACE_TOO_SMALL;
     Carver c(ws);
     FfnWs w{};
@@ -730,7 +731,7 @@ moe_status moe_forward(const moe_layer_desc *d, const void *X, int T, void *Y, v
     if (f.plan.a4 && !a4_aligned({X, d->W1, d->W3, d->W2, d->Ws1, d->Ws3, d->Ws2},
                                  {d->S1, d->S3, d->S2, d->Ss1, d->Ss3, d->Ss2}))
         return MOE_ERR_UNSUPPORTED;
-    if (!ws || ws_bytes < f.bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (!ws || ws_bytes < f.bytes || (f.plan.a4 && !a4_aligned({ws}, {}))) return MOE_ERR_WORKSPACE_TOO_SMALL;
     if (logits_out) f.logits = logits_out;
     if (topk_idx_out) f.idx = topk_idx_out;
     if (topk_w_out) f.w = topk_w_out;
