@@ -103,9 +103,11 @@ typedef enum {
  *    In moe_forward it needs Fs == 0 or Fs == F.
  *  TILED_A4 (MXFP4 weights only): the expert inputs (token rows, then h) are
  *    quantised to MXFP4 as moe_quantize_mxfp4_rows does and multiplied on the
- *    4-bit matrix cores (W4A4), for any number of rows (up to 2^30); h is
- *    quantised inside the gate/up GEMM, from its fp32 values. AUTO never picks
- *    it: it rounds activations to 4 bits. A row with a NaN or infinity gives
+ *    4-bit matrix cores (W4A4), for any number of rows, from one up to what a
+ *    launch takes (ceil(M / 256) * ceil(H / 128) below 2^22 - 1, and about 2^29
+ *    tiles of 64 rows or more x 128 columns of F, 256 of H); h is quantised
+ *    inside the gate/up GEMM, from its fp32 values. AUTO never picks it: it
+ *    rounds activations to 4 bits. A row with a NaN or infinity gives
  *    NaN outputs. Rows, outputs, codes and the workspace 16-byte aligned, scales
  *    4-byte. In moe_forward an MXFP4 shared expert needs Fs == F (a bf16 one does
  *    not). */

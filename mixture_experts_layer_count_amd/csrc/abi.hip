@@ -317,6 +317,11 @@ bool a4_aligned(std::initializer_list<const void *> wide, std::initializer_list<
         if (reinterpret_cast<uintptr_t>(p) & 3) return false;
     return true;
 }
+// sizes that its launches take
+bool a4_fits(const FfnPlan &p, int rows, int groups, int H, int F) {
+    const long long tiles = max_tiles_for(rows, groups, p.bm);
+    return rows <= kMaxA4Rows && mx4_panels_fit(rows, H) && tiled_a4_fits(tiles, F, true) && tiled_a4_fits(tiles, H, false);
+}
 // its operands: the rows' panels and scale words
 void set_a4(GemmProblem &g, const uint8_t *q, const uint32_t *sc, long long ld) {
     g.A = q;
@@ -500,6 +505,7 @@ size_t moe_grouped_ffn_workspace_bytes(int M, int G, int H, int F, moe_dtype act
                                        moe_dtype w_dt, moe_ffn_path path) {
     if (M < 0 || G < 1 || H < 1 || F < 1 || H > kMaxDim || F > kMaxDim) return 0;
     const FfnPlan p = plan_ffn(M, G, H, F, w_dt, path);
+    if (p.a4 && !a4_fits(p, M, G, H, F)) return 0;
     Carver c(nullptr);
     FfnWs w{};
     size_t bytes = ffn_ws_carve(c, w, p, M, G, H, F, act_dt, M, M, false);
@@ -522,14 +528,15 @@ moe_status moe_grouped_ffn(const void *Xin, const int32_t *row_src, int k, int M
     if (st != MOE_OK) return st;
     if (!path_ok(path)) return MOE_ERR_INVALID_ARG;
     if (path == MOE_PATH_TILED_A8 && w_dt != MOE_FP8_E4M3) return MOE_ERR_UNSUPPORTED;
-    if (path == MOE_PATH_TILED_A4 && (w_dt != MOE_MXFP4 || M > kMaxA4Rows)) return MOE_ERR_UNSUPPORTED;
+    if (path == MOE_PATH_TILED_A4 && w_dt != MOE_MXFP4) return MOE_ERR_UNSUPPORTED;
     if (M == 0) return MOE_OK;
     if (!Xin || !offsets || !W1 || !W3 || !W2 || !Yp) return MOE_ERR_INVALID_ARG;
     const bool sc = scaled(w_dt);
     if (sc != (S1 != nullptr) || sc != (S3 != nullptr) || sc != (S2 != nullptr))
         return MOE_ERR_INVALID_ARG;
     const FfnPlan p = plan_ffn(M, G, H, F, w_dt, path);
-    if (p.a4 && !a4_aligned({Xin, W1, W3, W2, Yp}, {S1, S3, S2})) return MOE_ERR_UNSUPPORTED;
+    if (p.a4 && (!a4_fits(p, M, G, H, F) || !a4_aligned({Xin, W1, W3, W2, Yp}, {S1, S3, S2})))
+        return MOE_ERR_UNSUPPORTED;
     if ((path == MOE_PATH_TILED || path == MOE_PATH_TILED_A8) && !p.tiled) return MOE_ERR_UNSUPPORTED;
     if (!ws || ws_bytes < moe_grouped_ffn_workspace_bytes(M, G, H, F, act_dt, w_dt, path) ||
         (p.a4 && !a4_aligned({ws}, {})))
@@ -658,6 +665,7 @@ struct ForwardWs {
     void *perm_ws, *route_ws;
     FfnWs ffn;
     FfnPlan plan, plan_s;
+    bool fits;       // in the launches that the plan takes
     float *part1_s;  // split-K partials of a separate shared-expert gate/up, or null
     bool combined;   // shared expert runs as an extra group of the routed launches
     size_t bytes;
@@ -698,7 +706,9 @@ ForwardWs carve_forward(const moe_layer_desc *d, int T, void *base) {
     FfnPlan carve = f.plan;
     const bool separate = d->Fs > 0 && !f.combined;
     if (separate && !f.plan.tiled && f.plan_s.ksplit2 > carve.ksplit2) carve.ksplit2 = f.plan_s.ksplit2;
-    ffn_ws_carve(c, f.ffn, carve, rows, groups, d->H, hw, d->act_dt, T, A + (f.combined ? T : 0), true);
+    const int a4_rows = A + (f.combined ? T : 0);
+    f.fits = !f.plan.a4 || a4_fits(f.plan, a4_rows, groups, d->H, d->F);
+    ffn_ws_carve(c, f.ffn, carve, rows, groups, d->H, hw, d->act_dt, T, a4_rows, true);
     f.part1_s = nullptr;
     if (separate && !f.plan_s.tiled && f.plan_s.ksplit1 > 1)
         f.part1_s = static_cast<float *>(c.take(sizeof(float) * (size_t)f.plan_s.ksplit1 * T * 2 * d->Fs));
@@ -711,7 +721,8 @@ ForwardWs carve_forward(const moe_layer_desc *d, int T, void *base) {
 size_t moe_forward_workspace_bytes(const moe_layer_desc *desc, int T) {
     // moe_forward takes at most 65535 tokens
     if (check_desc(desc) != MOE_OK || T < 0 || T > 65535) return 0;
-    return carve_forward(desc, T, nullptr).bytes;
+    const ForwardWs f = carve_forward(desc, T, nullptr);
+    return f.fits ? f.bytes : 0;
 }
 
 moe_status moe_forward(const moe_layer_desc *d, const void *X, int T, void *Y, void *ws,
@@ -728,6 +739,7 @@ moe_status moe_forward(const moe_layer_desc *d, const void *X, int T, void *Y, v
     if (T == 0) return MOE_OK;
     if (!X || !Y) return MOE_ERR_INVALID_ARG;
     ForwardWs f = carve_forward(d, T, ws);
+    if (!f.fits) return MOE_ERR_UNSUPPORTED;
     if (f.plan.a4 && !a4_aligned({X, d->W1, d->W3, d->W2, d->Ws1, d->Ws3, d->Ws2},
                                  {d->S1, d->S3, d->S2, d->Ss1, d->Ss3, d->Ss2}))
         return MOE_ERR_UNSUPPORTED;

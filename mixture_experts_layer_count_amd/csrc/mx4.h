@@ -113,6 +113,7 @@ struct Mx4Panels {
 };
 struct TilesJob;
 hipError_t launch_mx4_panels(const Mx4Panels &p, const TilesJob *tiles, hipStream_t s);
+bool mx4_panels_fit(long long rows, int C);  // in one launch, rows and extra together
 
 // The grouped product of MXFP4 weights and MXFP4 rows (tiled_a4.hip): A holds the rows'
 // panels and As their scale words, as_ld = cqs_ld their rows a panel (at least M + 256:
@@ -120,6 +121,7 @@ hipError_t launch_mx4_panels(const Mx4Panels &p, const TilesJob *tiles, hipStrea
 // Tiles of bm = tiled_a4_bm(rows, groups) rows.
 hipError_t launch_tiled_a4(const GemmProblem &p, bool swiglu, int bm, hipStream_t s);
 int tiled_a4_bm(long long rows, int groups);
+bool tiled_a4_fits(long long max_tiles, int N, bool swiglu);  // in one launch
 unsigned bounds_take_a4();  // bounds-checked build
 unsigned bounds_take_mx4();
 

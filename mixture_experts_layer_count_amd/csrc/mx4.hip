@@ -370,12 +370,18 @@ __global__ __launch_bounds__(1024) void mx4_panels_token_kernel(Mx4Panels p, int
 
 }  // namespace
 
+// workgroups of 1024 threads for 256 rows and a panel, and one for the tile list
+bool mx4_panels_fit(long long rows, int C) {
+    return (rows + 255) / 256 * mx4::panels(C) + 1 <= kMaxThreads / 1024;
+}
+
 hipError_t launch_mx4_panels(const Mx4Panels &p, const TilesJob *tiles, hipStream_t s) {
     if (p.rows < 0 || p.extra < 0 || p.C < kGroup || p.C % kGroup || p.gk < 1 || !p.A || !p.As ||
         p.ld < (long long)p.rows + p.extra)
         return hipErrorInvalidValue;
     const long long rows = (long long)p.rows + p.extra;
     if (rows == 0 && !tiles) return hipSuccess;
+    if (!mx4_panels_fit(rows, p.C)) return hipErrorInvalidValue;
     const int np = panels(p.C);
     // few blocks of 64 rows and a panel: a row a thread, for more workgroups (H 2048, 256
     // blocks: 3.4 against 5.1 us with four, 1024: 7.6 and 8.1, 4096: 17.5 and 16.5)
@@ -400,14 +406,12 @@ hipError_t launch_mx4_panels(const Mx4Panels &p, const TilesJob *tiles, hipStrea
         long long tokens = (p.rows + (long long)p.gk - 1) / p.gk;
         if (tokens < p.extra) tokens = p.extra;
         const long long chunks = (tokens + 255) / 256;
-        if (chunks * np > kMaxThreads / 1024) return hipErrorInvalidValue;
         hipLaunchKernelGGL(mx4_panels_token_kernel<4>, dim3((unsigned)(chunks * np)), block, 0, s, q, (int)chunks,
                            (int)tokens, token);
         return hipGetLastError();
     }
     const long long chunks = (rows + (few ? 64 : 256) - 1) / (few ? 64 : 256);
     const long long blocks = chunks * np + (tiles ? 1 : 0);
-    if (blocks > kMaxThreads / 1024) return hipErrorInvalidValue;
     if (few)
         hipLaunchKernelGGL(mx4_panels_kernel<1>, dim3((unsigned)blocks), block, 0, s, p, job, (int)chunks, token);
     else

@@ -600,14 +600,19 @@ __global__ __launch_bounds__(64 * NW, 1) void tiled_a4_kernel(GemmProblem p, int
     run_items<SWIGLU, 1>(p, nN, n_tiles, cut, lds);
 }
 
+int column_tiles(int N, bool swiglu) { return (N + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256); }
+// Workgroups of an XCD: one round of resident ones, or as many as keep to the item table
+long long slots_for(long long max_tiles, int nN) {
+    const long long items = (max_tiles * nN + kXcds - 1) / kXcds;  // at most
+    const long long rounds = (items + (long long)kA4Items * kBlocksPerXcd - 1) / (kA4Items * kBlocksPerXcd);
+    return kBlocksPerXcd * (rounds > 1 ? rounds : 1);
+}
+
 template <bool SWIGLU, int MI>
 hipError_t launch(const GemmProblem &p, hipStream_t s) {
-    const int nN = (p.N + (SWIGLU ? 127 : 255)) / (SWIGLU ? 128 : 256);
-    const long long items = ((long long)p.max_tiles * nN + kXcds - 1) / kXcds;  // of an XCD, at most
-    if (items > 0x0fffffffLL) return hipErrorInvalidValue;
-    // one round of resident workgroups, or as many as keep to the item table
-    long long slots = kBlocksPerXcd;
-    while ((items + slots - 1) / slots > kA4Items) slots += kBlocksPerXcd;
+    const int nN = column_tiles(p.N, SWIGLU);
+    if (!tiled_a4_fits(p.max_tiles, p.N, SWIGLU)) return hipErrorInvalidValue;
+    const long long slots = slots_for(p.max_tiles, nN);
     hipLaunchKernelGGL((tiled_a4_kernel<SWIGLU, MI>), dim3((unsigned)(slots * kXcds)), dim3(64 * NW), 0, s, p, nN);
     return hipGetLastError();
 }
@@ -625,6 +630,12 @@ hipError_t launch(const GemmProblem &p, hipStream_t s) {
 int tiled_a4_bm(long long rows, int groups) {
     const long long avg = rows / groups;
     return avg > 160 ? 256 : avg > 96 ? 192 : avg > 40 ? 128 : 64;
+}
+
+// fewer than 2^32 threads, and (then) tiles counted in ints
+bool tiled_a4_fits(long long max_tiles, int N, bool swiglu) {
+    using namespace tiled;
+    return slots_for(max_tiles, column_tiles(N, swiglu)) * kXcds * (64 * NW) <= 0xffffffffLL;
 }
 
 hipError_t launch_tiled_a4(const GemmProblem &p, bool swiglu, int bm, hipStream_t s) {

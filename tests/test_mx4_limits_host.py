@@ -18,3 +18,25 @@ def test_workspace_alignment():
         ws = ctypes.c_void_p(at)
         assert _ffn(moe.lib(), ws=ws, ws_bytes=1 << 60, path=A4, **MX) == WS_SMALL
         assert _forward(ws) == WS_SMALL
+
+
+def test_sizes_past_a_launch():
+    """64 rows of a panel take 256 to 1024 threads, a workgroup of 512 up to 64 tiles: sizes
+    that need 2^32 threads are refused, and have no workspace."""
+    lib = moe.lib()
+    size = lambda M, G, H, F: lib.moe_grouped_ffn_workspace_bytes(M, G, H, F, 1, 3, A4)  # noqa: E731
+    at_most = 4194302                                   # blocks of 256 rows and a panel, beside the tile list's
+    for M, G, H, F in ((1 << 30, 1, 32, 32), (256 * at_most + 1, 8, 128, 64), (128 * at_most + 1, 8, 160, 64),
+                       (1 << 20, 4, 1 << 20, 32),       # rows
+                       (64, 1 << 30, 32, 32), (64, 1 << 21, 32, 1 << 20), (64, 1 << 21, 1 << 20, 32)):  # tiles
+        assert size(M, G, H, F) == 0, (M, G, H, F)
+        assert _ffn(lib, M=M, G=G, H=H, F=F, ws_bytes=(1 << 63), path=A4, **MX) == 2, (M, G, H, F)
+    # up to there the size is what counts
+    for M, G, H, F in ((256 * at_most, 8, 128, 64), (128 * at_most - 256, 8, 160, 64), (64, 1 << 25, 32, 32)):
+        assert 0 < size(M, G, H, F) < 1 << 62
+        assert _ffn(lib, M=M, G=G, H=H, F=F, ws_bytes=64, path=A4, **MX) == WS_SMALL, (M, G, H, F)
+    # the layer: 65535 tokens of the widest rows
+    big = dict(H=1 << 20, E=64, k=64)
+    d = _desc(F=1024, w_dt=3, S1=0x1000, S3=0x1000, S2=0x1000, path=A4, **big)
+    assert lib.moe_forward_workspace_bytes(ctypes.byref(d), 65535) == 0 < lib.moe_forward_workspace_bytes(ctypes.byref(d), 500)
+    assert _forward(T=65535, **big) == 2
