@@ -482,6 +482,11 @@ class EPLoopback:
         if self.E % G:
             raise ValueError("E must be divisible by G")
         self.El = self.E // G
+        # a bf16 shared expert runs on the bf16 tiled kernels beside routed experts on a
+        # path of their dtype alone, as in moe_forward
+        Ws1 = weights.get("Ws1")
+        bf16 = Ws1 is not None and weight_dtype(Ws1, weights.get("Ss1")) == MOE_BF16
+        self.shared_path = "tiled" if bf16 and path in ("tiled_a8", "tiled_a4") else path
 
     def _experts(self, d: int):
         sl = slice(d * self.El, (d + 1) * self.El)
@@ -557,7 +562,7 @@ class EPLoopback:
                 off = torch.tensor([0, nt], dtype=torch.int32, device=dev)
                 sw = [None if self.w.get(key) is None else self.w[key].unsqueeze(0)
                       for key in ("Ws1", "Ws3", "Ws2", "Ss1", "Ss3", "Ss2")]
-                S = grouped_ffn(X[sl], off, *sw, path=self.path)
+                S = grouped_ffn(X[sl], off, *sw, path=self.shared_path)
             combine(ret[r, :nt * k], send_slot[r, :nt * k], routes[r][2], S, out=Y[sl])
         mark(7)
         if keep:
