@@ -257,12 +257,15 @@ def grouped_ffn(Xin, offsets, W1, W3, W2, S1=None, S3=None, S2=None, row_src=Non
                 and S2.shape == sf and offsets.shape == (G + 1,)
                 and W3.dtype is u8 and W2.dtype is u8 and S3.dtype is u8 and S2.dtype is u8
                 and Xin.device == W1.device == W3.device == W2.device == S1.device == S3.device == S2.device
-                == offsets.device):
+                == offsets.device == Yp.device and (row_src is None or row_src.device == Xin.device)):
             for t, n, shape in ((W3, "W3", W1.shape), (W2, "W2", (G, F // 2, H)), (S1, "S1", sk), (S3, "S3", sk),
                                 (S2, "S2", sf)):
                 _want(t, n, shape, u8, Xin.device)
             _want(W1, "W1", W1.shape, u8, Xin.device)
             _want(offsets, "offsets", (G + 1,), torch.int32, Xin.device)
+            _want(Yp, "out", (M, H), Xin.dtype, Xin.device)
+            if row_src is not None:
+                _want(row_src, "row_src", row_src.shape, torch.int32, Xin.device)
         if Xin.dim() != 2 or Xin.shape[1] != H or (Xin.shape[0] if row_src is None else row_src.numel()) < M:
             raise ValueError("Xin must be [T, H], and row_src (without one, Xin) must have M rows")
     nbytes = _ws_bytes("moe_grouped_ffn", M, G, H, F, adt, wdt, p)

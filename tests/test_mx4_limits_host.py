@@ -2,6 +2,9 @@
 answered with a status before anything is launched. No GPU is needed."""
 import ctypes
 
+import pytest
+import torch
+
 import mixture_experts_layer_count_amd as moe
 from test_abi_host import _desc, _ffn
 from test_mx4_host import A4, FAKE, MX, WS_SMALL
@@ -40,3 +43,37 @@ def test_sizes_past_a_launch():
     d = _desc(F=1024, w_dt=3, S1=0x1000, S3=0x1000, S2=0x1000, path=A4, **big)
     assert lib.moe_forward_workspace_bytes(ctypes.byref(d), 65535) == 0 < lib.moe_forward_workspace_bytes(ctypes.byref(d), 500)
     assert _forward(T=65535, **big) == 2
+
+
+class _Tensor:
+    """What the binding asks of a device tensor, on a machine without one."""
+    is_cuda = True
+
+    def __init__(self, shape, dtype, device="cuda:0"):
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, torch.device(device)
+
+    def is_contiguous(self):
+        return True
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def data_ptr(self):
+        return 0x1000
+
+
+@pytest.mark.parametrize("name", ["offsets", "W1", "S2", "row_src", "out"])
+def test_operands_on_another_device(name):
+    """A call runs on its rows' device; whatever lies elsewhere is refused by name."""
+    G, H, F, T, k = 4, 64, 96, 5, 2
+    u8, i32, bf = torch.uint8, torch.int32, torch.bfloat16
+    a = {"Xin": ((T, H), bf), "offsets": ((G + 1,), i32), "W1": ((G, H // 2, F), u8), "W3": ((G, H // 2, F), u8),
+         "W2": ((G, F // 2, H), u8), "S1": ((G, H // 32, F), u8), "S3": ((G, H // 32, F), u8),
+         "S2": ((G, F // 32, H), u8), "row_src": ((T * k,), i32), "out": ((T * k, H), bf)}
+    t = {n: _Tensor(*v) for n, v in a.items()}
+    t[name] = _Tensor(*a[name], device="cuda:1")
+    with pytest.raises(ValueError, match=name):
+        moe.grouped_ffn(**t, k=k, path="tiled_a4")
