@@ -59,27 +59,6 @@ __device__ __forceinline__ uint32_t max_bits(const u32x4 &x) {
                                               __builtin_elementwise_max(mags(x[2]), mags(x[3]))));
 }
 
-// 8 consecutive values of X at element offset o (16-byte aligned)
-template <bool F32>
-__device__ __forceinline__ void load8(const void *X, long long o, float (&v)[8]) {
-    if constexpr (F32) {
-        const f32x4 *p = reinterpret_cast<const f32x4 *>(reinterpret_cast<const float *>(X) + o);
-        const f32x4 a = p[0], b = p[1];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = a[i];
-            v[4 + i] = b[i];
-        }
-    } else {
-        const u32x4 a = *reinterpret_cast<const u32x4 *>(reinterpret_cast<const uint16_t *>(X) + o);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = bf16_lo(a[i]);
-            v[2 * i + 1] = bf16_hi(a[i]);
-        }
-    }
-}
-
 // The layout that the 4-bit product reads rows in: for each 128 columns (a
 // panel, the last one filled up with zeros) 64 bytes of codes a row, row after
 // row, and one word of 4 scale bytes a row. A tile's K step is then one

@@ -32,6 +32,16 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
     return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4e, 0xf, 0xf, true));  // lanes 2 3 0 1
 }
 
+// 8 consecutive fp32 values
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+    const f32x4 a = reinterpret_cast<const f32x4 *>(p)[0], b = reinterpret_cast<const f32x4 *>(p)[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = a[i];
+        v[4 + i] = b[i];
+    }
+}
+
 // ---- rows: a thread owns 16 consecutive values; the two threads of a group
 // exchange their maxima, and one of them stores the scale byte ----
 template <bool F32>
@@ -49,8 +59,8 @@ __global__ __launch_bounds__(256) void mx4_rows_kernel(const void *X, long long 
     u32x2 q;
     if constexpr (F32) {
         float v[2][8];
-        load8<true>(X, o, v[0]);
-        load8<true>(X, o + 8, v[1]);
+        load8(static_cast<const float *>(X) + o, v[0]);
+        load8(static_cast<const float *>(X) + o + 8, v[1]);
         m = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) m = max(m, max(mag_bits(v[0][j]), mag_bits(v[1][j])));
