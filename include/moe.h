@@ -91,8 +91,9 @@ typedef enum {
 /* Expert-FFN kernel choice. AUTO picks the row-streaming (batched GEMV) path
  * when the experts average fewer than 15 rows (48 for MXFP4 weights) and the
  * LDS-tiled grouped GEMM otherwise (prefill); for FP8 weights the tiled choice
- * is TILED_A8. All give results within the same tolerance of the exact layer;
- * the forced values exist for testing and comparison.
+ * is TILED_A8. These give results within the same tolerance of the exact layer;
+ * their forced values exist for testing and comparison. TILED_A4 is a choice of
+ * its own, with activations rounded to 4 bits.
  *  GEMV, TILED: activations stay in act_dt; FP8 weights are decoded exactly
  *    and each 128-deep K block is scaled (W8A16).
  *  TILED_A8 (FP8 weights only, H and F multiples of 128): the expert inputs
@@ -107,7 +108,11 @@ typedef enum {
  *    launch takes (ceil(M / 256) * ceil(H / 128) below 2^22 - 1, and about 2^29
  *    tiles of 64 rows or more x 128 columns of F, 256 of H); h is quantised
  *    inside the gate/up GEMM, from its fp32 values. AUTO never picks it: it
- *    rounds activations to 4 bits. A row with a NaN or infinity gives
+ *    rounds activations to 4 bits. Few rows: with wide experts GEMV is the
+ *    faster up to about 8 rows an expert (8 experts of 4096 x 14336, k 2, T 1:
+ *    67 us against 93, T 32: 169 and 185, T 64: 248 and 186), with narrow ones
+ *    TILED_A4 is as fast or faster from one token on (128 experts of 2048 x 768,
+ *    k 8, T 1: 30 and 20, T 64: 80 and 71). A row with a NaN or infinity gives
  *    NaN outputs. Rows, outputs, codes and the workspace 16-byte aligned, scales
  *    4-byte. In moe_forward an MXFP4 shared expert needs Fs == F (a bf16 one does
  *    not). */
@@ -250,8 +255,8 @@ moe_status moe_combine(const void *Yp, const int32_t *assign_row, const float *t
  * Whole layer: route -> permute -> grouped FFN (+ shared expert) -> combine.
  * Weights are borrowed device pointers described by moe_layer_desc. The
  * shared expert (Fs > 0) uses Ws1, Ws3 [H, Fs], Ws2 [Fs, H] in ws_dt (+ Ss*
- * scales when ws_dt is FP8) and is added with weight 1. ws_dt equals w_dt,
- * or is BF16 beside FP8 routed experts: the page "MoE-推理部署"
+ * scales when ws_dt is FP8 or MXFP4) and is added with weight 1. ws_dt equals
+ * w_dt, or is BF16 beside FP8 or MXFP4 routed experts: the page "MoE-推理部署"
  * (expert-quantisation section) notes that the shared expert, like the
  * router, is usually kept at higher precision than the routed experts. A
  * shared expert whose dtype or width differs from the routed experts' runs
@@ -273,7 +278,7 @@ typedef struct moe_layer_desc {
     const float *S1, *S3, *S2;
     const void *Ws1, *Ws3, *Ws2;
     const float *Ss1, *Ss3, *Ss2;
-    moe_dtype ws_dt;         /* shared expert weights: w_dt, or BF16 beside FP8 */
+    moe_dtype ws_dt;         /* shared expert weights: w_dt, or BF16 beside FP8 or MXFP4 */
     int gate_f32;            /* 0: Wg in act_dt; 1: Wg fp32 (higher-precision
                                 router, see moe_route); other values rejected */
 } moe_layer_desc;

@@ -3,9 +3,11 @@
 //
 // HBM-bound: 2 (fp32: 4) bytes a value in, 17/32 out, and the reverse. A value's
 // arithmetic is about one instruction (a conversion takes two values and the packed
-// maximum two), so bf16 stays in pairs as it lies in memory. bf16, at the copy's rate of
-// 4.5 TB/s or above: rows 32768 x 4096 62-78 us and back 56 (339 MB), weights 8 x 4096 x
-// 14336 254 us (4.7 TB/s) and back 193 (6.2, most of it written).
+// maximum two), so bf16 stays in pairs as it lies in memory. About the copy's rate of 4.5 TB/s
+// or above, fastest and median of 20 calls. bf16: rows 32768 x 4096 (339 MB) 64 and 78 us
+// (5.3 and 4.3 TB/s), back 49 and 50; weights 8 x 4096 x 14336 (1.19 GB) 225 and 260 (5.3 and
+// 4.6), back 194 and 195 (6.1). fp32: rows 16384 x 7168 (532 MB) 95 and 103 (5.6 and 5.2),
+// back 89 and 94; the same weights (2.13 GB) 400 and 411 (5.3 and 5.2), back 384 and 391.
 #include "mx4.h"
 #include "schedule.h"
 #include "train.h"
@@ -440,8 +442,8 @@ using namespace moe;
 
 namespace {
 
-// values of one call: a launch of 256 threads per 4096 (rows) or 65536 values,
-// and a grid's dimension holds fewer than 2^32 threads
+// values of one call: a launch of 256 threads per 4096 values of rows (of weights 32768 or
+// 65536, by the columns a thread takes), and a grid's dimension holds fewer than 2^32 threads
 constexpr long long kMaxValues = (1LL << 36) - 4096;
 
 bool off16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }

@@ -36,9 +36,9 @@
 //
 // What bounds it. Few rows an expert: the weights' bytes (32 experts of 7168 x 2048, 8
 // rows each: gate/up 499 MB in 108 us, down 250 MB in 56; 120 rows: 135 and 83; 128 on
-// average, 6 to 592, 2.5 rounds of tiles: 166 and 90). Many: the matrix
+// average, 6 to 592, 2.5 rounds of tiles: 172 to 177 and 89 to 96). Many: the matrix
 // cores, at the clock that the card holds under them. 8 experts, 8192 rows, H 4096,
-// F 14336: gate/up 520 to 570 us, 3.7 to 3.4 PFLOP/s, down 270 to 295; tiles are 12 % larger than
+// F 14336: gate/up 515 to 565 us, 3.7 to 3.4 PFLOP/s, down 265 to 292; tiles are 12 % larger than
 // the rows, and the matrix cores are busy for 60 % of the cycles at 1.5 to 1.8 GHz. A
 // loop of the same products, LDS reads and a barrier a step reaches 4.8 PFLOP/s cold
 // and 6.0 in the long run, at 1.3 to 1.7 GHz, against 8.7 at 2.4 GHz with zeros. Fewer
@@ -566,7 +566,8 @@ __global__ __launch_bounds__(64 * NW, 1) void tiled_a4_kernel(GemmProblem p, int
     // the XCD's workgroups. 8 experts, 8192 rows (4.5 tiles an expert), whole and cut: H 8192,
     // F 2048 330 and 319 us, H 2048, F 8192 288 and 271, H 1024, F 1024 48 and 46; with two
     // rounds of pieces (H 1024, F 4096) 96.5 and 98. 32 experts of 7168 x 2048, 6 to 592 rows:
-    // gate/up 172 us with pieces counted as if tiles were full, 166 with those that have rows.
+    // gate/up 172 us with pieces counted as if tiles were full, 166 with those that have rows
+    // (fastest calls of one run; other runs of the latter begin at 172).
     // (Equal parts over K, their sums joined through memory: as fast at K 14336, and nothing
     // below 12 steps a part.)
     int tail = MI > 1 && slots == kBlocksPerXcd ? scalar(mine % slots) : 0;
